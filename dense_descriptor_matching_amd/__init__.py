@@ -13,6 +13,10 @@ seed grid and keeps the seeds that cycle ("MASt3R" note on cv-learn.com,
 section 手法とアーキテクチャ, FRM paragraph; the fast_reciprocal_NNs routine
 quoted in "DUSt3R和MASt3R论文阅读", section MASt3R matching).
 Pixel indices are linear, p = x + W * y; :func:`to_xy` converts.
+
+:mod:`dense_descriptor_matching_amd.network` has the operators of the network that
+produces the maps and of its training: :func:`attention`, :func:`layer_norm` and
+:func:`matching_loss`.
 """
 from __future__ import annotations
 
@@ -81,6 +85,7 @@ def _declare(lib):
     lib.ddm_frm_stats.argtypes = [P, I, I, I64, I64, P]; lib.ddm_frm_stats.restype = I
     lib.ddm_frm_match_noalloc.argtypes = [P, I, I, P, I, I, I, I, I, I, P, P, P, I, P, P, P, P]
     lib.ddm_frm_match_noalloc.restype = I
+    network.declare(lib)
     return lib
 
 
@@ -505,7 +510,14 @@ def mutual_nn(D1: torch.Tensor, D2: torch.Tensor, return_nn: bool = False, metri
     return res
 
 
-__all__ = ["nn", "frm_match", "frm_match_batched", "frm_match_into", "frm_match_ex", "c2f_match", "mutual_nn",
+# ------------------------------------------------------------------- descriptor network
+from . import network  # noqa: E402  (uses this module's handle and checks)
+from .network import (attention, attention_backward, attention_forward, layer_norm, layer_norm_backward,  # noqa: E402
+                      layer_norm_forward, matching_loss, matching_loss_backward, matching_loss_forward)
+
+__all__ = ["attention", "attention_forward", "attention_backward", "layer_norm", "layer_norm_forward",
+           "layer_norm_backward", "matching_loss", "matching_loss_forward", "matching_loss_backward",
+           "nn", "frm_match", "frm_match_batched", "frm_match_into", "frm_match_ex", "c2f_match", "mutual_nn",
            "mutual_nn_into", "seed_count", "to_xy", "FrmBuffers", "MutualBuffers", "DDMError", "lib", "LIB_PATH",
            "profile_enable", "profile_read", "frm_set_mode", "frm_get_mode", "frm_set_barrier_polls",
            "debug_set_grid_cap", "debug_set_output_bitmap_limit", "frm_set_tail_after",

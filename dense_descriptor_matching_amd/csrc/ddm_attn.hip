@@ -1,0 +1,191 @@
+// ddm_attn.hip -- host side of ddm_attention_*: checks, variants and launches.
+#include "../../include/ddm.h"
+#include "ddm_attn.hpp"
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+using namespace ddm;
+
+namespace {
+
+constexpr int SPLIT_ROWS = 32;            // rows of a workgroup of the split form
+
+struct Plan {
+    int d;                                // padded head dimension: 32, 64 or 128
+    bool split;
+    int chunk, cap;
+    size_t bytes;                         // forward workspace
+};
+
+int esize(int dtype) { return dtype == DDM_F32 ? 4 : 2; }
+
+// Which form the forward pass takes, from the sizes alone (the lengths are on the device).
+Plan make_plan(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int D) {
+    Plan p{};
+    p.d = D <= 32 ? 32 : D <= 64 ? 64 : 128;
+    const long long rows = (long long)Tq * (Hq / Hkv);
+    // Split the keys where whole rows would leave most of the 256 CUs without work: few workgroups of 128 rows, and keys
+    // enough per sequence for two chunks.
+    const long long wgs = (rows / 128 + B) * Hkv;
+    p.split = rows <= 64ll * B && wgs < 1024 && Tk / B >= 128;
+    if (p.split) {
+        // some 2048 workgroups of one wave over all keys, in whole tiles of 64 keys
+        const long long avg = ((long long)Tk * Hkv + 2047) / 2048;
+        p.chunk = (int)std::min<long long>(std::max<long long>((avg + 63) / 64 * 64, 64), 4096);
+        const long long mean = (rows + B - 1) / B;
+        p.cap = (int)std::min<long long>((2 * mean + SPLIT_ROWS - 1) / SPLIT_ROWS * SPLIT_ROWS, 4 * SPLIT_ROWS);
+        if (mean <= SPLIT_ROWS / 2) p.cap = SPLIT_ROWS;
+        p.bytes = (size_t)(slot_count(B, Tk, 1, p.chunk) * Hkv) * p.cap * (D + 4) * sizeof(float);
+    }
+    return p;
+}
+
+// Sizes that every entry point checks alike.
+int check(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int D) {
+    if (dtype != DDM_F32 && dtype != DDM_F16 && dtype != DDM_BF16) return DDM_ERR_UNSUPPORTED;
+    if (B < 1 || Tq < 0 || Tk < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv) return DDM_ERR_INVALID;
+    if (D < 1 || D > DDM_MAX_D || D * esize(dtype) % 16) return DDM_ERR_UNSUPPORTED;
+    const long long G = Hq / Hkv;
+    if (B > (1 << 20) || (long long)Tq * G * G >= (1ll << 31) || Tk >= INT_MAX - (1 << 22)) return DDM_ERR_INVALID;
+    if (((long long)Tq * G / 32 + B + 2) * Hkv >= INT_MAX || ((long long)Tk / 32 + B + 2) * Hkv >= INT_MAX)
+        return DDM_ERR_INVALID;
+    return DDM_OK;
+}
+
+// Rows are whole 16-byte pieces at 16-byte boundaries, and 64 of them lie within 31-bit offsets.
+bool bad_view(const void *p, int64_t ts, int64_t hs, int heads, int dtype) {
+    const int e = esize(dtype);
+    if (!p || (uintptr_t)p % 16 || ts < 0 || hs < 0 || ts * e % 16 || hs * e % 16) return true;
+    return ts * e >= (1ll << 24) || hs * e >= (1ll << 24) || hs * e * heads >= (1ll << 29);
+}
+bool bad_ptr(const void *p) { return !p || (uintptr_t)p % 16; }
+
+template <class T, int D>
+hipError_t forward(const AttnArgs &a, const Plan &pl, hipStream_t s) {
+    const int G = a.group.g;
+    constexpr bool wide = sizeof(T) == 2;
+    if (pl.split) {
+        constexpr int BN = wide ? 64 : 32;
+        const long long slots = slot_count(a.B, a.Tk, 1, pl.chunk);
+        hipLaunchKernelGGL((attn_fwd_kernel<T, D, 1, 1, BN, true>), dim3((unsigned)(slots * a.Hkv), pl.cap / SPLIT_ROWS),
+                           dim3(64), 0, s, a);
+        if (hipError_t e = hipGetLastError()) return e;
+        const long long ids = (long long)a.Tq * a.Hq;
+        hipLaunchKernelGGL((attn_join_kernel<T>), dim3((unsigned)((ids + 3) / 4)), dim3(256), 0, s, a);
+        return hipGetLastError();
+    }
+    constexpr int BN = wide ? 64 : 32, NR = wide && D <= 64 ? 2 : 1;
+    const long long big = slot_count(a.B, a.Tq, G, 128 * NR) * a.Hkv;
+    if (NR == 2 && (long long)a.Tq * G / 256 * a.Hkv >= 512) {
+        hipLaunchKernelGGL((attn_fwd_kernel<T, D, 4, NR, BN, false>), dim3((unsigned)big), dim3(256), 0, s, a);
+    } else {
+        const long long n = slot_count(a.B, a.Tq, G, 128) * a.Hkv;
+        hipLaunchKernelGGL((attn_fwd_kernel<T, D, 4, 1, BN, false>), dim3((unsigned)n), dim3(256), 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+template <class T, int D>
+hipError_t backward(const AttnArgs &a, hipStream_t s) {
+    const int G = a.group.g;
+    constexpr bool wide = sizeof(T) == 2;
+    constexpr int BN = wide ? 64 : 32, NR = 1;
+    if (a.Tq) {
+        const long long n = slot_count(a.B, a.Tq, G, 128 * NR) * a.Hkv;
+        hipLaunchKernelGGL((attn_dq_kernel<T, D, 4, NR, BN>), dim3((unsigned)n), dim3(256), 0, s, a);
+        if (hipError_t e = hipGetLastError()) return e;
+    }
+    if (a.Tk) {
+        const long long n = slot_count(a.B, a.Tk, 1, 128 * NR) * a.Hkv;
+        hipLaunchKernelGGL((attn_dkv_kernel<T, D, 4, NR, BN>), dim3((unsigned)n), dim3(256), 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+template <class F>
+hipError_t with_type(int dtype, int d, F f) {
+    if (dtype == DDM_F16) return d == 32 ? f(_Float16{}, std::integral_constant<int, 32>{})
+                                 : d == 64 ? f(_Float16{}, std::integral_constant<int, 64>{})
+                                           : f(_Float16{}, std::integral_constant<int, 128>{});
+    if (dtype == DDM_BF16) return d == 32 ? f(__bf16{}, std::integral_constant<int, 32>{})
+                                  : d == 64 ? f(__bf16{}, std::integral_constant<int, 64>{})
+                                            : f(__bf16{}, std::integral_constant<int, 128>{});
+    return d == 32 ? f(float{}, std::integral_constant<int, 32>{})
+           : d == 64 ? f(float{}, std::integral_constant<int, 64>{})
+                     : f(float{}, std::integral_constant<int, 128>{});
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ddm_attention_forward_workspace_bytes(int B, int Tq, int Tk, int Hq, int Hkv, int D, int dtype) {
+    if (check(dtype, B, Tq, Tk, Hq, Hkv, D) != DDM_OK) return 0;
+    return std::max<size_t>(make_plan(dtype, B, Tq, Tk, Hq, Hkv, D).bytes, 16);
+}
+
+int ddm_attention_forward(const void *q, int64_t q_ts, int64_t q_hs, const void *k, int64_t k_ts, int64_t k_hs,
+                          const void *v, int64_t v_ts, int64_t v_hs, const int32_t *cu_q, const int32_t *cu_k, int B,
+                          int Tq, int Tk, int Hq, int Hkv, int D, int dtype, int causal, double scale, void *out,
+                          float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (int rc = check(dtype, B, Tq, Tk, Hq, Hkv, D)) return rc;
+    if (!(scale > 0) || !std::isfinite(scale) || (causal != 0 && causal != 1)) return DDM_ERR_INVALID;
+    if ((!cu_q || !cu_k) && B != 1) return DDM_ERR_INVALID;
+    if (Tq == 0) return DDM_OK;
+    if (bad_view(q, q_ts, q_hs, Hq, dtype) || bad_ptr(out) || bad_ptr(lse)) return DDM_ERR_INVALID;
+    if (Tk && (bad_view(k, k_ts, k_hs, Hkv, dtype) || bad_view(v, v_ts, v_hs, Hkv, dtype))) return DDM_ERR_INVALID;
+    const Plan pl = make_plan(dtype, B, Tq, Tk, Hq, Hkv, D);
+    if (pl.bytes && (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < pl.bytes)) return DDM_ERR_WORKSPACE;
+    AttnArgs a{};
+    a.q = q; a.k = k; a.v = v; a.out = out; a.lse = lse;
+    a.cu_q = cu_q; a.cu_k = cu_k;
+    a.B = B; a.Tq = Tq; a.Tk = Tk; a.Hq = Hq; a.Hkv = Hkv; a.D = D;
+    a.group = make_div(Hq / Hkv);
+    a.q_ts = q_ts; a.q_hs = q_hs; a.k_ts = k_ts; a.k_hs = k_hs; a.v_ts = v_ts; a.v_hs = v_hs;
+    a.scale = (float)scale; a.c = (float)(scale * 1.4426950408889634); a.causal = causal;
+    a.chunk = pl.chunk; a.cap = pl.cap; a.part = (float *)workspace;
+    const hipError_t e = with_type(dtype, pl.d, [&](auto t, auto d) {
+        return forward<decltype(t), decltype(d)::value>(a, pl, stream);
+    });
+    return e == hipSuccess ? DDM_OK : DDM_ERR_HIP;
+}
+
+size_t ddm_attention_backward_workspace_bytes(int B, int Tq, int Tk, int Hq, int Hkv, int D, int dtype) {
+    if (check(dtype, B, Tq, Tk, Hq, Hkv, D) != DDM_OK) return 0;
+    return std::max<size_t>((size_t)Tq * Hq * sizeof(float) * (dtype == DDM_F16 ? 2 : 1), 16);
+}
+
+int ddm_attention_backward(const void *dout, int64_t g_ts, int64_t g_hs, const void *q, int64_t q_ts, int64_t q_hs,
+                           const void *k, int64_t k_ts, int64_t k_hs, const void *v, int64_t v_ts, int64_t v_hs,
+                           const void *out, const float *lse, const int32_t *cu_q, const int32_t *cu_k, int B, int Tq,
+                           int Tk, int Hq, int Hkv, int D, int dtype, int causal, double scale, void *dq, void *dk,
+                           void *dv, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (int rc = check(dtype, B, Tq, Tk, Hq, Hkv, D)) return rc;
+    if (!(scale > 0) || !std::isfinite(scale) || (causal != 0 && causal != 1)) return DDM_ERR_INVALID;
+    if ((!cu_q || !cu_k) && B != 1) return DDM_ERR_INVALID;
+    if (Tq && (bad_view(q, q_ts, q_hs, Hq, dtype) || bad_view(dout, g_ts, g_hs, Hq, dtype) || bad_ptr(out) || bad_ptr(lse) ||
+               bad_ptr(dq)))
+        return DDM_ERR_INVALID;
+    if (Tk && (bad_view(k, k_ts, k_hs, Hkv, dtype) || bad_view(v, v_ts, v_hs, Hkv, dtype) || bad_ptr(dk) || bad_ptr(dv)))
+        return DDM_ERR_INVALID;
+    const size_t need = ddm_attention_backward_workspace_bytes(B, Tq, Tk, Hq, Hkv, D, dtype);
+    if (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < need) return DDM_ERR_WORKSPACE;
+    const Plan pl = make_plan(dtype, B, Tq, Tk, Hq, Hkv, D);
+    AttnArgs a{};
+    a.q = q; a.k = k; a.v = v; a.o = out; a.dout = dout; a.lse = const_cast<float *>(lse); a.delta = (float *)workspace;
+    a.dq = dq; a.dk = dk; a.dv = dv;
+    a.cu_q = cu_q; a.cu_k = cu_k;
+    a.B = B; a.Tq = Tq; a.Tk = Tk; a.Hq = Hq; a.Hkv = Hkv; a.D = D;
+    a.group = make_div(Hq / Hkv);
+    a.q_ts = q_ts; a.q_hs = q_hs; a.k_ts = k_ts; a.k_hs = k_hs; a.v_ts = v_ts; a.v_hs = v_hs; a.g_ts = g_ts; a.g_hs = g_hs;
+    a.scale = (float)scale; a.c = (float)(scale * 1.4426950408889634); a.causal = causal;
+    const hipError_t e = with_type(dtype, pl.d, [&](auto t, auto d) {
+        return backward<decltype(t), decltype(d)::value>(a, stream);
+    });
+    return e == hipSuccess ? DDM_OK : DDM_ERR_HIP;
+}
+
+}  // extern "C"

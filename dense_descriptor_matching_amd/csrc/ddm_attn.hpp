@@ -1,0 +1,723 @@
+// ddm_attn.hpp -- attention over packed sequences, forward and backward.
+//
+//   z_ij = scale q_i . k_j,  lse_i = log sum_j e^{z_ij},  P_ij = e^{z_ij - lse_i},  o_i = sum_j P_ij v_j
+//   D_i = do_i . o_i,  dS_ij = P_ij (do_i . v_j - D_i)
+//   dv_j = sum_i P_ij do_i,  dk_j = scale sum_i dS_ij q_i,  dq_i = scale sum_j dS_ij k_j
+// over the keys j that query i of its sequence sees: all, or with causal j <= i + Lk - Lq.
+//
+// The G = Hq / Hkv query heads that share a key head are rows of one problem: row r of a sequence is query r / G, head
+// r % G of the group, so a key tile in LDS serves all of them and the sum of dk and dv over the group is a product's.
+#pragma once
+#include "ddm_tile.hpp"
+
+namespace ddm {
+
+struct AttnArgs {
+    const void *q, *k, *v, *o, *dout;     // o: forward writes it through `out`, backward reads it here
+    void *out, *dq, *dk, *dv;
+    float *lse, *delta;                   // [Tq][Hq]; delta: D_i and, for fp16, the exponent of the row's largest |do|
+    const int32_t *cu_q, *cu_k;
+    int B, Tq, Tk, Hq, Hkv, D;
+    Div group;
+    int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, g_ts, g_hs;   // token and head strides in elements (g: dout)
+    float scale, c;                       // c = scale log2(e)
+    int causal;
+    int chunk, cap;                       // split form: keys of a chunk, rows of a sequence that are split
+    float *part;                          // split form: [slot][Hkv][cap][D + 2]
+};
+
+// Bytes from row 0 of `rows` strided rows of d elements to the end of the last.
+template <class T>
+__device__ __forceinline__ int64_t rows_bytes(int rows, int64_t ts, int d) {
+    return rows <= 0 ? 0 : ((int64_t)(rows - 1) * ts + d) * (int64_t)sizeof(T);
+}
+
+// Operand rows straight from global memory: 8 elements at k positions 16 c + 8 h of a row, zeros past d or without a row.
+template <class T>
+__device__ __forceinline__ Frag<T> global_rows(const T *row, int k, int d, bool in) {
+    Frag<T> f = {};
+    if (!in) return f;
+    if constexpr (sizeof(T) == 2) {
+        if (k < d) f = *reinterpret_cast<const Frag<T> *>(row + k);
+    } else {
+        if (k < d) {
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(row + k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = a[i];
+        }
+        if (k + 4 < d) {
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(row + k + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i + 4] = a[i];
+        }
+    }
+    return f;
+}
+
+// Four consecutive elements of an output row, rounded once.
+template <class T>
+__device__ __forceinline__ void store4(T *p, float a, float b, float c, float d) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<f32x4 *>(p) = f32x4{a, b, c, d};
+    } else {
+        typedef T t4 __attribute__((ext_vector_type(4)));
+        *reinterpret_cast<t4 *>(p) = t4{(T)a, (T)b, (T)c, (T)d};
+    }
+}
+
+// --------------------------------------------------------------------------------------------------------- forward
+// A workgroup takes BM = 32 NW NR rows (each wave NR blocks of 32) and walks over the keys in tiles of BN, which lie in
+// LDS twice over: while one is used, the next is on its way through registers. Running maximum m (in units of log2) and
+// sum l per row; the accumulator is rescaled only when a row's maximum has grown by more than 2^8 since the last time
+// (any reference gives the same quotient; p stays below 2^8, far inside fp16 and bf16).
+// p is rounded to the inputs' type for the second product, which the matrix cores take; l sums it before that.
+// SPLIT: the workgroup takes a chunk of the keys, for few rows and many keys; attn_join joins the chunks.
+template <class T, int D, int NW, int NR, int BN, bool SPLIT>
+__global__ __launch_bounds__(NW * 64, 2) void attn_fwd_kernel(AttnArgs p) {
+    using TL = Tile<T, D>;
+    constexpr int BM = NW * NR * 32, KB = BN / 32, DC = D / 16, DB = D / 32;
+    constexpr int TILE_BYTES = BN * TL::ROW;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[2][2 * TILE_BYTES];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int h = lane >> 5, n = lane & 31;
+    const int G = p.group.g;
+
+    int hk, s, index, row_tile;
+    if constexpr (SPLIT) {
+        hk = blockIdx.x % p.Hkv;
+        row_tile = blockIdx.y;
+        s = find_slot(p.cu_k, p.B, p.Tk, 1, p.chunk, blockIdx.x / p.Hkv, &index);
+        if (s == 0 || s == p.B + 1) return;
+    } else {
+        // workgroups go round-robin to the 8 XCDs, each with its own L2: with 8 | Hkv, a key head stays on one XCD
+        const int heads = p.Hkv, x = blockIdx.x % heads;
+        hk = (heads & 7) ? x : (x & 7) * (heads >> 3) + (x >> 3);
+        const int slots = gridDim.x / heads;
+        // the last rows of a causal sequence see the most keys: they start first
+        s = find_slot(p.cu_q, p.B, p.Tq, G, BM, slots - 1 - blockIdx.x / heads, &index);
+        row_tile = index;
+    }
+    const Span sq = span_of(p.cu_q, p.B, p.Tq, s);
+    Span sk = span_of(p.cu_k, p.B, p.Tk, s);
+    if (s == 0 || s == p.B + 1) sk.hi = sk.lo;
+    const int rows = (sq.hi - sq.lo) * G, Lk = sk.hi - sk.lo, shift = Lk - (sq.hi - sq.lo);
+    int k_from = 0, k_to = Lk;
+    bool whole = !SPLIT;
+    int chunks = 1;
+    if constexpr (SPLIT) {
+        chunks = (Lk + p.chunk - 1) / p.chunk;
+        if (index >= chunks) return;
+        k_from = index * p.chunk;
+        k_to = min(Lk, k_from + p.chunk);
+    }
+    const T *kb = (const T *)p.k + (int64_t)sk.lo * p.k_ts + (int64_t)hk * p.k_hs;
+    const T *vb = (const T *)p.v + (int64_t)sk.lo * p.v_ts + (int64_t)hk * p.v_hs;
+    using In = Dma<T, D, NW, BN>;
+    int koff[In::N], voff[In::N];
+#pragma unroll
+    for (int i = 0; i < In::N; ++i) {
+        koff[i] = In::offset(i, w, lane, p.k_ts, p.D);
+        voff[i] = In::offset(i, w, lane, p.v_ts, p.D);
+    }
+    const int row_at = TL::row_base(lane), col_at = TL::col_base(lane);
+
+    for (;;) {
+        const int row0 = row_tile * BM;
+        if (row0 >= rows) return;
+        // rows of this wave
+        Frag<T> qf[NR][DC];
+        int lim[NR], tok[NR], head[NR];
+        int top = 0, low = k_to;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const int r = row0 + (w * NR + i) * 32 + n;
+            const bool in = r < rows;
+            const int rr = in ? r : rows - 1, qi = (int)div_by(rr, p.group);
+            head[i] = hk * G + (rr - qi * G);
+            tok[i] = in ? sq.lo + qi : -1;
+            lim[i] = p.causal ? min(k_to, qi + shift + 1) : k_to;
+            const T *qr = (const T *)p.q + (int64_t)(sq.lo + qi) * p.q_ts + (int64_t)head[i] * p.q_hs;
+#pragma unroll
+            for (int c = 0; c < DC; ++c) qf[i][c] = global_rows<T>(qr, 16 * c + 8 * h, p.D, in);
+        }
+        if (p.causal) {
+            top = min(k_to, (int)div_by(min(row0 + BM, rows) - 1, p.group) + shift + 1);
+            low = min(k_to, (int)div_by(row0, p.group) + shift + 1);
+        } else {
+            top = k_to;
+        }
+        const int t_end = top > k_from ? (top - k_from + BN - 1) / BN : 0;
+        int wave_top = 0;                                    // keys from here on no row of this wave sees
+        if (const int last = min(row0 + (w + 1) * NR * 32, rows) - 1; last >= row0 + w * NR * 32)
+            wave_top = p.causal ? min(k_to, (int)div_by(last, p.group) + shift + 1) : k_to;
+
+        f32x16 o[NR][DB];
+        float m[NR], l[NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+#pragma unroll
+            for (int d = 0; d < DB; ++d) o[i][d] = 0.f;
+        }
+
+        auto fetch = [&](int t, unsigned char *to) {
+            const int j0 = k_from + t * BN, left = min(k_to - j0, BN);
+            In::load(buffer_of(kb + (int64_t)j0 * p.k_ts, rows_bytes<T>(left, p.k_ts, p.D)), koff, to, w);
+            In::load(buffer_of(vb + (int64_t)j0 * p.v_ts, rows_bytes<T>(left, p.v_ts, p.D)), voff, to + TILE_BYTES, w);
+        };
+        auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, auto masked) {
+            if (t + 1 < t_end) fetch(t + 1, next);
+            if (k_from + t * BN >= wave_top) return;
+            const unsigned char *kt = cur, *vt = cur + TILE_BYTES;
+            f32x16 z[NR][KB];
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+#pragma unroll
+                for (int i = 0; i < NR; ++i) z[i][b] = 0.f;
+#pragma unroll
+                for (int c = 0; c < DC; ++c) {
+                    const Frag<T> kf = TL::rows(kt, row_at, 32 * b, c);
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) mma(z[i][b], kf, qf[i][c]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                if constexpr (decltype(masked)::value) {
+                    const int j0 = k_from + t * BN + 4 * h;
+#pragma unroll
+                    for (int b = 0; b < KB; ++b)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            if (j0 + 32 * b + 8 * (r / 4) + r % 4 >= lim[i]) z[i][b][r] = -INFINITY;
+                }
+                float mx = z[i][0][0];
+#pragma unroll
+                for (int b = 0; b < KB; ++b)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) mx = fmaxf(mx, z[i][b][r]);
+                mx = half_max(mx) * p.c;
+                if (__any(mx > m[i] + 8.f)) {
+                    const float next = fmaxf(m[i], mx);
+                    const float a = next == -INFINITY ? 1.f : exp2_fast(m[i] - next);
+                    l[i] *= a;
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) o[i][d] *= a;
+                    m[i] = next;
+                }
+                const float ref = m[i] == -INFINITY ? 0.f : m[i];
+                float sum = 0.f;
+#pragma unroll
+                for (int b = 0; b < KB; ++b)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        z[i][b][r] = exp2_fast(__builtin_fmaf(z[i][b][r], p.c, -ref));
+                        sum += z[i][b][r];
+                    }
+                l[i] += sum;
+            }
+#pragma unroll
+            for (int kc = 0; kc < BN / 16; ++kc) {
+                Frag<T> pf[NR];
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = z[i][kc / 2][(kc & 1) * 8 + e];
+                    pf[i] = to_frag<T>(x);
+                }
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    const Frag<T> vf = TL::cols(vt, col_at, 16 * kc, 32 * d);
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) mma(o[i][d], vf, pf[i]);
+                }
+            }
+        };
+
+        if (t_end > 0) {
+            fetch(0, lds[0]);
+            tiles_ready();
+            const int t_full = max(0, min(t_end, (low - k_from) / BN));      // tiles that every row sees whole
+            for (int t = 0; t < t_end; ++t) {
+                if (t < t_full) step(t, lds[t & 1], lds[(t + 1) & 1], std::integral_constant<bool, false>{});
+                else step(t, lds[t & 1], lds[(t + 1) & 1], std::integral_constant<bool, true>{});
+                tiles_ready();
+            }
+        }
+
+        // the row's sum over both lane halves; row n of block i is this lane's column
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const float sum = half_sum(l[i]);
+            if (tok[i] < 0) continue;
+            if (whole) {
+                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                T *orow = (T *)p.out + ((int64_t)tok[i] * p.Hq + head[i]) * p.D;
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; r += 4) {
+                        const int col = 32 * d + 8 * (r / 4) + 4 * h;
+                        if (col < p.D)
+                            store4<T>(orow + col, o[i][d][r] * inv, o[i][d][r + 1] * inv, o[i][d][r + 2] * inv,
+                                      o[i][d][r + 3] * inv);
+                    }
+                if (h == 0)
+                    p.lse[(int64_t)tok[i] * p.Hq + head[i]] =
+                        sum > 0.f ? (m[i] + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f : -INFINITY;
+            } else {
+                const int r0 = row0 + (w * NR + i) * 32 + n;
+                float *part = p.part + ((int64_t)blockIdx.x * p.cap + r0) * (p.D + 4);
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; r += 4) {
+                        const int col = 32 * d + 8 * (r / 4) + 4 * h;
+                        if (col < p.D)
+                            store4<float>(part + 4 + col, o[i][d][r], o[i][d][r + 1], o[i][d][r + 2], o[i][d][r + 3]);
+                    }
+                if (h == 0) { part[0] = m[i]; part[1] = sum; }
+            }
+        }
+        if constexpr (!SPLIT) return;
+        // rows past the split ones (longer sequences than the call's average): whole tiles, shared out over the chunks
+        if (!whole && row_tile != 0) return;
+        row_tile = whole ? row_tile + chunks : p.cap / BM + index;
+        whole = true;
+        k_from = 0;
+        k_to = Lk;
+        __syncthreads();
+    }
+}
+
+// Joins the chunks of the split form: one wave for each (query, head). 4-byte reads of D floats a chunk.
+template <class T>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
+    const int lane = threadIdx.x & 63;
+    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (id >= (int64_t)p.Tq * p.Hq) return;
+    const int tok = __builtin_amdgcn_readfirstlane((int)(id / p.Hq)), head = (int)(id % p.Hq);
+    int sq = -1;                                                // the last sequence that begins at or before the token
+    for (int base = 0; base < p.B + 2; base += 64) {
+        const int x = base + lane;
+        const int c = __popcll(__ballot(x < p.B + 2 && bound_at(p.cu_q, p.B, p.Tq, x) <= tok));
+        sq += c;
+        if (c < 64) break;
+    }
+    sq = __builtin_amdgcn_readfirstlane(sq);
+    const Span q = span_of(p.cu_q, p.B, p.Tq, sq);
+    Span k = span_of(p.cu_k, p.B, p.Tk, sq);
+    if (sq == 0 || sq == p.B + 1) k.hi = k.lo;
+    const int G = p.group.g, hk = head / G, r = (tok - q.lo) * G + head % G;
+    const int chunks = (k.hi - k.lo + p.chunk - 1) / p.chunk;
+    T *orow = (T *)p.out + id * p.D;
+    if (chunks > 0 && r >= p.cap) return;                       // written whole
+    const int slot0 = k.lo / p.chunk + sq;
+    const float *part = p.part + (((int64_t)slot0 * p.Hkv + hk) * p.cap + r) * (p.D + 4);
+    const int64_t pitch = (int64_t)p.Hkv * p.cap * (p.D + 4);
+    float top = -INFINITY;
+    for (int c = lane; c < chunks; c += 64) top = fmaxf(top, part[c * pitch]);
+#pragma unroll
+    for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
+    float sum = 0.f, a0 = 0.f, a1 = 0.f;
+    const float ref = top == -INFINITY ? 0.f : top;
+    for (int c = 0; c < chunks; ++c) {
+        const float *pc = part + c * pitch;
+        const float f = exp2_fast(pc[0] - ref);
+        sum += f * pc[1];
+        if (lane < p.D) a0 += f * pc[4 + lane];
+        if (lane + 64 < p.D) a1 += f * pc[4 + 64 + lane];
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    if (lane < p.D) orow[lane] = (T)(a0 * inv);
+    if (lane + 64 < p.D) orow[lane + 64] = (T)(a1 * inv);
+    if (lane == 0) p.lse[id] = sum > 0.f ? (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f : -INFINITY;
+}
+
+// -------------------------------------------------------------------------------------------------------- backward
+// fp16 holds dS to few bits once it is below 2^-14, which small gradients make it; there each row's dS is divided by the power
+// of two next to its largest |do| before it is rounded, and the products are multiplied back in fp32.
+template <class T> constexpr bool scaled_ds = sizeof(T) == 2 && !std::is_same_v<T, __bf16>;
+constexpr float NO_EXPONENT = -100.f;
+
+// dq and D_i, one row block at a time as in the forward pass: S and dO V^T of 32 keys from two key tiles' rows, then dS
+// times K from the key tile's columns. No sum crosses workgroups, so the result does not depend on their order; the price
+// is that S and dO V^T are computed here and again in attn_dkv_kernel (7 products instead of 5).
+template <class T, int D, int NW, int NR, int BN>
+__global__ __launch_bounds__(NW * 64, 2) void attn_dq_kernel(AttnArgs p) {
+    using TL = Tile<T, D>;
+    constexpr int BM = NW * NR * 32, DC = D / 16, DB = D / 32;
+    constexpr int TILE_BYTES = BN * TL::ROW;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[2][2 * TILE_BYTES];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int h = lane >> 5, n = lane & 31;
+    const int G = p.group.g;
+
+    const int heads = p.Hkv, x = blockIdx.x % heads;
+    const int hk = (heads & 7) ? x : (x & 7) * (heads >> 3) + (x >> 3);
+    int row_tile;
+    const int s = find_slot(p.cu_q, p.B, p.Tq, G, BM, gridDim.x / heads - 1 - blockIdx.x / heads, &row_tile);
+    const Span sq = span_of(p.cu_q, p.B, p.Tq, s);
+    Span sk = span_of(p.cu_k, p.B, p.Tk, s);
+    if (s == 0 || s == p.B + 1) sk.hi = sk.lo;
+    const int rows = (sq.hi - sq.lo) * G, Lk = sk.hi - sk.lo, shift = Lk - (sq.hi - sq.lo), row0 = row_tile * BM;
+    if (row0 >= rows) return;
+    const T *kb = (const T *)p.k + (int64_t)sk.lo * p.k_ts + (int64_t)hk * p.k_hs;
+    const T *vb = (const T *)p.v + (int64_t)sk.lo * p.v_ts + (int64_t)hk * p.v_hs;
+    using In = Dma<T, D, NW, BN>;
+    int koff[In::N], voff[In::N];
+#pragma unroll
+    for (int i = 0; i < In::N; ++i) {
+        koff[i] = In::offset(i, w, lane, p.k_ts, p.D);
+        voff[i] = In::offset(i, w, lane, p.v_ts, p.D);
+    }
+    const int row_at = TL::row_base(lane), col_at = TL::col_base(lane);
+
+    Frag<T> qf[NR][DC], gf[NR][DC];
+    int lim[NR];
+    int64_t at[NR];
+    float lse[NR], delta[NR], inv[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const int r = row0 + (w * NR + i) * 32 + n;
+        const bool in = r < rows;
+        const int rr = in ? r : rows - 1, qi = (int)div_by(rr, p.group), head = hk * G + (rr - qi * G);
+        const int64_t tok = sq.lo + qi;
+        lim[i] = p.causal ? min(Lk, qi + shift + 1) : Lk;
+        at[i] = in ? tok * p.Hq + head : -1;
+        const T *qr = (const T *)p.q + tok * p.q_ts + (int64_t)head * p.q_hs;
+        const T *gr = (const T *)p.dout + tok * p.g_ts + (int64_t)head * p.g_hs;
+        const T *orow = (const T *)p.o + (tok * p.Hq + head) * p.D;
+        float sum = 0.f, big = 0.f;
+#pragma unroll
+        for (int c = 0; c < DC; ++c) {
+            qf[i][c] = global_rows<T>(qr, 16 * c + 8 * h, p.D, in);
+            gf[i][c] = global_rows<T>(gr, 16 * c + 8 * h, p.D, in);
+            const Frag<T> of = global_rows<T>(orow, 16 * c + 8 * h, p.D, in);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                sum = __builtin_fmaf((float)gf[i][c][e], (float)of[e], sum);
+                if constexpr (scaled_ds<T>) big = fmaxf(big, fabsf((float)gf[i][c][e]));
+            }
+        }
+        delta[i] = half_sum(sum);
+        const float z = in ? p.lse[at[i]] : -INFINITY;
+        lse[i] = z == -INFINITY ? INFINITY : z * 1.44269504088896341f;      // a row that sees no key: every P is 0
+        inv[i] = 1.f;
+        float ex = NO_EXPONENT;
+        if constexpr (scaled_ds<T>) {
+            big = half_max(big);
+            if (big > 0.f) ex = fmaxf(NO_EXPONENT, (float)__builtin_amdgcn_frexp_expf(big));
+            inv[i] = exp2_fast(-ex);
+        }
+        if (in && h == 0) {
+            p.delta[at[i]] = delta[i];
+            if constexpr (scaled_ds<T>) p.delta[at[i] + (int64_t)p.Tq * p.Hq] = ex;
+        }
+    }
+    int top = Lk, low = Lk;
+    if (p.causal) {
+        top = min(Lk, (int)div_by(min(row0 + BM, rows) - 1, p.group) + shift + 1);
+        low = min(Lk, (int)div_by(row0, p.group) + shift + 1);
+    }
+    const int t_end = top > 0 ? (top + BN - 1) / BN : 0;
+    int wave_top = 0;
+    if (const int last = min(row0 + (w + 1) * NR * 32, rows) - 1; last >= row0 + w * NR * 32)
+        wave_top = p.causal ? min(Lk, (int)div_by(last, p.group) + shift + 1) : Lk;
+
+    f32x16 dq[NR][DB];
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int d = 0; d < DB; ++d) dq[i][d] = 0.f;
+
+    auto fetch = [&](int t, unsigned char *to) {
+        const int j0 = t * BN, left = min(Lk - j0, BN);
+        In::load(buffer_of(kb + (int64_t)j0 * p.k_ts, rows_bytes<T>(left, p.k_ts, p.D)), koff, to, w);
+        In::load(buffer_of(vb + (int64_t)j0 * p.v_ts, rows_bytes<T>(left, p.v_ts, p.D)), voff, to + TILE_BYTES, w);
+    };
+    auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, auto masked) {
+        if (t + 1 < t_end) fetch(t + 1, next);
+        if (t * BN >= wave_top) return;
+        const unsigned char *kt = cur, *vt = cur + TILE_BYTES;
+#pragma unroll 1
+        for (int b = 0; b < BN / 32; ++b) {
+            f32x16 z[NR], y[NR];
+#pragma unroll
+            for (int i = 0; i < NR; ++i) { z[i] = 0.f; y[i] = 0.f; }
+#pragma unroll
+            for (int c = 0; c < DC; ++c) {
+                const Frag<T> kf = TL::rows(kt, row_at, 32 * b, c), vf = TL::rows(vt, row_at, 32 * b, c);
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    mma(z[i], kf, qf[i][c]);
+                    mma(y[i], vf, gf[i][c]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const float pr = exp2_fast(__builtin_fmaf(z[i][r], p.c, -lse[i]));
+                    float ds = pr * (y[i][r] - delta[i]);
+                    if constexpr (scaled_ds<T>) ds *= inv[i];
+                    if constexpr (decltype(masked)::value)
+                        if (t * BN + 32 * b + 4 * h + 8 * (r / 4) + r % 4 >= lim[i]) ds = 0.f;
+                    z[i][r] = ds;
+                }
+#pragma unroll
+            for (int kc = 0; kc < 2; ++kc) {
+                Frag<T> sf[NR];
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = z[i][kc * 8 + e];
+                    sf[i] = to_frag<T>(v);
+                }
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    const Frag<T> kf = TL::cols(kt, col_at, 32 * b + 16 * kc, 32 * d);
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) mma(dq[i][d], kf, sf[i]);
+                }
+            }
+        }
+    };
+    if (t_end > 0) {
+        fetch(0, lds[0]);
+        tiles_ready();
+        const int t_full = max(0, min(t_end, low / BN));
+        for (int t = 0; t < t_end; ++t) {
+            if (t < t_full) step(t, lds[t & 1], lds[(t + 1) & 1], std::integral_constant<bool, false>{});
+            else step(t, lds[t & 1], lds[(t + 1) & 1], std::integral_constant<bool, true>{});
+            tiles_ready();
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        if (at[i] < 0) continue;
+        const float f = scaled_ds<T> ? p.scale / inv[i] : p.scale;
+        T *row = (T *)p.dq + at[i] * p.D;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+                const int col = 32 * d + 8 * (r / 4) + 4 * h;
+                if (col < p.D)
+                    store4<T>(row + col, dq[i][d][r] * f, dq[i][d][r + 1] * f, dq[i][d][r + 2] * f, dq[i][d][r + 3] * f);
+            }
+    }
+}
+
+// dk and dv: a workgroup keeps 32 NW NR keys (K and V rows as operands in registers) and walks over the rows of the key
+// head's whole group in tiles of BQ, Q and dO in LDS. S = Q K^T and dO V^T come out with the keys as columns, so P and dS feed
+// the products with dO and Q (read as columns) without leaving their lanes.
+template <class T, int D, int NW, int NR, int BQ>
+__global__ __launch_bounds__(NW * 64, D == 128 ? 1 : 2) void attn_dkv_kernel(AttnArgs p) {
+    using TL = Tile<T, D>;
+    constexpr int BK = NW * NR * 32, DC = D / 16, DB = D / 32;
+    constexpr int TILE_BYTES = BQ * TL::ROW;
+    static_assert(BQ <= 64, "a wave loads a tile's statistics");
+    __shared__ __attribute__((aligned(16))) unsigned char lds[2][2 * TILE_BYTES];
+    __shared__ __attribute__((aligned(16))) float st_lse[2][BQ], st_delta[2][BQ];
+    __shared__ __attribute__((aligned(16))) int st_lim[2][BQ];
+    __shared__ float st_exp[2];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int h = lane >> 5, n = lane & 31;
+    const int G = p.group.g;
+
+    const int heads = p.Hkv, x = blockIdx.x % heads;
+    const int hk = (heads & 7) ? x : (x & 7) * (heads >> 3) + (x >> 3);
+    int key_tile;
+    const int s = find_slot(p.cu_k, p.B, p.Tk, 1, BK, blockIdx.x / heads, &key_tile);
+    Span sq = span_of(p.cu_q, p.B, p.Tq, s);
+    const Span sk = span_of(p.cu_k, p.B, p.Tk, s);
+    if (s == 0 || s == p.B + 1) sq.hi = sq.lo;
+    const int rows = (sq.hi - sq.lo) * G, Lk = sk.hi - sk.lo, shift = Lk - (sq.hi - sq.lo), j0 = key_tile * BK;
+    if (j0 >= Lk) return;
+    const int j_end = min(j0 + BK, Lk);
+
+    Frag<T> kf[NR][DC], vf[NR][DC];
+    int key[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        key[i] = j0 + (w * NR + i) * 32 + n;
+        const bool in = key[i] < Lk;
+        const int64_t tok = sk.lo + (in ? key[i] : Lk - 1);
+        const T *kr = (const T *)p.k + tok * p.k_ts + (int64_t)hk * p.k_hs;
+        const T *vr = (const T *)p.v + tok * p.v_ts + (int64_t)hk * p.v_hs;
+#pragma unroll
+        for (int c = 0; c < DC; ++c) {
+            kf[i][c] = global_rows<T>(kr, 16 * c + 8 * h, p.D, in);
+            vf[i][c] = global_rows<T>(vr, 16 * c + 8 * h, p.D, in);
+        }
+    }
+    const int first = p.causal ? min(rows, max(0, j0 - shift) * G) : 0;     // earlier rows see none of these keys
+    const int t_end = (rows - first + BQ - 1) / BQ;
+    const int wave_key = j0 + w * NR * 32;
+
+    f32x16 dk[NR][DB], dv[NR][DB];
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int d = 0; d < DB; ++d) { dk[i][d] = 0.f; dv[i][d] = 0.f; }
+    float ref = NO_EXPONENT;                                  // dk is held in units of 2^ref (fp16)
+
+    using In = Dma<T, D, NW, BQ>;
+    const int row_at = TL::row_base(lane), col_at = TL::col_base(lane);
+    float s_lse = INFINITY, s_delta = 0.f, s_exp = NO_EXPONENT;
+    int s_lim = 0;
+    auto fetch = [&](int t, unsigned char *to) {
+        const int r0 = first + t * BQ, q0 = (int)div_by(r0, p.group);
+        const auto qb = buffer_of((const T *)p.q + (int64_t)(sq.lo + q0) * p.q_ts + (int64_t)hk * G * p.q_hs, INT64_MAX);
+        const auto gb = buffer_of((const T *)p.dout + (int64_t)(sq.lo + q0) * p.g_ts + (int64_t)hk * G * p.g_hs, INT64_MAX);
+        int qo[In::N], go[In::N];
+#pragma unroll
+        for (int i = 0; i < In::N; ++i) {
+            const int r = r0 + In::row(i, w, lane), pc = In::piece(i, w, lane);
+            const int qi = (int)div_by(r, p.group), g = r - qi * G;
+            const bool in = r < rows && pc * TL::PE < p.D;
+            qo[i] = in ? ((qi - q0) * (int)p.q_ts + g * (int)p.q_hs) * (int)sizeof(T) + pc * 16 : OUTSIDE;
+            go[i] = in ? ((qi - q0) * (int)p.g_ts + g * (int)p.g_hs) * (int)sizeof(T) + pc * 16 : OUTSIDE;
+        }
+        In::load(qb, qo, to, w);
+        In::load(gb, go, to + TILE_BYTES, w);
+        if (tid < BQ) {
+            const int r = r0 + tid;
+            const bool in = r < rows;
+            const int rr = in ? r : rows - 1, qi = (int)div_by(rr, p.group);
+            const int64_t at = (int64_t)(sq.lo + qi) * p.Hq + hk * G + (rr - qi * G);
+            const float z = p.lse[at];
+            s_lse = !in || z == -INFINITY ? INFINITY : z * 1.44269504088896341f;
+            s_delta = in ? p.delta[at] : 0.f;
+            s_lim = qi + shift + 1;
+            if constexpr (scaled_ds<T>) s_exp = in ? p.delta[at + (int64_t)p.Tq * p.Hq] : NO_EXPONENT;
+        }
+    };
+    auto put_stats = [&](int b) {
+        if (tid < BQ) {
+            st_lse[b][tid] = s_lse;
+            st_delta[b][tid] = s_delta;
+            st_lim[b][tid] = s_lim;
+        }
+        if constexpr (scaled_ds<T>) {
+            if (tid < 64) {
+                float e = tid < BQ ? s_exp : NO_EXPONENT;
+#pragma unroll
+                for (int d = 32; d; d >>= 1) e = fmaxf(e, __shfl_xor(e, d));
+                if (tid == 0) st_exp[b] = e;
+            }
+        }
+    };
+    auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, bool busy, auto masked) {
+        if (t + 1 < t_end) fetch(t + 1, next);
+        if (!busy) return;
+        const int buf = t & 1;
+        const unsigned char *qt = cur, *gt = cur + TILE_BYTES;
+        float inv = 1.f;
+        if constexpr (scaled_ds<T>) {
+            const float e = st_exp[buf];
+            if (e > ref) {
+                const float f = exp2_fast(ref - e);
+#pragma unroll
+                for (int i = 0; i < NR; ++i)
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) dk[i][d] *= f;
+                ref = e;
+            }
+            inv = exp2_fast(-ref);
+        }
+#pragma unroll 1
+        for (int b = 0; b < BQ / 32; ++b) {
+            f32x16 z[NR], y[NR];
+#pragma unroll
+            for (int i = 0; i < NR; ++i) { z[i] = 0.f; y[i] = 0.f; }
+#pragma unroll
+            for (int c = 0; c < DC; ++c) {
+                const Frag<T> qf = TL::rows(qt, row_at, 32 * b, c), gf = TL::rows(gt, row_at, 32 * b, c);
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    mma(z[i], qf, kf[i][c]);
+                    mma(y[i], gf, vf[i][c]);
+                }
+            }
+#pragma unroll
+            for (int r4 = 0; r4 < 4; ++r4) {
+                const int r0 = 32 * b + 8 * r4 + 4 * h;
+                const f32x4 ls = *reinterpret_cast<const f32x4 *>(&st_lse[buf][r0]);
+                const f32x4 de = *reinterpret_cast<const f32x4 *>(&st_delta[buf][r0]);
+#pragma unroll
+                for (int i = 0; i < NR; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = 4 * r4 + e;
+                        float pr = exp2_fast(__builtin_fmaf(z[i][r], p.c, -ls[e]));
+                        if constexpr (decltype(masked)::value) pr = key[i] < st_lim[buf][r0 + e] ? pr : 0.f;
+                        z[i][r] = pr;
+                        y[i][r] = pr * (y[i][r] - de[e]);
+                        if constexpr (scaled_ds<T>) y[i][r] *= inv;
+                    }
+            }
+#pragma unroll
+            for (int kc = 0; kc < 2; ++kc) {
+                Frag<T> pf[NR], sf[NR];
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    float a[8], c[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) { a[e] = z[i][kc * 8 + e]; c[e] = y[i][kc * 8 + e]; }
+                    pf[i] = to_frag<T>(a);
+                    sf[i] = to_frag<T>(c);
+                }
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    const Frag<T> gf = TL::cols(gt, col_at, 32 * b + 16 * kc, 32 * d);
+                    const Frag<T> qf = TL::cols(qt, col_at, 32 * b + 16 * kc, 32 * d);
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) {
+                        mma(dv[i][d], gf, pf[i]);
+                        mma(dk[i][d], qf, sf[i]);
+                    }
+                }
+            }
+        }
+    };
+    if (t_end > 0) {
+        fetch(0, lds[0]);
+        put_stats(0);
+        tiles_ready();
+        for (int t = 0; t < t_end; ++t) {
+            const int r0 = first + t * BQ;
+            bool busy = wave_key < Lk, full = true;
+            if (p.causal) {
+                busy = busy && wave_key < (int)div_by(min(r0 + BQ, rows) - 1, p.group) + shift + 1;
+                full = j_end <= (int)div_by(r0, p.group) + shift + 1;
+            }
+            if (full) step(t, lds[t & 1], lds[(t + 1) & 1], busy, std::integral_constant<bool, false>{});
+            else step(t, lds[t & 1], lds[(t + 1) & 1], busy, std::integral_constant<bool, true>{});
+            if (t + 1 < t_end) put_stats((t + 1) & 1);
+            tiles_ready();
+        }
+    }
+    const float f = scaled_ds<T> ? p.scale * exp2_fast(ref) : p.scale;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        if (key[i] >= Lk) continue;
+        const int64_t at = ((int64_t)(sk.lo + key[i]) * p.Hkv + hk) * p.D;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+                const int col = 32 * d + 8 * (r / 4) + 4 * h;
+                if (col >= p.D) continue;
+                store4<T>((T *)p.dk + at + col, dk[i][d][r] * f, dk[i][d][r + 1] * f, dk[i][d][r + 2] * f,
+                          dk[i][d][r + 3] * f);
+                store4<T>((T *)p.dv + at + col, dv[i][d][r], dv[i][d][r + 1], dv[i][d][r + 2], dv[i][d][r + 3]);
+            }
+    }
+}
+
+}  // namespace ddm

@@ -1,0 +1,452 @@
+// ddm_loss.hip -- the matching loss and its gradient (ddm_matching_loss_*).
+//
+//   z_ij = a_i . b_j / t,  loss_i = (lse_a_i + lse_b_i) / 2 - z_ii
+//   dz_ij = (g_i e^{z_ij - lse_a_i} + g_j e^{z_ij - lse_b_j}) / 2 - g_i [i = j]
+//   da_i = sum_j dz_ij b_j / t,  db_j = sum_i dz_ij a_i / t
+// within each packed set. Scores exist only as matrix-core tiles. With some 24 to 64 components a score costs far less on the
+// matrix cores than its exponentials on the vector units, so each direction has its own pass: rows of one side
+// stay in registers and the other side's go by, and no sum crosses workgroups except over the S pieces that a set's columns
+// are cut into when there are too few rows to fill the card; those are joined in order.
+#include "../../include/ddm.h"
+#include "ddm_attn.hpp"
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+using namespace ddm;
+
+namespace {
+
+constexpr float LOG2E = 1.44269504088896341f, LN2 = 0.69314718055994531f;
+
+struct LossArgs {
+    const void *a, *b;               // [P][ld] rows, of which w elements are read (w = d, or the padded d of copied rows)
+    const int32_t *cu;
+    int B, P, d, w, ld, S;
+    float c, inv_t;                  // c = log2(e) / t
+    float2 *ml;                      // forward: [2][S][P] running maximum (times c) and sum
+    float *hit;                      // forward: c z_ii t
+    const float *g, *lse_a, *lse_b;  // backward
+    void *da, *db;
+    float *part;                     // backward: [2][S][P][DP], or null: written straight to da, db
+};
+
+// Columns [from, to) of piece `s` of S of a set of n.
+__device__ __forceinline__ void piece_of(int n, int S, int s, int tile, int *from, int *to) {
+    const int each = ((n + S - 1) / S + tile - 1) / tile * tile;
+    *from = min(n, s * each);
+    *to = min(n, *from + each);
+}
+
+// Forward, one direction (blockIdx.z): rows x of one side, columns y of the other. As attention's forward without values;
+// the maximum is exact here, since the loss of a clear match is the logarithm of a sum next to 1.
+template <class T, int D, int BN>
+__global__ __launch_bounds__(256, 2) void loss_fwd_kernel(LossArgs p) {
+    using TL = Tile<T, D>;
+    using In = Dma<T, D, 4, BN>;
+    constexpr int DC = D / 16, KB = BN / 32, BM = 128;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[2][BN * TL::ROW];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+    const int dir = blockIdx.z;
+    int index;
+    const int s = find_slot(p.cu, p.B, p.P, 1, BM, blockIdx.x, &index);
+    const Span span = span_of(p.cu, p.B, p.P, s);
+    const int n = span.hi - span.lo, row0 = index * BM;
+    if (row0 >= n) return;
+    int from = 0, to = 0;
+    if (s != 0 && s != p.B + 1) piece_of(n, p.S, blockIdx.y, BN, &from, &to);
+    const T *xs = (const T *)(dir ? p.b : p.a) + (int64_t)span.lo * p.ld, *ys = (const T *)(dir ? p.a : p.b) + (int64_t)span.lo * p.ld;
+    const int row = row0 + w * 32 + (lane & 31);
+    const bool in = row < n;
+    Frag<T> xf[DC];
+#pragma unroll
+    for (int c = 0; c < DC; ++c) xf[c] = global_rows<T>(xs + (int64_t)(in ? row : n - 1) * p.ld, 16 * c + 8 * h, p.w, in);
+    int off[In::N];
+#pragma unroll
+    for (int i = 0; i < In::N; ++i) off[i] = In::offset(i, w, lane, p.ld, p.w);
+    const int row_at = TL::row_base(lane);
+    float m = -INFINITY, l = 0.f, hit = -INFINITY;
+    const int t_end = (to - from + BN - 1) / BN;
+    auto fetch = [&](int t, unsigned char *dst) {
+        const int j0 = from + t * BN;
+        In::load(buffer_of(ys + (int64_t)j0 * p.ld, rows_bytes<T>(min(to - j0, BN), p.ld, p.w)), off, dst, w);
+    };
+    auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, auto special) {
+        if (t + 1 < t_end) fetch(t + 1, next);
+        f32x16 z[KB];
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+            z[b] = 0.f;
+#pragma unroll
+            for (int c = 0; c < DC; ++c) mma(z[b], TL::rows(cur, row_at, 32 * b, c), xf[c]);
+        }
+        if constexpr (decltype(special)::value) {
+            const int j0 = from + t * BN + 4 * h;
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int j = j0 + 32 * b + 8 * (r / 4) + r % 4;
+                    if (j == row) hit = z[b][r];
+                    if (j >= to) z[b][r] = -INFINITY;
+                }
+        }
+        float mx = z[0][0];
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, z[b][r]);
+        const float next_m = fmaxf(m, half_max(mx) * p.c);
+        float sum = 0.f;
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sum += exp2_fast(__builtin_fmaf(z[b][r], p.c, -next_m));
+        l = __builtin_fmaf(l, exp2_fast(m - next_m), sum);
+        m = next_m;
+    };
+    if (t_end > 0) {
+        fetch(0, lds[0]);
+        tiles_ready();
+        for (int t = 0; t < t_end; ++t) {
+            const int j0 = from + t * BN;
+            const bool special = j0 + BN > to || (j0 < row0 + BM && row0 < j0 + BN);
+            if (special) step(t, lds[t & 1], lds[(t + 1) & 1], std::integral_constant<bool, true>{});
+            else step(t, lds[t & 1], lds[(t + 1) & 1], std::integral_constant<bool, false>{});
+            tiles_ready();
+        }
+    }
+    l = half_sum(l);
+    hit = half_max(hit);
+    if (!in || h) return;
+    p.ml[((int64_t)dir * p.S + blockIdx.y) * p.P + span.lo + row] = make_float2(m, l);
+    if (dir == 0) {
+        if (row >= from && row < to) p.hit[span.lo + row] = hit * p.c;
+    }
+}
+
+__global__ __launch_bounds__(256) void loss_join_kernel(LossArgs p, float *loss, float *lse_a, float *lse_b) {
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= p.P) return;
+    float top[2], log_sum[2];
+    bool any = false;
+    for (int dir = 0; dir < 2; ++dir) {
+        const float2 *ml = p.ml + (int64_t)dir * p.S * p.P + i;
+        float m = -INFINITY, l = 0.f;
+        for (int s = 0; s < p.S; ++s) m = fmaxf(m, ml[(int64_t)s * p.P].x);
+        for (int s = 0; s < p.S; ++s) {
+            const float2 v = ml[(int64_t)s * p.P];
+            if (v.y > 0.f) l += v.y * exp2_fast(v.x - m);
+        }
+        any = l > 0.f;
+        top[dir] = m;
+        log_sum[dir] = __builtin_amdgcn_logf(l);
+    }
+    const float hit = p.hit[i];
+    lse_a[i] = any ? (top[0] + log_sum[0]) * LN2 : 0.f;
+    lse_b[i] = any ? (top[1] + log_sum[1]) * LN2 : 0.f;
+    loss[i] = any ? (((top[0] - hit) + (top[1] - hit)) + (log_sum[0] + log_sum[1])) * (0.5f * LN2) : 0.f;
+}
+
+// Backward, one direction: dx of the rows, the gradient by the scores made tile by tile. fp16 holds it to few bits below 2^-14,
+// where a mean over many matches lies: there g is divided by a power of two next to its largest value in reach first.
+template <class T, int D, int BN>
+__global__ __launch_bounds__(256, 2) void loss_bwd_kernel(LossArgs p) {
+    using TL = Tile<T, D>;
+    using In = Dma<T, D, 4, BN>;
+    constexpr int DC = D / 16, DB = D / 32, BM = 128;
+    constexpr bool exact_exp = sizeof(T) == 4;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[2][BN * TL::ROW];
+    __shared__ __attribute__((aligned(16))) float st_lse[2][BN], st_g[2][BN];
+    __shared__ float biggest[4];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+    const int dir = blockIdx.z;
+    int index;
+    const int s = find_slot(p.cu, p.B, p.P, 1, BM, blockIdx.x, &index);
+    const Span span = span_of(p.cu, p.B, p.P, s);
+    const int n = span.hi - span.lo, row0 = index * BM;
+    if (row0 >= n) return;
+    int from = 0, to = 0;
+    if (s != 0 && s != p.B + 1) piece_of(n, p.S, blockIdx.y, BN, &from, &to);
+    const T *xs = (const T *)(dir ? p.b : p.a) + (int64_t)span.lo * p.ld, *ys = (const T *)(dir ? p.a : p.b) + (int64_t)span.lo * p.ld;
+    const float *lse_x = (dir ? p.lse_b : p.lse_a) + span.lo, *lse_y = (dir ? p.lse_a : p.lse_b) + span.lo, *g = p.g + span.lo;
+    const int row = row0 + w * 32 + (lane & 31);
+    const bool in = row < n;
+    const float unit = exact_exp ? 1.f : LOG2E;                // exponents in natural or base-2 units
+    const float slope = exact_exp ? p.inv_t : p.c;
+    float scale = 1.f;
+    if constexpr (scaled_ds<T>) {
+        float big = 0.f;
+        for (int j = from + tid; j < to; j += 256) big = fmaxf(big, fabsf(g[j]));
+        if (row0 + tid < n && tid < BM) big = fmaxf(big, fabsf(g[row0 + tid]));
+#pragma unroll
+        for (int x = 32; x; x >>= 1) big = fmaxf(big, __shfl_xor(big, x));
+        if (lane == 0) biggest[w] = big;
+        __syncthreads();
+        big = fmaxf(fmaxf(biggest[0], biggest[1]), fmaxf(biggest[2], biggest[3]));
+        if (big > 0.f) scale = exp2_fast(fminf(100.f, -(float)__builtin_amdgcn_frexp_expf(big)));
+    }
+    const float my_g = in ? g[row] * scale : 0.f, half_g = 0.5f * my_g, my_lse = in ? lse_x[row] * unit : INFINITY;
+    Frag<T> xf[DC];
+#pragma unroll
+    for (int c = 0; c < DC; ++c) xf[c] = global_rows<T>(xs + (int64_t)(in ? row : n - 1) * p.ld, 16 * c + 8 * h, p.w, in);
+    int off[In::N];
+#pragma unroll
+    for (int i = 0; i < In::N; ++i) off[i] = In::offset(i, w, lane, p.ld, p.w);
+    const int row_at = TL::row_base(lane), col_at = TL::col_base(lane);
+    float diag = 0.f;                                          // dz_ii, kept out of the rounded products: it is the largest
+    f32x16 dx[DB];
+#pragma unroll
+    for (int d = 0; d < DB; ++d) dx[d] = 0.f;
+    const int t_end = (to - from + BN - 1) / BN;
+    float s_lse = INFINITY, s_g = 0.f;
+    auto fetch = [&](int t, unsigned char *dst) {
+        const int j0 = from + t * BN;
+        In::load(buffer_of(ys + (int64_t)j0 * p.ld, rows_bytes<T>(min(to - j0, BN), p.ld, p.w)), off, dst, w);
+        if (tid < BN) {
+            const bool ok = j0 + tid < to;
+            s_lse = ok ? lse_y[j0 + tid] * unit : INFINITY;
+            s_g = ok ? 0.5f * scale * g[j0 + tid] : 0.f;
+        }
+    };
+    auto put_stats = [&](int b) {
+        if (tid < BN) { st_lse[b][tid] = s_lse; st_g[b][tid] = s_g; }
+    };
+    auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, auto special) {
+        if (t + 1 < t_end) fetch(t + 1, next);
+#pragma unroll
+        for (int b = 0; b < BN / 32; ++b) {
+            f32x16 z = 0.f;
+#pragma unroll
+            for (int c = 0; c < DC; ++c) mma(z, TL::rows(cur, row_at, 32 * b, c), xf[c]);
+#pragma unroll
+            for (int r4 = 0; r4 < 4; ++r4) {
+                const int k0 = 32 * b + 8 * r4 + 4 * h;
+                const f32x4 ly = *reinterpret_cast<const f32x4 *>(&st_lse[t & 1][k0]);
+                const f32x4 gy = *reinterpret_cast<const f32x4 *>(&st_g[t & 1][k0]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v = z[4 * r4 + e];
+                    float ux = __builtin_fmaf(v, slope, -my_lse), uy = __builtin_fmaf(v, slope, -ly[e]);
+                    if constexpr (exact_exp) { ux *= LOG2E; uy *= LOG2E; }
+                    float dz = __builtin_fmaf(gy[e], exp2_fast(uy), half_g * exp2_fast(ux));
+                    if constexpr (decltype(special)::value) {
+                        const int j = from + t * BN + k0 + e;
+                        if (j == row) { diag = dz - my_g; dz = 0.f; }
+                        if (j >= to) dz = 0.f;
+                    }
+                    z[4 * r4 + e] = dz;
+                }
+            }
+#pragma unroll
+            for (int kc = 0; kc < 2; ++kc) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = z[kc * 8 + e];
+                const Frag<T> zf = to_frag<T>(v);
+#pragma unroll
+                for (int d = 0; d < DB; ++d) mma(dx[d], TL::cols(cur, col_at, 32 * b + 16 * kc, 32 * d), zf);
+            }
+        }
+    };
+    if (t_end > 0) {
+        fetch(0, lds[0]);
+        put_stats(0);
+        tiles_ready();
+        for (int t = 0; t < t_end; ++t) {
+            const int j0 = from + t * BN;
+            const bool special = j0 + BN > to || (j0 < row0 + BM && row0 < j0 + BN);
+            if (special) step(t, lds[t & 1], lds[(t + 1) & 1], std::integral_constant<bool, true>{});
+            else step(t, lds[t & 1], lds[(t + 1) & 1], std::integral_constant<bool, false>{});
+            if (t + 1 < t_end) put_stats((t + 1) & 1);
+            tiles_ready();
+        }
+    }
+    diag = half_sum(diag);
+    if (!in) return;
+    const float f = p.inv_t / scale;
+    if (diag != 0.f) {
+        const T *match = ys + (int64_t)row * p.ld;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int col = 32 * d + 8 * (r / 4) + 4 * h + r % 4;
+                if (col < p.d) dx[d][r] = __builtin_fmaf(diag, (float)match[col], dx[d][r]);
+            }
+    }
+    if (p.part) {
+        float *out = p.part + (((int64_t)dir * p.S + blockIdx.y) * p.P + span.lo + row) * D;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4)
+                store4<float>(out + 32 * d + 8 * (r / 4) + 4 * h, dx[d][r] * f, dx[d][r + 1] * f, dx[d][r + 2] * f, dx[d][r + 3] * f);
+    } else {
+        T *out = (T *)(dir ? p.db : p.da) + (int64_t)(span.lo + row) * p.d;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+                const int col = 32 * d + 8 * (r / 4) + 4 * h;
+                if (col < p.d) store4<T>(out + col, dx[d][r] * f, dx[d][r + 1] * f, dx[d][r + 2] * f, dx[d][r + 3] * f);
+            }
+    }
+}
+
+// da (blockIdx.y = 0) and db (1) from the pieces.
+template <class T>
+__global__ __launch_bounds__(256) void loss_sum_kernel(LossArgs p, int dp) {
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e >= (int64_t)p.P * p.d) return;
+    const int64_t i = e / p.d, c = e % p.d;
+    const float *part = p.part + ((int64_t)blockIdx.y * p.S * p.P + i) * dp + c;
+    float sum = 0.f;
+    for (int s = 0; s < p.S; ++s) sum += part[(int64_t)s * p.P * dp];
+    ((T *)(blockIdx.y ? p.db : p.da))[e] = (T)sum;
+}
+
+// Rows that are not whole 16-byte pieces at 16-byte boundaries: copied with zeros up to dp elements.
+template <class T>
+__global__ __launch_bounds__(256) void loss_repack_kernel(const T *a, const T *b, int P, int d, int dp, T *out) {
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e >= (int64_t)P * dp) return;
+    const int64_t i = e / dp, c = e % dp;
+    out[(int64_t)blockIdx.y * P * dp + e] = c < d ? (blockIdx.y ? b : a)[i * d + c] : (T)0.f;
+}
+
+int esize(int dtype) { return dtype == DDM_F32 ? 4 : 2; }
+
+struct Plan {
+    int dp, S;                       // padded components, pieces of a set's columns
+    bool direct;                     // backward writes da and db straight away
+    size_t rows, ml, hit, part, bytes;
+};
+
+// Some 512 row tiles of 128 and pieces: two directions make 1024 workgroups, four on each CU.
+Plan make_plan(int B, int P, int d, int dtype) {
+    Plan p{};
+    p.dp = d <= 32 ? 32 : d <= 64 ? 64 : 128;
+    const long long tiles = P / 128 + B;
+    p.S = (int)std::min<long long>(std::max<long long>(512 / tiles, 1), 16);
+    while (p.S > 1 && (long long)P / B / p.S < 64) p.S /= 2;     // a piece has a tile of columns on average
+    p.direct = p.S == 1 && d % 4 == 0;
+    size_t at = 0;
+    auto take = [&](size_t n) { const size_t o = at; at += (n + 255) / 256 * 256; return o; };
+    p.rows = take(2 * (size_t)P * p.dp * esize(dtype));
+    p.ml = take(2 * (size_t)p.S * P * sizeof(float2));
+    p.hit = take((size_t)P * 4);
+    p.part = take(p.direct ? 0 : 2 * (size_t)p.S * P * p.dp * 4);
+    p.bytes = std::max<size_t>(at, 256);
+    return p;
+}
+
+int check(int B, int P, int d, int dtype) {
+    if (dtype != DDM_F32 && dtype != DDM_F16 && dtype != DDM_BF16) return DDM_ERR_UNSUPPORTED;
+    if (d < 1 || d > DDM_MAX_D) return DDM_ERR_UNSUPPORTED;
+    if (B < 1 || B > (1 << 20) || P < 0 || P > (1 << 28)) return DDM_ERR_INVALID;
+    return DDM_OK;
+}
+bool off(const void *p, int e) { return !p || (uintptr_t)p % e; }
+
+template <class F>
+hipError_t with_type(int dtype, int dp, F f) {
+    auto go = [&](auto t) {
+        if (dp == 32) return f(t, std::integral_constant<int, 32>{});
+        if (dp == 64) return f(t, std::integral_constant<int, 64>{});
+        return f(t, std::integral_constant<int, 128>{});
+    };
+    if (dtype == DDM_F32) return go(float{});
+    if (dtype == DDM_F16) return go(_Float16{});
+    return go(__bf16{});
+}
+
+// Rows as the kernels read them: in place, or repacked.
+template <class T>
+hipError_t rows_for(LossArgs &p, const Plan &pl, unsigned char *ws, hipStream_t s) {
+    p.ld = p.w = p.d;
+    if (p.d * sizeof(T) % 16 == 0 && (uintptr_t)p.a % 16 == 0 && (uintptr_t)p.b % 16 == 0) return hipSuccess;
+    T *out = (T *)(ws + pl.rows);
+    const int64_t n = (int64_t)p.P * pl.dp;
+    hipLaunchKernelGGL((loss_repack_kernel<T>), dim3((unsigned)((n + 255) / 256), 2), dim3(256), 0, s, (const T *)p.a,
+                       (const T *)p.b, p.P, p.d, pl.dp, out);
+    p.a = out;
+    p.b = out + n;
+    p.ld = p.w = pl.dp;
+    return hipGetLastError();
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ddm_matching_loss_workspace_bytes(int B, int P, int d, int dtype) {
+    if (check(B, P, d, dtype) != DDM_OK) return 0;
+    return make_plan(B, P, d, dtype).bytes;
+}
+
+int ddm_matching_loss_forward(const void *a, const void *b, const int32_t *cu, int B, int P, int d, int dtype,
+                              double temperature, float *loss, float *lse_a, float *lse_b, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream) {
+    if (int rc = check(B, P, d, dtype)) return rc;
+    if (!(temperature > 0) || !std::isfinite(temperature) || (!cu && B != 1)) return DDM_ERR_INVALID;
+    if (P == 0) return DDM_OK;
+    if (off(a, esize(dtype)) || off(b, esize(dtype)) || off(loss, 4) || off(lse_a, 4) || off(lse_b, 4)) return DDM_ERR_INVALID;
+    const Plan pl = make_plan(B, P, d, dtype);
+    if (off(workspace, 16) || workspace_bytes < pl.bytes) return DDM_ERR_WORKSPACE;
+    unsigned char *ws = (unsigned char *)workspace;
+    LossArgs p{};
+    p.a = a; p.b = b; p.cu = cu; p.B = B; p.P = P; p.d = d; p.S = pl.S;
+    p.c = (float)(1.4426950408889634 / temperature); p.inv_t = (float)(1.0 / temperature);
+    p.ml = (float2 *)(ws + pl.ml); p.hit = (float *)(ws + pl.hit);
+    const hipError_t e = with_type(dtype, pl.dp, [&](auto t, auto dp) {
+        using T = decltype(t);
+        if (hipError_t r = rows_for<T>(p, pl, ws, stream)) return r;
+        hipLaunchKernelGGL((loss_fwd_kernel<T, decltype(dp)::value, 64>), dim3((unsigned)slot_count(B, P, 1, 128), pl.S, 2),
+                           dim3(256), 0, stream, p);
+        if (hipError_t r = hipGetLastError()) return r;
+        hipLaunchKernelGGL(loss_join_kernel, dim3((P + 255) / 256), dim3(256), 0, stream, p, loss, lse_a, lse_b);
+        return hipGetLastError();
+    });
+    return e == hipSuccess ? DDM_OK : DDM_ERR_HIP;
+}
+
+int ddm_matching_loss_backward(const float *dloss, const void *a, const void *b, const float *lse_a, const float *lse_b,
+                               const int32_t *cu, int B, int P, int d, int dtype, double temperature, void *da, void *db,
+                               void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (int rc = check(B, P, d, dtype)) return rc;
+    if (!(temperature > 0) || !std::isfinite(temperature) || (!cu && B != 1)) return DDM_ERR_INVALID;
+    if (P == 0) return DDM_OK;
+    const int es = esize(dtype);
+    if (off(a, es) || off(b, es) || off(dloss, 4) || off(lse_a, 4) || off(lse_b, 4) || off(da, es) || off(db, es))
+        return DDM_ERR_INVALID;
+    const Plan pl = make_plan(B, P, d, dtype);
+    if (off(workspace, 16) || workspace_bytes < pl.bytes) return DDM_ERR_WORKSPACE;
+    unsigned char *ws = (unsigned char *)workspace;
+    LossArgs p{};
+    p.a = a; p.b = b; p.cu = cu; p.B = B; p.P = P; p.d = d; p.S = pl.S;
+    p.c = (float)(1.4426950408889634 / temperature); p.inv_t = (float)(1.0 / temperature);
+    p.g = dloss; p.lse_a = lse_a; p.lse_b = lse_b; p.da = da; p.db = db;
+    const bool aligned = (uintptr_t)da % 16 == 0 && (uintptr_t)db % 16 == 0;
+    if (!pl.direct) p.part = (float *)(ws + pl.part);
+    else if (!aligned) return DDM_ERR_INVALID;
+    const hipError_t e = with_type(dtype, pl.dp, [&](auto t, auto dp) {
+        using T = decltype(t);
+        if (hipError_t r = rows_for<T>(p, pl, ws, stream)) return r;
+        hipLaunchKernelGGL((loss_bwd_kernel<T, decltype(dp)::value, 64>), dim3((unsigned)slot_count(B, P, 1, 128), pl.S, 2),
+                           dim3(256), 0, stream, p);
+        hipError_t r = hipGetLastError();
+        if (r == hipSuccess && p.part) {
+            const int64_t n = (int64_t)P * d;
+            hipLaunchKernelGGL((loss_sum_kernel<T>), dim3((unsigned)((n + 255) / 256), 2), dim3(256), 0, stream, p,
+                               decltype(dp)::value);
+            r = hipGetLastError();
+        }
+        return r;
+    });
+    return e == hipSuccess ? DDM_OK : DDM_ERR_HIP;
+}
+
+}  // extern "C"

@@ -301,6 +301,74 @@ int ddm_mutual_nn_ex(const void *D1, int H1, int W1, const void *D2, int H2, int
                      int32_t *out_count, int32_t *nn12, float *s12,
                      void *workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ---------------------------------------------- descriptor network ---
+ * Operators of the transformer that produces descriptor maps and of its training ("MASt3R" note on cv-learn.com, section
+ * 手法とアーキテクチャ: ViT encoder, cross-attention decoders, matching head, InfoNCE matching loss): attention, layer norm and
+ * the matching loss, each with its gradient. Conventions as above, and:
+ *  - Packed sets: sequences (sets of matches) of different lengths lie one after another along the first axis; cu is device
+ *    int32[B + 1], non-decreasing, sequence b = [cu[b], cu[b+1]). NULL cu means one sequence of everything (B = 1). Contents
+ *    of cu outside [0, T] are clamped, so no value leads outside a tensor. Values of elements inside a sequence must be
+ *    finite; elements outside every sequence influence nothing (their own outputs are written, as zeros).
+ *  - 16-byte aligned pointers unless a function says otherwise. Statistics, sums and gradients' accumulators are fp32;
+ *    outputs are rounded once, to nearest even. No atomics: results do not depend on the order of workgroups.
+ *  - Nothing is kept between calls; the calls launch kernels on `stream` only and can be captured into a HIP graph. */
+
+/* Attention over packed sequences. Query head h uses key head h / (Hq / Hkv).
+ *   z_ij = scale q_i.k_j,  lse_i = log sum_j exp z_ij,  out_i = sum_j exp(z_ij - lse_i) v_j
+ * over the keys j of query i's sequence; with causal = 1 over j <= i + Lk - Lq (positions in the sequence, so that the last
+ * query sees every key). A query that sees no key gets out = 0, lse = -inf and gives no gradient.
+ *   q            [Tq][Hq][D], row (t, h) at q + (t * q_ts + h * q_hs) elements, D elements contiguous; k, v [Tk][Hkv][D] and
+ *                dout [Tq][Hq][D] likewise; strides non-negative, whole 16-byte pieces, below 16 MB
+ *   out, dq, dk, dv  contiguous, in the inputs' type;  lse  float [Tq][Hq]
+ *   D            1..DDM_MAX_D with D * element size a multiple of 16 (else DDM_ERR_UNSUPPORTED)
+ *   scale        > 0
+ * With few query rows and long sequences the keys are split over workgroups and joined (the workspace holds the parts).
+ * Products take the inputs' type with fp32 accumulation; probabilities and their gradients are rounded to that type before
+ * the second product. The workspace of backward is scratch: forward keeps only out and lse. */
+size_t ddm_attention_forward_workspace_bytes(int B, int Tq, int Tk, int Hq, int Hkv, int D, int dtype);
+int ddm_attention_forward(const void *q, int64_t q_ts, int64_t q_hs, const void *k, int64_t k_ts, int64_t k_hs,
+                          const void *v, int64_t v_ts, int64_t v_hs, const int32_t *cu_q, const int32_t *cu_k, int B,
+                          int Tq, int Tk, int Hq, int Hkv, int D, int dtype, int causal, double scale, void *out,
+                          float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream);
+size_t ddm_attention_backward_workspace_bytes(int B, int Tq, int Tk, int Hq, int Hkv, int D, int dtype);
+int ddm_attention_backward(const void *dout, int64_t g_ts, int64_t g_hs, const void *q, int64_t q_ts, int64_t q_hs,
+                           const void *k, int64_t k_ts, int64_t k_hs, const void *v, int64_t v_ts, int64_t v_hs,
+                           const void *out, const float *lse, const int32_t *cu_q, const int32_t *cu_k, int B, int Tq,
+                           int Tk, int Hq, int Hkv, int D, int dtype, int causal, double scale, void *dq, void *dk,
+                           void *dv, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Layer norm over the last axis of [N][C]:  xh = (x - mean) rstd,  rstd = (var + eps)^-1/2,  y = xh weight + bias.
+ *   x, y, dy, dx  in dtype, x with row stride ldx >= C elements, the others contiguous; any alignment of whole elements
+ *   weight, bias, dweight, dbias  [C] in wtype (DDM_F32 or dtype); weight and bias may be NULL (1 and 0)
+ *   mean, rstd    float [N]
+ *   dx = rstd (u - mean(u) - xh mean(u xh)) with u = dy weight;  dweight = sum over rows of dy xh;  dbias = sum of dy;
+ *   each of dx, dweight, dbias may be NULL when it is not wanted.
+ * 1 <= C <= DDM_MAX_NORM_C, N >= 0 (N = 0: dweight and dbias are zeros), N < 2^31, eps >= 0. */
+#define DDM_MAX_NORM_C 8192
+int ddm_layer_norm_forward(const void *x, int64_t ldx, const void *weight, const void *bias, int64_t N, int C, int dtype,
+                           int wtype, double eps, void *y, float *mean, float *rstd, hipStream_t stream);
+size_t ddm_layer_norm_backward_workspace_bytes(int64_t N, int C, int dtype);
+int ddm_layer_norm_backward(const void *dy, const void *x, int64_t ldx, const void *weight, const float *mean,
+                            const float *rstd, int64_t N, int C, int dtype, int wtype, void *dx, void *dweight,
+                            void *dbias, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Matching loss (InfoNCE in both directions) of packed sets of matches: row p of a [P][d] and row p of b [P][d] are the
+ * descriptors of match p; within a set, z_ij = a_i.b_j / temperature and
+ *   loss_i = (lse_a_i + lse_b_i) / 2 - z_ii,  lse_a_i = log sum_j exp z_ij,  lse_b_j = log sum_i exp z_ij
+ *   dz_ij = (g_i exp(z_ij - lse_a_i) + g_j exp(z_ij - lse_b_j)) / 2 - g_i [i = j]
+ *   da_i = sum_j dz_ij b_j / temperature,  db_j = sum_i dz_ij a_i / temperature
+ * where g = dloss (float [P]) is the gradient by the losses (float [P]). The score matrix is never stored.
+ *   1 <= d <= DDM_MAX_D; contiguous rows; a and b at any whole element, da and db 16-byte aligned; temperature > 0;
+ *   0 <= P <= 2^28.
+ * Rows outside every set: loss and lse 0, gradients 0. */
+size_t ddm_matching_loss_workspace_bytes(int B, int P, int d, int dtype);
+int ddm_matching_loss_forward(const void *a, const void *b, const int32_t *cu, int B, int P, int d, int dtype,
+                              double temperature, float *loss, float *lse_a, float *lse_b, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+int ddm_matching_loss_backward(const float *dloss, const void *a, const void *b, const float *lse_a, const float *lse_b,
+                               const int32_t *cu, int B, int P, int d, int dtype, double temperature, void *da, void *db,
+                               void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* ------------------------------------------------------- kernel timing ---
  * Benchmark aid, off by default. ddm_profile_enable(mask) makes later calls
  * bracket each fused NN sweep launch with two HIP events on the call's stream:
