@@ -26,8 +26,8 @@ struct LossArgs {
     const int32_t *cu;
     int B, P, d, w, ld, S;
     float c, inv_t;                  // c = log2(e) / t
-    float2 *ml;                      // forward: [2][S][P] running maximum (times c) and sum
-    float *hit;                      // forward: c z_ii t
+    float2 *ml;                      // forward: [2][S][P] largest a_i.b_j and the sum of exponentials about it
+    float *hit;                      // forward: a_i.b_i
     const float *g, *lse_a, *lse_b;  // backward
     void *da, *db;
     float *part;                     // backward: [2][S][P][DP], or null: written straight to da, db
@@ -98,13 +98,18 @@ __global__ __launch_bounds__(256, 2) void loss_fwd_kernel(LossArgs p) {
         for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) mx = fmaxf(mx, z[b][r]);
-        const float next_m = fmaxf(m, half_max(mx) * p.c);
+        const float next_m = fmaxf(m, half_max(mx)), ref = next_m * p.c;
         float sum = 0.f;
 #pragma unroll
         for (int b = 0; b < KB; ++b)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) sum += exp2_fast(__builtin_fmaf(z[b][r], p.c, -next_m));
-        l = __builtin_fmaf(l, exp2_fast(m - next_m), sum);
+            for (int r = 0; r < 16; ++r) {
+                // with the match among them the largest score counts as exactly 1; elsewhere ref's rounding is a common factor
+                // of 1 + 2^-20 at most on what is added, and saves an instruction a score
+                if constexpr (decltype(special)::value) sum += exp2_fast((z[b][r] - next_m) * p.c);
+                else sum += exp2_fast(__builtin_fmaf(z[b][r], p.c, -ref));
+            }
+        l = __builtin_fmaf(l, exp2_fast((m - next_m) * p.c), sum);
         m = next_m;
     };
     if (t_end > 0) {
@@ -123,7 +128,7 @@ __global__ __launch_bounds__(256, 2) void loss_fwd_kernel(LossArgs p) {
     if (!in || h) return;
     p.ml[((int64_t)dir * p.S + blockIdx.y) * p.P + span.lo + row] = make_float2(m, l);
     if (dir == 0) {
-        if (row >= from && row < to) p.hit[span.lo + row] = hit * p.c;
+        if (row >= from && row < to) p.hit[span.lo + row] = hit;
     }
 }
 
@@ -138,16 +143,16 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs p, float *loss,
         for (int s = 0; s < p.S; ++s) m = fmaxf(m, ml[(int64_t)s * p.P].x);
         for (int s = 0; s < p.S; ++s) {
             const float2 v = ml[(int64_t)s * p.P];
-            if (v.y > 0.f) l += v.y * exp2_fast(v.x - m);
+            if (v.y > 0.f) l += v.y * exp2_fast((v.x - m) * p.c);
         }
         any = l > 0.f;
         top[dir] = m;
         log_sum[dir] = __builtin_amdgcn_logf(l);
     }
     const float hit = p.hit[i];
-    lse_a[i] = any ? (top[0] + log_sum[0]) * LN2 : 0.f;
-    lse_b[i] = any ? (top[1] + log_sum[1]) * LN2 : 0.f;
-    loss[i] = any ? (((top[0] - hit) + (top[1] - hit)) + (log_sum[0] + log_sum[1])) * (0.5f * LN2) : 0.f;
+    lse_a[i] = any ? __builtin_fmaf(top[0], p.inv_t, log_sum[0] * LN2) : 0.f;
+    lse_b[i] = any ? __builtin_fmaf(top[1], p.inv_t, log_sum[1] * LN2) : 0.f;
+    loss[i] = any ? 0.5f * __builtin_fmaf((top[0] - hit) + (top[1] - hit), p.inv_t, (log_sum[0] + log_sum[1]) * LN2) : 0.f;
 }
 
 // Backward, one direction: dx of the rows, the gradient by the scores made tile by tile. fp16 holds it to few bits below 2^-14,

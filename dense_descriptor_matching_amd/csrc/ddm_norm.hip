@@ -25,7 +25,7 @@ struct NormArgs {
     float *mean, *rstd, *part;       // part: [workgroup][2][C]
     int64_t ldx, N;
     int C;
-    float eps, inv_c;
+    float eps;
 };
 
 // Sum over the 64 lanes, in every lane: DPP exchanges within 16 lanes, then the swaps of rows and halves.
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs p) {
 #pragma unroll
             for (int e = 0; e < VE; ++e) sum += x[j][e];
         }
-        const float mean = team_sum<TEAM>(sum, scratch, turn) * p.inv_c;
+        const float mean = team_sum<TEAM>(sum, scratch, turn) / (float)p.C;
         sum = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j)
@@ -116,7 +116,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs p) {
                 x[j][e] = (j * TEAM + t) * VE + e < p.C ? x[j][e] - mean : 0.f;
                 sum = __builtin_fmaf(x[j][e], x[j][e], sum);
             }
-        const float rstd = 1.f / sqrtf(team_sum<TEAM>(sum, scratch, turn) * p.inv_c + p.eps);
+        const float rstd = 1.f / sqrtf(team_sum<TEAM>(sum, scratch, turn) / (float)p.C + p.eps);
         T *out = (T *)p.y + n * p.C;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -166,8 +166,8 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormArgs p) {
                 s2 = __builtin_fmaf(g[j][e], x[j][e], s2);
             }
         if (!p.dx) continue;
-        s1 = team_sum<TEAM>(s1, scratch, turn) * p.inv_c;
-        s2 = team_sum<TEAM>(s2, scratch, turn) * p.inv_c;
+        s1 = team_sum<TEAM>(s1, scratch, turn) / (float)p.C;
+        s2 = team_sum<TEAM>(s2, scratch, turn) / (float)p.C;
         T *out = (T *)p.dx + n * p.C;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -281,7 +281,7 @@ int ddm_layer_norm_forward(const void *x, int64_t ldx, const void *weight, const
         return DDM_ERR_INVALID;
     NormArgs a{};
     a.x = x; a.w = weight; a.b = bias; a.y = y; a.mean = mean; a.rstd = rstd;
-    a.ldx = ldx; a.N = N; a.C = C; a.eps = (float)eps; a.inv_c = (float)(1.0 / C);
+    a.ldx = ldx; a.N = N; a.C = C; a.eps = (float)eps;
     const Shape s = shape_of(C, dtype);
     const int teams = 256 / s.team;
     const unsigned grid = (unsigned)std::min<int64_t>((N + teams - 1) / teams, 2048);
@@ -314,7 +314,7 @@ int ddm_layer_norm_backward(const void *dy, const void *x, int64_t ldx, const vo
         return DDM_ERR_WORKSPACE;
     NormArgs a{};
     a.x = x; a.dy = dy; a.w = weight; a.dx = dx; a.mean = const_cast<float *>(mean); a.rstd = const_cast<float *>(rstd);
-    a.part = (float *)workspace; a.ldx = ldx; a.N = N; a.C = C; a.inv_c = (float)(1.0 / C);
+    a.part = (float *)workspace; a.ldx = ldx; a.N = N; a.C = C;
     const Shape s = shape_of(C, dtype);
     const int groups = bwd_groups(N, C, dtype);
     if (N && (dx || params)) {
