@@ -34,7 +34,7 @@ Plan make_plan(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int D) {
     if (p.split) {
         // some 2048 workgroups of one wave over all keys, in whole tiles of 64 keys
         const long long avg = ((long long)Tk * Hkv + 2047) / 2048;
-        p.chunk = (int)std::min<long long>(std::max<long long>((avg + 63) / 64 * 64, 64), 4096);
+        p.chunk = (int)std::max<long long>((avg + 63) / 64 * 64, 64);
         const long long mean = (rows + B - 1) / B;
         p.cap = (int)std::min<long long>((2 * mean + SPLIT_ROWS - 1) / SPLIT_ROWS * SPLIT_ROWS, 4 * SPLIT_ROWS);
         if (mean <= SPLIT_ROWS / 2) p.cap = SPLIT_ROWS;
@@ -49,7 +49,7 @@ int check(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int D) {
     if (B < 1 || Tq < 0 || Tk < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv) return DDM_ERR_INVALID;
     if (D < 1 || D > DDM_MAX_D || D * esize(dtype) % 16) return DDM_ERR_UNSUPPORTED;
     const long long G = Hq / Hkv;
-    if (B > (1 << 20) || (long long)Tq * G * G >= (1ll << 31) || Tk >= INT_MAX - (1 << 22)) return DDM_ERR_INVALID;
+    if ((long long)Tq * Hq >= INT_MAX || B > (1 << 20) || (long long)Tq * G * G >= (1ll << 31) || Tk >= INT_MAX - (1 << 22)) return DDM_ERR_INVALID;
     if (((long long)Tq * G / 32 + B + 2) * Hkv >= INT_MAX || ((long long)Tk / 32 + B + 2) * Hkv >= INT_MAX)
         return DDM_ERR_INVALID;
     return DDM_OK;
@@ -68,13 +68,12 @@ hipError_t forward(const AttnArgs &a, const Plan &pl, hipStream_t s) {
     const int G = a.group.g;
     constexpr bool wide = sizeof(T) == 2;
     if (pl.split) {
-        constexpr int BN = wide ? 64 : 32;
+        constexpr int BN = 32;
         const long long slots = slot_count(a.B, a.Tk, 1, pl.chunk);
         hipLaunchKernelGGL((attn_fwd_kernel<T, D, 1, 1, BN, true>), dim3((unsigned)(slots * a.Hkv), pl.cap / SPLIT_ROWS),
                            dim3(64), 0, s, a);
         if (hipError_t e = hipGetLastError()) return e;
-        const long long ids = (long long)a.Tq * a.Hq;
-        hipLaunchKernelGGL((attn_join_kernel<T>), dim3((unsigned)((ids + 3) / 4)), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((unsigned)((long long)a.Tq * a.Hq)), dim3(256), 0, s, a);
         return hipGetLastError();
     }
     constexpr int BN = wide ? 64 : 32, NR = wide && D <= 64 ? 2 : 1;
@@ -99,8 +98,9 @@ hipError_t backward(const AttnArgs &a, hipStream_t s) {
         if (hipError_t e = hipGetLastError()) return e;
     }
     if (a.Tk) {
-        const long long n = slot_count(a.B, a.Tk, 1, 128 * NR) * a.Hkv;
-        hipLaunchKernelGGL((attn_dkv_kernel<T, D, 4, NR, BN>), dim3((unsigned)n), dim3(256), 0, s, a);
+        constexpr int KG = wide && D == 128 ? 2 : 4, RG = wide && D == 128 ? 4 : wide ? 2 : 1;
+        const long long n = slot_count(a.B, a.Tk, 1, 32 * KG) * a.Hkv;
+        hipLaunchKernelGGL((attn_dkv_kernel<T, D, KG, RG, 1>), dim3((unsigned)n), dim3(KG * RG * 64), 0, s, a);
     }
     return hipGetLastError();
 }

@@ -166,7 +166,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_fwd_kernel(AttnArgs p) {
             In::load(buffer_of(kb + (int64_t)j0 * p.k_ts, rows_bytes<T>(left, p.k_ts, p.D)), koff, to, w);
             In::load(buffer_of(vb + (int64_t)j0 * p.v_ts, rows_bytes<T>(left, p.v_ts, p.D)), voff, to + TILE_BYTES, w);
         };
-        auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, auto masked) {
+        auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, bool masked) {
             if (t + 1 < t_end) fetch(t + 1, next);
             if (k_from + t * BN >= wave_top) return;
             const unsigned char *kt = cur, *vt = cur + TILE_BYTES;
@@ -184,7 +184,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_fwd_kernel(AttnArgs p) {
             }
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
-                if constexpr (decltype(masked)::value) {
+                if (masked) {
                     const int j0 = k_from + t * BN + 4 * h;
 #pragma unroll
                     for (int b = 0; b < KB; ++b)
@@ -241,8 +241,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_fwd_kernel(AttnArgs p) {
             tiles_ready();
             const int t_full = max(0, min(t_end, (low - k_from) / BN));      // tiles that every row sees whole
             for (int t = 0; t < t_end; ++t) {
-                if (t < t_full) step(t, lds[t & 1], lds[(t + 1) & 1], std::integral_constant<bool, false>{});
-                else step(t, lds[t & 1], lds[(t + 1) & 1], std::integral_constant<bool, true>{});
+                step(t, lds[t & 1], lds[(t + 1) & 1], t >= t_full);
                 tiles_ready();
             }
         }
@@ -292,13 +291,14 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_fwd_kernel(AttnArgs p) {
     }
 }
 
-// Joins the chunks of the split form: one wave for each (query, head). 4-byte reads of D floats a chunk.
-template <class T>
+// Joins the chunks of the split form: a workgroup for each (query, head). Every chunk's weight first, one thread each; then DP
+// threads a chunk add up its row, 256 / DP chunks at a time, eight loads in flight a thread.
+constexpr int MAX_CHUNKS = 2064;          // of one sequence; the plan's chunks are at least 2048th parts of all keys
+template <class T, int DP>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
-    const int lane = threadIdx.x & 63;
-    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (id >= (int64_t)p.Tq * p.Hq) return;
-    const int tok = __builtin_amdgcn_readfirstlane((int)(id / p.Hq)), head = (int)(id % p.Hq);
+    __shared__ float weight[MAX_CHUNKS], red[2][4], rows[256 / DP][DP];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int tok = blockIdx.x / p.Hq, head = blockIdx.x % p.Hq;
     int sq = -1;                                                // the last sequence that begins at or before the token
     for (int base = 0; base < p.B + 2; base += 64) {
         const int x = base + lane;
@@ -312,28 +312,46 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
     if (sq == 0 || sq == p.B + 1) k.hi = k.lo;
     const int G = p.group.g, hk = head / G, r = (tok - q.lo) * G + head % G;
     const int chunks = (k.hi - k.lo + p.chunk - 1) / p.chunk;
-    T *orow = (T *)p.out + id * p.D;
     if (chunks > 0 && r >= p.cap) return;                       // written whole
     const int slot0 = k.lo / p.chunk + sq;
     const float *part = p.part + (((int64_t)slot0 * p.Hkv + hk) * p.cap + r) * (p.D + 4);
     const int64_t pitch = (int64_t)p.Hkv * p.cap * (p.D + 4);
     float top = -INFINITY;
-    for (int c = lane; c < chunks; c += 64) top = fmaxf(top, part[c * pitch]);
+    for (int c = tid; c < chunks; c += 256) {
+        weight[c] = part[c * pitch];
+        top = fmaxf(top, weight[c]);
+    }
 #pragma unroll
     for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
-    float sum = 0.f, a0 = 0.f, a1 = 0.f;
+    if (lane == 0) red[0][tid >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
     const float ref = top == -INFINITY ? 0.f : top;
-    for (int c = 0; c < chunks; ++c) {
-        const float *pc = part + c * pitch;
-        const float f = exp2_fast(pc[0] - ref);
-        sum += f * pc[1];
-        if (lane < p.D) a0 += f * pc[4 + lane];
-        if (lane + 64 < p.D) a1 += f * pc[4 + 64 + lane];
+    float sum = 0.f;
+    for (int c = tid; c < chunks; c += 256) {
+        const float f = exp2_fast(weight[c] - ref);
+        weight[c] = f;
+        sum = __builtin_fmaf(f, part[c * pitch + 1], sum);
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    if (lane < p.D) orow[lane] = (T)(a0 * inv);
-    if (lane + 64 < p.D) orow[lane + 64] = (T)(a1 * inv);
-    if (lane == 0) p.lse[id] = sum > 0.f ? (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f : -INFINITY;
+#pragma unroll
+    for (int x = 32; x; x >>= 1) sum += __shfl_xor(sum, x);
+    if (lane == 0) red[1][tid >> 6] = sum;
+    __syncthreads();
+    sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    const int col = tid % DP, g = tid / DP;
+    float a = 0.f;
+    if (col < p.D) {
+#pragma unroll 8
+        for (int c = g; c < chunks; c += 256 / DP) a = __builtin_fmaf(weight[c], part[c * pitch + 4 + col], a);
+    }
+    rows[g][col] = a;
+    __syncthreads();
+    if (g == 0 && col < p.D) {
+#pragma unroll
+        for (int x = 1; x < 256 / DP; ++x) a += rows[x][col];
+        ((T *)p.out)[(int64_t)blockIdx.x * p.D + col] = (T)(sum > 0.f ? a / sum : 0.f);
+        if (col == 0) p.lse[blockIdx.x] = sum > 0.f ? (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f : -INFINITY;
+    }
 }
 
 // -------------------------------------------------------------------------------------------------------- backward
@@ -438,11 +456,11 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dq_kernel(AttnArgs p) {
         In::load(buffer_of(kb + (int64_t)j0 * p.k_ts, rows_bytes<T>(left, p.k_ts, p.D)), koff, to, w);
         In::load(buffer_of(vb + (int64_t)j0 * p.v_ts, rows_bytes<T>(left, p.v_ts, p.D)), voff, to + TILE_BYTES, w);
     };
-    auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, auto masked) {
+    auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, bool masked) {
         if (t + 1 < t_end) fetch(t + 1, next);
         if (t * BN >= wave_top) return;
         const unsigned char *kt = cur, *vt = cur + TILE_BYTES;
-#pragma unroll 1
+#pragma unroll
         for (int b = 0; b < BN / 32; ++b) {
             f32x16 z[NR], y[NR];
 #pragma unroll
@@ -463,10 +481,15 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dq_kernel(AttnArgs p) {
                     const float pr = exp2_fast(__builtin_fmaf(z[i][r], p.c, -lse[i]));
                     float ds = pr * (y[i][r] - delta[i]);
                     if constexpr (scaled_ds<T>) ds *= inv[i];
-                    if constexpr (decltype(masked)::value)
-                        if (t * BN + 32 * b + 4 * h + 8 * (r / 4) + r % 4 >= lim[i]) ds = 0.f;
                     z[i][r] = ds;
                 }
+            if (masked) {
+#pragma unroll
+                for (int i = 0; i < NR; ++i)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        if (t * BN + 32 * b + 4 * h + 8 * (r / 4) + r % 4 >= lim[i]) z[i][r] = 0.f;
+            }
 #pragma unroll
             for (int kc = 0; kc < 2; ++kc) {
                 Frag<T> sf[NR];
@@ -491,8 +514,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dq_kernel(AttnArgs p) {
         tiles_ready();
         const int t_full = max(0, min(t_end, low / BN));
         for (int t = 0; t < t_end; ++t) {
-            if (t < t_full) step(t, lds[t & 1], lds[(t + 1) & 1], std::integral_constant<bool, false>{});
-            else step(t, lds[t & 1], lds[(t + 1) & 1], std::integral_constant<bool, true>{});
+            step(t, lds[t & 1], lds[(t + 1) & 1], t >= t_full);
             tiles_ready();
         }
     }
@@ -512,21 +534,25 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dq_kernel(AttnArgs p) {
     }
 }
 
-// dk and dv: a workgroup keeps 32 NW NR keys (K and V rows as operands in registers) and walks over the rows of the key
-// head's whole group in tiles of BQ, Q and dO in LDS. S = Q K^T and dO V^T come out with the keys as columns, so P and dS feed
-// the products with dO and Q (read as columns) without leaving their lanes.
-template <class T, int D, int NW, int NR, int BQ>
-__global__ __launch_bounds__(NW * 64, D == 128 ? 1 : 2) void attn_dkv_kernel(AttnArgs p) {
+// dk and dv: a workgroup keeps 32 KG NR keys (K and V rows as operands in registers) and walks over the rows of the key
+// head's whole group in tiles of BQ = 32 RG, Q and dO in LDS. S = Q K^T and dO V^T come out with the keys as columns, so P and
+// dS feed the products with dO and Q (read as columns) without leaving their lanes. Of its KG RG waves, KG share out the keys and
+// RG the rows of each tile; the RG shares of dk and dv are added through LDS, in order, when the rows are done.
+template <class T, int D, int KG, int RG, int NR>
+__global__ __launch_bounds__(KG * RG * 64, KG * RG > 4 ? 1 : sizeof(T) == 4 && D == 128 ? 1 : 2) void attn_dkv_kernel(AttnArgs p) {
     using TL = Tile<T, D>;
-    constexpr int BK = NW * NR * 32, DC = D / 16, DB = D / 32;
+    constexpr int NW = KG * RG, BK = KG * NR * 32, BQ = RG * 32, DC = D / 16, DB = D / 32;
     constexpr int TILE_BYTES = BQ * TL::ROW;
-    static_assert(BQ <= 64, "a wave loads a tile's statistics");
+    static_assert(BQ <= NW * 64 && BQ % 32 == 0, "a thread loads a row's statistics");
     __shared__ __attribute__((aligned(16))) unsigned char lds[2][2 * TILE_BYTES];
+    // 128 16-bit components: with V in registers too, the accumulators would be spilled
+    constexpr bool V_LDS = D == 128 && sizeof(T) == 2;
+    __shared__ __attribute__((aligned(16))) unsigned char v_lds[V_LDS ? BK * TL::ROW : 16];
     __shared__ __attribute__((aligned(16))) float st_lse[2][BQ], st_delta[2][BQ];
     __shared__ __attribute__((aligned(16))) int st_lim[2][BQ];
-    __shared__ float st_exp[2];
+    __shared__ float st_exp[2][RG];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int h = lane >> 5, n = lane & 31;
+    const int h = lane >> 5, n = lane & 31, kg = w % KG, rg = w / KG;
     const int G = p.group.g;
 
     const int heads = p.Hkv, x = blockIdx.x % heads;
@@ -540,11 +566,11 @@ __global__ __launch_bounds__(NW * 64, D == 128 ? 1 : 2) void attn_dkv_kernel(Att
     if (j0 >= Lk) return;
     const int j_end = min(j0 + BK, Lk);
 
-    Frag<T> kf[NR][DC], vf[NR][DC];
+    Frag<T> kf[NR][DC], vf[NR][V_LDS ? 1 : DC];
     int key[NR];
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-        key[i] = j0 + (w * NR + i) * 32 + n;
+        key[i] = j0 + (kg * NR + i) * 32 + n;
         const bool in = key[i] < Lk;
         const int64_t tok = sk.lo + (in ? key[i] : Lk - 1);
         const T *kr = (const T *)p.k + tok * p.k_ts + (int64_t)hk * p.k_hs;
@@ -552,12 +578,12 @@ __global__ __launch_bounds__(NW * 64, D == 128 ? 1 : 2) void attn_dkv_kernel(Att
 #pragma unroll
         for (int c = 0; c < DC; ++c) {
             kf[i][c] = global_rows<T>(kr, 16 * c + 8 * h, p.D, in);
-            vf[i][c] = global_rows<T>(vr, 16 * c + 8 * h, p.D, in);
+            if constexpr (!V_LDS) vf[i][c] = global_rows<T>(vr, 16 * c + 8 * h, p.D, in);
         }
     }
     const int first = p.causal ? min(rows, max(0, j0 - shift) * G) : 0;     // earlier rows see none of these keys
     const int t_end = (rows - first + BQ - 1) / BQ;
-    const int wave_key = j0 + w * NR * 32;
+    const int wave_key = j0 + kg * NR * 32;
 
     f32x16 dk[NR][DB], dv[NR][DB];
 #pragma unroll
@@ -604,22 +630,22 @@ __global__ __launch_bounds__(NW * 64, D == 128 ? 1 : 2) void attn_dkv_kernel(Att
             st_lim[b][tid] = s_lim;
         }
         if constexpr (scaled_ds<T>) {
-            if (tid < 64) {
-                float e = tid < BQ ? s_exp : NO_EXPONENT;
+            if (tid < BQ) {                                    // one value for the 32 rows of a wave's step
+                float e = s_exp;
 #pragma unroll
-                for (int d = 32; d; d >>= 1) e = fmaxf(e, __shfl_xor(e, d));
-                if (tid == 0) st_exp[b] = e;
+                for (int d = 16; d; d >>= 1) e = fmaxf(e, __shfl_xor(e, d));
+                if (tid % 32 == 0) st_exp[b][tid / 32] = e;
             }
         }
     };
-    auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, bool busy, auto masked) {
+    auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, bool busy, bool masked) {
         if (t + 1 < t_end) fetch(t + 1, next);
         if (!busy) return;
         const int buf = t & 1;
         const unsigned char *qt = cur, *gt = cur + TILE_BYTES;
         float inv = 1.f;
         if constexpr (scaled_ds<T>) {
-            const float e = st_exp[buf];
+            const float e = st_exp[buf][rg];
             if (e > ref) {
                 const float f = exp2_fast(ref - e);
 #pragma unroll
@@ -630,79 +656,135 @@ __global__ __launch_bounds__(NW * 64, D == 128 ? 1 : 2) void attn_dkv_kernel(Att
             }
             inv = exp2_fast(-ref);
         }
-#pragma unroll 1
-        for (int b = 0; b < BQ / 32; ++b) {
-            f32x16 z[NR], y[NR];
+        f32x16 z[NR], y[NR];
 #pragma unroll
-            for (int i = 0; i < NR; ++i) { z[i] = 0.f; y[i] = 0.f; }
+        for (int i = 0; i < NR; ++i) { z[i] = 0.f; y[i] = 0.f; }
 #pragma unroll
-            for (int c = 0; c < DC; ++c) {
-                const Frag<T> qf = TL::rows(qt, row_at, 32 * b, c), gf = TL::rows(gt, row_at, 32 * b, c);
+        for (int c = 0; c < DC; ++c) {
+            const Frag<T> qf = TL::rows(qt, row_at, 32 * rg, c), gf = TL::rows(gt, row_at, 32 * rg, c);
 #pragma unroll
-                for (int i = 0; i < NR; ++i) {
-                    mma(z[i], qf, kf[i][c]);
-                    mma(y[i], gf, vf[i][c]);
-                }
+            for (int i = 0; i < NR; ++i) {
+                mma(z[i], qf, kf[i][c]);
+                if constexpr (V_LDS) mma(y[i], gf, TL::rows(v_lds, row_at, 32 * (kg * NR + i), c));
+                else mma(y[i], gf, vf[i][c]);
             }
+        }
+        if (masked) {
 #pragma unroll
-            for (int r4 = 0; r4 < 4; ++r4) {
-                const int r0 = 32 * b + 8 * r4 + 4 * h;
-                const f32x4 ls = *reinterpret_cast<const f32x4 *>(&st_lse[buf][r0]);
-                const f32x4 de = *reinterpret_cast<const f32x4 *>(&st_delta[buf][r0]);
+            for (int r = 0; r < 16; ++r) {
+                const int lim = st_lim[buf][32 * rg + 8 * (r / 4) + 4 * h + r % 4];
 #pragma unroll
                 for (int i = 0; i < NR; ++i)
+                    if (key[i] >= lim) z[i][r] = -INFINITY;
+            }
+        }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int r = 4 * r4 + e;
-                        float pr = exp2_fast(__builtin_fmaf(z[i][r], p.c, -ls[e]));
-                        if constexpr (decltype(masked)::value) pr = key[i] < st_lim[buf][r0 + e] ? pr : 0.f;
-                        z[i][r] = pr;
-                        y[i][r] = pr * (y[i][r] - de[e]);
-                        if constexpr (scaled_ds<T>) y[i][r] *= inv;
-                    }
+        for (int r4 = 0; r4 < 4; ++r4) {
+            const int r0 = 32 * rg + 8 * r4 + 4 * h;
+            const f32x4 ls = *reinterpret_cast<const f32x4 *>(&st_lse[buf][r0]);
+            const f32x4 de = *reinterpret_cast<const f32x4 *>(&st_delta[buf][r0]);
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = 4 * r4 + e;
+                    const float pr = exp2_fast(__builtin_fmaf(z[i][r], p.c, -ls[e]));
+                    z[i][r] = pr;
+                    y[i][r] = pr * (y[i][r] - de[e]);
+                    if constexpr (scaled_ds<T>) y[i][r] *= inv;
+                }
+        }
+        if constexpr (D == 128) __builtin_amdgcn_sched_barrier(0);   // loads hoisted further up would not fit the registers
+#pragma unroll
+        for (int kc = 0; kc < 2; ++kc) {
+            Frag<T> pf[NR], sf[NR];
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                float a[8], c[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) { a[e] = z[i][kc * 8 + e]; c[e] = y[i][kc * 8 + e]; }
+                pf[i] = to_frag<T>(a);
+                sf[i] = to_frag<T>(c);
             }
 #pragma unroll
-            for (int kc = 0; kc < 2; ++kc) {
-                Frag<T> pf[NR], sf[NR];
+            for (int d = 0; d < DB; ++d) {
+                const Frag<T> gf = TL::cols(gt, col_at, 32 * rg + 16 * kc, 32 * d);
+                const Frag<T> qf = TL::cols(qt, col_at, 32 * rg + 16 * kc, 32 * d);
 #pragma unroll
                 for (int i = 0; i < NR; ++i) {
-                    float a[8], c[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) { a[e] = z[i][kc * 8 + e]; c[e] = y[i][kc * 8 + e]; }
-                    pf[i] = to_frag<T>(a);
-                    sf[i] = to_frag<T>(c);
-                }
-#pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    const Frag<T> gf = TL::cols(gt, col_at, 32 * b + 16 * kc, 32 * d);
-                    const Frag<T> qf = TL::cols(qt, col_at, 32 * b + 16 * kc, 32 * d);
-#pragma unroll
-                    for (int i = 0; i < NR; ++i) {
-                        mma(dv[i][d], gf, pf[i]);
-                        mma(dk[i][d], qf, sf[i]);
-                    }
+                    mma(dv[i][d], gf, pf[i]);
+                    mma(dk[i][d], qf, sf[i]);
                 }
             }
         }
     };
     if (t_end > 0) {
+        if constexpr (V_LDS) {
+            using Iv = Dma<T, D, NW, BK>;
+            int off[Iv::N];
+#pragma unroll
+            for (int i = 0; i < Iv::N; ++i) off[i] = Iv::offset(i, w, lane, p.v_ts, p.D);
+            Iv::load(buffer_of((const T *)p.v + (int64_t)(sk.lo + j0) * p.v_ts + (int64_t)hk * p.v_hs,
+                               rows_bytes<T>(j_end - j0, p.v_ts, p.D)), off, v_lds, w);
+        }
         fetch(0, lds[0]);
         put_stats(0);
         tiles_ready();
         for (int t = 0; t < t_end; ++t) {
             const int r0 = first + t * BQ;
             bool busy = wave_key < Lk, full = true;
+            const int w0 = r0 + 32 * rg;                        // this wave's rows of the tile
+            busy = busy && w0 < rows;
             if (p.causal) {
-                busy = busy && wave_key < (int)div_by(min(r0 + BQ, rows) - 1, p.group) + shift + 1;
-                full = j_end <= (int)div_by(r0, p.group) + shift + 1;
+                busy = busy && wave_key < (int)div_by(min(w0 + 32, rows) - 1, p.group) + shift + 1;
+                full = j_end <= (int)div_by(w0, p.group) + shift + 1;
             }
-            if (full) step(t, lds[t & 1], lds[(t + 1) & 1], busy, std::integral_constant<bool, false>{});
-            else step(t, lds[t & 1], lds[(t + 1) & 1], busy, std::integral_constant<bool, true>{});
+            step(t, lds[t & 1], lds[(t + 1) & 1], busy, !full);
             if (t + 1 < t_end) put_stats((t + 1) & 1);
             tiles_ready();
         }
     }
     const float f = scaled_ds<T> ? p.scale * exp2_fast(ref) : p.scale;
+    if constexpr (RG > 1) {
+        // row group 0 adds the others': each passes dv, then dk, through LDS (the tiles are no longer needed) in a layout of whole
+        // 256-byte lines, element by element
+        constexpr int SLOT = 64 * NR * DB * 16;               // floats of one wave's share
+        static_assert(KG * SLOT * 4 <= 4 * TILE_BYTES, "a row group's share fits the tiles");
+        float *share = reinterpret_cast<float *>(lds[0]) + kg * SLOT + lane;
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+            for (int d = 0; d < DB; ++d) dk[i][d] *= f;
+        for (int g = 1; g < RG; ++g)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                __syncthreads();
+                if (rg == g) {
+#pragma unroll
+                    for (int i = 0; i < NR; ++i)
+#pragma unroll
+                        for (int d = 0; d < DB; ++d)
+#pragma unroll
+                            for (int r = 0; r < 16; ++r)
+                                share[((i * DB + d) * 16 + r) * 64] = half ? dk[i][d][r] : dv[i][d][r];
+                }
+                __syncthreads();
+                if (rg == 0) {
+#pragma unroll
+                    for (int i = 0; i < NR; ++i)
+#pragma unroll
+                        for (int d = 0; d < DB; ++d)
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) {
+                                const float v = share[((i * DB + d) * 16 + r) * 64];
+                                if (half) dk[i][d][r] += v;
+                                else dv[i][d][r] += v;
+                            }
+                }
+            }
+        if (rg != 0) return;
+    }
+    const float out_f = RG > 1 ? 1.f : f;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
         if (key[i] >= Lk) continue;
@@ -713,8 +795,8 @@ __global__ __launch_bounds__(NW * 64, D == 128 ? 1 : 2) void attn_dkv_kernel(Att
             for (int r = 0; r < 16; r += 4) {
                 const int col = 32 * d + 8 * (r / 4) + 4 * h;
                 if (col >= p.D) continue;
-                store4<T>((T *)p.dk + at + col, dk[i][d][r] * f, dk[i][d][r + 1] * f, dk[i][d][r + 2] * f,
-                          dk[i][d][r + 3] * f);
+                store4<T>((T *)p.dk + at + col, dk[i][d][r] * out_f, dk[i][d][r + 1] * out_f, dk[i][d][r + 2] * out_f,
+                          dk[i][d][r + 3] * out_f);
                 store4<T>((T *)p.dv + at + col, dv[i][d][r], dv[i][d][r + 1], dv[i][d][r + 2], dv[i][d][r + 3]);
             }
     }

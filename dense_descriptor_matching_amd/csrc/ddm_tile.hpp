@@ -131,8 +131,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, int64
 template <class T, int D, int NW, int ROWS>
 struct Dma {
     using TL = Tile<T, D>;
-    static constexpr int N = ROWS * TL::NP / (NW * 64);
-    static_assert(N * NW * 64 == ROWS * TL::NP, "whole waves");
+    static constexpr int ALL = ROWS * TL::NP / 64, N = (ALL + NW - 1) / NW;      // loads of the tile, and of a wave
+    static_assert(ALL * 64 == ROWS * TL::NP, "whole waves");
     __device__ static __forceinline__ int row(int n, int w, int lane) { return ((w * N + n) * 64 + lane) / TL::NP; }
     __device__ static __forceinline__ int piece(int n, int w, int lane) {
         return ((w * N + n) * 64 + lane) % TL::NP ^ TL::swizzle(row(n, w, lane));
@@ -145,8 +145,9 @@ struct Dma {
     __device__ static __forceinline__ void load(__amdgpu_buffer_rsrc_t b, const int (&off)[N], unsigned char *t, int w) {
 #pragma unroll
         for (int n = 0; n < N; ++n)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (void __attribute__((address_space(3))) *)(t + (w * N + n) * 1024), 16,
-                                                     off[n], 0, 0, 0);
+            if (ALL % NW == 0 || w * N + n < ALL)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (void __attribute__((address_space(3))) *)(t + (w * N + n) * 1024), 
+                                                         16, off[n], 0, 0, 0);
     }
 };
 
@@ -199,6 +200,6 @@ inline __host__ __device__ long long slot_count(int B, int T, int mul, int tile)
 // r / g by multiplication: m = ceil(2^32 / g) is exact for r g < 2^32; g == 1 has no 32-bit m.
 struct Div { uint32_t g, m; };
 inline Div make_div(uint32_t g) { return Div{g, g > 1 ? (uint32_t)((0x100000000ull + g - 1) / g) : 0}; }
-__device__ __forceinline__ uint32_t div_by(uint32_t r, Div d) { return d.g == 1 ? r : __umulhi(r, d.m); }
+__device__ __forceinline__ uint32_t div_by(uint32_t r, Div d) { return __umulhi(r, d.m) + (d.m ? 0 : r); }
 
 }  // namespace ddm
