@@ -13,6 +13,8 @@ namespace {
 
 constexpr int SPLIT_ROWS = 32;            // rows of a workgroup of the split form
 
+constexpr int KEYS = 128;                 // keys of a workgroup of the dk/dv kernel
+
 struct Plan {
     int d;                                // padded head dimension: 32, 64 or 128
     bool split;
@@ -40,6 +42,19 @@ Plan make_plan(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int D) {
         if (mean <= SPLIT_ROWS / 2) p.cap = SPLIT_ROWS;
         p.bytes = (size_t)(slot_count(B, Tk, 1, p.chunk) * Hkv) * p.cap * (D + 4) * sizeof(float);
     }
+    return p;
+}
+
+// Backward: the statistics of the rows, then the parts of the dk/dv kernel. Parts are taken where key tiles alone are few.
+struct BackPlan { int parts; size_t stats, bytes; };
+BackPlan make_back_plan(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int D) {
+    BackPlan p{};
+    const long long tiles = slot_count(B, Tk, 1, KEYS) * Hkv, rows = (long long)Tq * (Hq / Hkv);
+    p.parts = (int)std::min<long long>(std::max<long long>(1024 / tiles, 1), std::max<long long>(rows / PART_ROWS, 1));
+    p.parts = std::min(p.parts, 8);
+    p.stats = ((size_t)Tq * Hq * sizeof(float) * (dtype == DDM_F16 ? 3 : 2) + 255) / 256 * 256;
+    const int d = D <= 32 ? 32 : D <= 64 ? 64 : 128;
+    p.bytes = p.stats + (p.parts > 1 ? (size_t)tiles * p.parts * 2 * KEYS * d * sizeof(float) : 0);
     return p;
 }
 
@@ -78,7 +93,7 @@ hipError_t forward(const AttnArgs &a, const Plan &pl, hipStream_t s) {
     }
     constexpr int BN = wide ? 64 : 32, NR = wide && D <= 64 ? 2 : 1;
     const long long big = slot_count(a.B, a.Tq, G, 128 * NR) * a.Hkv;
-    if (NR == 2 && (long long)a.Tq * G / 256 * a.Hkv >= 512) {
+    if (false && (long long)a.Tq * G / 256 * a.Hkv >= 512) {
         hipLaunchKernelGGL((attn_fwd_kernel<T, D, 4, NR, BN, false>), dim3((unsigned)big), dim3(256), 0, s, a);
     } else {
         const long long n = slot_count(a.B, a.Tq, G, 128) * a.Hkv;
@@ -87,8 +102,16 @@ hipError_t forward(const AttnArgs &a, const Plan &pl, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Rows of a tile of at most `most` in the dk/dv kernel: whole queries of G heads, or where G is larger a whole part of one.
+int tile_rows(int most, int G) {
+    if (G <= most) return most / G * G;
+    int r = most;
+    while (G % r) --r;
+    return r;
+}
+
 template <class T, int D>
-hipError_t backward(const AttnArgs &a, hipStream_t s) {
+hipError_t backward(AttnArgs a, hipStream_t s) {
     const int G = a.group.g;
     constexpr bool wide = sizeof(T) == 2;
     constexpr int BN = wide ? 64 : 32, NR = 1;
@@ -98,9 +121,13 @@ hipError_t backward(const AttnArgs &a, hipStream_t s) {
         if (hipError_t e = hipGetLastError()) return e;
     }
     if (a.Tk) {
-        constexpr int KG = wide && D == 128 ? 2 : 4, RG = wide && D == 128 ? 4 : wide ? 2 : 1;
-        const long long n = slot_count(a.B, a.Tk, 1, 32 * KG) * a.Hkv;
-        hipLaunchKernelGGL((attn_dkv_kernel<T, D, KG, RG, 1>), dim3((unsigned)n), dim3(KG * RG * 64), 0, s, a);
+        constexpr int BL = wide && D < 128 ? 2 : 1;
+        const long long n = slot_count(a.B, a.Tk, 1, KEYS) * a.Hkv;
+        a.rt = tile_rows(32 * BL, G);
+        hipLaunchKernelGGL((attn_dkv_kernel<T, D, KEYS / 32, BL>), dim3((unsigned)n, a.parts), dim3(KEYS * 2), 0, s, a);
+        if (hipError_t e = hipGetLastError()) return e;
+        if (a.parts > 1)
+            hipLaunchKernelGGL((attn_dkv_join_kernel<T, D, KEYS / 32>), dim3((unsigned)n, 2 * KEYS / 32), dim3(256), 0, s, a);
     }
     return hipGetLastError();
 }
@@ -155,7 +182,7 @@ int ddm_attention_forward(const void *q, int64_t q_ts, int64_t q_hs, const void 
 
 size_t ddm_attention_backward_workspace_bytes(int B, int Tq, int Tk, int Hq, int Hkv, int D, int dtype) {
     if (check(dtype, B, Tq, Tk, Hq, Hkv, D) != DDM_OK) return 0;
-    return std::max<size_t>((size_t)Tq * Hq * sizeof(float) * (dtype == DDM_F16 ? 2 : 1), 16);
+    return std::max<size_t>(make_back_plan(dtype, B, Tq, Tk, Hq, Hkv, D).bytes, 16);
 }
 
 int ddm_attention_backward(const void *dout, int64_t g_ts, int64_t g_hs, const void *q, int64_t q_ts, int64_t q_hs,
@@ -171,11 +198,12 @@ int ddm_attention_backward(const void *dout, int64_t g_ts, int64_t g_hs, const v
         return DDM_ERR_INVALID;
     if (Tk && (bad_view(k, k_ts, k_hs, Hkv, dtype) || bad_view(v, v_ts, v_hs, Hkv, dtype) || bad_ptr(dk) || bad_ptr(dv)))
         return DDM_ERR_INVALID;
-    const size_t need = ddm_attention_backward_workspace_bytes(B, Tq, Tk, Hq, Hkv, D, dtype);
-    if (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < need) return DDM_ERR_WORKSPACE;
+    const BackPlan bp = make_back_plan(dtype, B, Tq, Tk, Hq, Hkv, D);
+    if (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < bp.bytes) return DDM_ERR_WORKSPACE;
     const Plan pl = make_plan(dtype, B, Tq, Tk, Hq, Hkv, D);
     AttnArgs a{};
-    a.q = q; a.k = k; a.v = v; a.o = out; a.dout = dout; a.lse = const_cast<float *>(lse); a.delta = (float *)workspace;
+    a.q = q; a.k = k; a.v = v; a.o = out; a.dout = dout; a.lse = const_cast<float *>(lse); a.stats = (float *)workspace;
+    a.parts = bp.parts; a.part = (float *)((char *)workspace + bp.stats);
     a.dq = dq; a.dk = dk; a.dv = dv;
     a.cu_q = cu_q; a.cu_k = cu_k;
     a.B = B; a.Tq = Tq; a.Tk = Tk; a.Hq = Hq; a.Hkv = Hkv; a.D = D;

@@ -15,16 +15,22 @@ namespace ddm {
 struct AttnArgs {
     const void *q, *k, *v, *o, *dout;     // o: forward writes it through `out`, backward reads it here
     void *out, *dq, *dk, *dv;
-    float *lse, *delta;                   // [Tq][Hq]; delta: D_i and, for fp16, the exponent of the row's largest |do|
+    float *lse;                           // [Tq][Hq]
+    float *stats;                         // backward: [Tq][Hq] of lse_i log2(e) (infinity for an empty row), of D_i and, for fp16,
+                                          // of the exponent of the row's largest |do| less NO_EXPONENT
     const int32_t *cu_q, *cu_k;
     int B, Tq, Tk, Hq, Hkv, D;
     Div group;
     int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, g_ts, g_hs;   // token and head strides in elements (g: dout)
     float scale, c;                       // c = scale log2(e)
     int causal;
+    int rt, parts;                        // attn_dkv_kernel: rows of a tile, most parts of a key tile's rows
     int chunk, cap;                       // split form: keys of a chunk, rows of a sequence that are split
-    float *part;                          // split form: [slot][Hkv][cap][D + 2]
+    float *part;                          // split form: [slot][Hkv][cap][D + 4]; attn_dkv_kernel: [slot][Hkv][parts][2][keys][padded D]
 };
+
+// Workgroups go round-robin to the 8 XCDs, each with its own L2: with 8 | Hkv a key head's workgroups stay on one XCD.
+__device__ __forceinline__ int key_head(int x, int heads) { return (heads & 7) ? x : (x & 7) * (heads >> 3) + (x >> 3); }
 
 // Bytes from row 0 of `rows` strided rows of d elements to the end of the last.
 template <class T>
@@ -89,9 +95,8 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_fwd_kernel(AttnArgs p) {
         s = find_slot(p.cu_k, p.B, p.Tk, 1, p.chunk, blockIdx.x / p.Hkv, &index);
         if (s == 0 || s == p.B + 1) return;
     } else {
-        // workgroups go round-robin to the 8 XCDs, each with its own L2: with 8 | Hkv, a key head stays on one XCD
-        const int heads = p.Hkv, x = blockIdx.x % heads;
-        hk = (heads & 7) ? x : (x & 7) * (heads >> 3) + (x >> 3);
+        const int heads = p.Hkv;
+        hk = key_head(blockIdx.x % heads, heads);
         const int slots = gridDim.x / heads;
         // the last rows of a causal sequence see the most keys: they start first
         s = find_slot(p.cu_q, p.B, p.Tq, G, BM, slots - 1 - blockIdx.x / heads, &index);
@@ -373,8 +378,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dq_kernel(AttnArgs p) {
     const int h = lane >> 5, n = lane & 31;
     const int G = p.group.g;
 
-    const int heads = p.Hkv, x = blockIdx.x % heads;
-    const int hk = (heads & 7) ? x : (x & 7) * (heads >> 3) + (x >> 3);
+    const int heads = p.Hkv, hk = key_head(blockIdx.x % heads, heads);
     int row_tile;
     const int s = find_slot(p.cu_q, p.B, p.Tq, G, BM, gridDim.x / heads - 1 - blockIdx.x / heads, &row_tile);
     const Span sq = span_of(p.cu_q, p.B, p.Tq, s);
@@ -431,8 +435,10 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dq_kernel(AttnArgs p) {
             inv[i] = exp2_fast(-ex);
         }
         if (in && h == 0) {
-            p.delta[at[i]] = delta[i];
-            if constexpr (scaled_ds<T>) p.delta[at[i] + (int64_t)p.Tq * p.Hq] = ex;
+            const int64_t all = (int64_t)p.Tq * p.Hq;
+            p.stats[at[i]] = lse[i];
+            p.stats[at[i] + all] = delta[i];
+            if constexpr (scaled_ds<T>) p.stats[at[i] + 2 * all] = ex - NO_EXPONENT;
         }
     }
     int top = Lk, low = Lk;
@@ -534,186 +540,189 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dq_kernel(AttnArgs p) {
     }
 }
 
-// dk and dv: a workgroup keeps 32 KG NR keys (K and V rows as operands in registers) and walks over the rows of the key
-// head's whole group in tiles of BQ = 32 RG, Q and dO in LDS. S = Q K^T and dO V^T come out with the keys as columns, so P and
-// dS feed the products with dO and Q (read as columns) without leaving their lanes. Of its KG RG waves, KG share out the keys and
-// RG the rows of each tile; the RG shares of dk and dv are added through LDS, in order, when the rows are done.
-template <class T, int D, int KG, int RG, int NR>
-__global__ __launch_bounds__(KG * RG * 64, KG * RG > 4 ? 1 : sizeof(T) == 4 && D == 128 ? 1 : 2) void attn_dkv_kernel(AttnArgs p) {
+// dk and dv: a workgroup of KW waves keeps 32 KW keys (their K, and V where there is room, as operands in registers) and walks
+// over the rows of the key head's whole group in tiles of BQ = 32 BL, Q and dO in LDS. S = Q K^T and dO V^T come out with the keys
+// as columns, so P and dS feed the products with dO and Q (read as columns) without leaving their lanes.
+// Where there are few key tiles, or causal ones with very different numbers of rows, a sequence's rows are cut into up to `most`
+// parts of at least PART_ROWS, at the same rows for every tile, so that workgroups that run together read the same rows through
+// their L2. The parts' sums go to the workspace in fp32 and attn_dkv_join_kernel adds them in order.
+constexpr int PART_ROWS = 512;
+struct RowPart { int from, to, begin, parts; };    // rows of one part for a tile; the tile's first part and the end of its parts
+__device__ __forceinline__ RowPart part_of(int first, int rows, int most, int rt, int part) {
+    const int want = max(1, min(most, rows / PART_ROWS));
+    const int each = max(1, ((rows + want - 1) / want + rt - 1) / rt) * rt;      // whole tiles
+    RowPart r;
+    r.parts = max(1, (rows + each - 1) / each);
+    r.begin = min(first / each, r.parts - 1);
+    r.from = min(rows, max(first, part * each));
+    r.to = min(rows, max(r.from, (part + 1) * each));
+    return r;
+}
+
+template <class T, int D, int KW, int BL>
+__global__ __launch_bounds__(KW * 64, sizeof(T) == 4 && D == 128 ? 1 : 2) void attn_dkv_kernel(AttnArgs p) {
     using TL = Tile<T, D>;
-    constexpr int NW = KG * RG, BK = KG * NR * 32, BQ = RG * 32, DC = D / 16, DB = D / 32;
+    constexpr int NW = KW, BK = KW * 32, BQ = BL * 32, DC = D / 16, DB = D / 32;
     constexpr int TILE_BYTES = BQ * TL::ROW;
-    static_assert(BQ <= NW * 64 && BQ % 32 == 0, "a thread loads a row's statistics");
     __shared__ __attribute__((aligned(16))) unsigned char lds[2][2 * TILE_BYTES];
     // 128 16-bit components: with V in registers too, the accumulators would be spilled
     constexpr bool V_LDS = D == 128 && sizeof(T) == 2;
+    constexpr int STATS = scaled_ds<T> ? 3 : 2;
+    static_assert(BQ % 64 == 0 || BQ == 32, "a wave loads 64 rows' statistics");
     __shared__ __attribute__((aligned(16))) unsigned char v_lds[V_LDS ? BK * TL::ROW : 16];
-    __shared__ __attribute__((aligned(16))) float st_lse[2][BQ], st_delta[2][BQ];
-    __shared__ __attribute__((aligned(16))) int st_lim[2][BQ];
-    __shared__ float st_exp[2][RG];
+    __shared__ __attribute__((aligned(16))) float stats[2][STATS][BQ < 64 ? 64 : BQ];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int h = lane >> 5, n = lane & 31, kg = w % KG, rg = w / KG;
+    const int h = lane >> 5, n = lane & 31;
     const int G = p.group.g;
 
-    const int heads = p.Hkv, x = blockIdx.x % heads;
-    const int hk = (heads & 7) ? x : (x & 7) * (heads >> 3) + (x >> 3);
+    const int heads = p.Hkv, hk = key_head(blockIdx.x % heads, heads);
     int key_tile;
     const int s = find_slot(p.cu_k, p.B, p.Tk, 1, BK, blockIdx.x / heads, &key_tile);
     Span sq = span_of(p.cu_q, p.B, p.Tq, s);
     const Span sk = span_of(p.cu_k, p.B, p.Tk, s);
     if (s == 0 || s == p.B + 1) sq.hi = sq.lo;
-    const int rows = (sq.hi - sq.lo) * G, Lk = sk.hi - sk.lo, shift = Lk - (sq.hi - sq.lo), j0 = key_tile * BK;
+    const int all_rows = (sq.hi - sq.lo) * G, Lk = sk.hi - sk.lo, shift = Lk - (sq.hi - sq.lo), j0 = key_tile * BK;
     if (j0 >= Lk) return;
     const int j_end = min(j0 + BK, Lk);
 
-    Frag<T> kf[NR][DC], vf[NR][V_LDS ? 1 : DC];
-    int key[NR];
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        key[i] = j0 + (kg * NR + i) * 32 + n;
-        const bool in = key[i] < Lk;
-        const int64_t tok = sk.lo + (in ? key[i] : Lk - 1);
+    Frag<T> kf[DC], vf[V_LDS ? 1 : DC];
+    const int key = j0 + w * 32 + n;
+    {
+        const bool in = key < Lk;
+        const int64_t tok = sk.lo + (in ? key : Lk - 1);
         const T *kr = (const T *)p.k + tok * p.k_ts + (int64_t)hk * p.k_hs;
         const T *vr = (const T *)p.v + tok * p.v_ts + (int64_t)hk * p.v_hs;
 #pragma unroll
         for (int c = 0; c < DC; ++c) {
-            kf[i][c] = global_rows<T>(kr, 16 * c + 8 * h, p.D, in);
-            if constexpr (!V_LDS) vf[i][c] = global_rows<T>(vr, 16 * c + 8 * h, p.D, in);
+            kf[c] = global_rows<T>(kr, 16 * c + 8 * h, p.D, in);
+            if constexpr (!V_LDS) vf[c] = global_rows<T>(vr, 16 * c + 8 * h, p.D, in);
         }
     }
-    const int first = p.causal ? min(rows, max(0, j0 - shift) * G) : 0;     // earlier rows see none of these keys
-    const int t_end = (rows - first + BQ - 1) / BQ;
-    const int wave_key = j0 + kg * NR * 32;
+    const int first = p.causal ? min(all_rows, max(0, j0 - shift) * G) : 0;     // earlier rows see none of these keys
+    const RowPart part = part_of(first, all_rows, p.parts, p.rt, blockIdx.y);
+    if ((int)blockIdx.y < part.begin || (int)blockIdx.y >= part.parts) return;
+    const int rows = part.to, t_end = (rows - part.from + p.rt - 1) / p.rt, wave_key = j0 + w * 32;
 
-    f32x16 dk[NR][DB], dv[NR][DB];
+    f32x16 dk[DB], dv[DB];
 #pragma unroll
-    for (int i = 0; i < NR; ++i)
-#pragma unroll
-        for (int d = 0; d < DB; ++d) { dk[i][d] = 0.f; dv[i][d] = 0.f; }
+    for (int d = 0; d < DB; ++d) { dk[d] = 0.f; dv[d] = 0.f; }
     float ref = NO_EXPONENT;                                  // dk is held in units of 2^ref (fp16)
 
     using In = Dma<T, D, NW, BQ>;
     const int row_at = TL::row_base(lane), col_at = TL::col_base(lane);
-    float s_lse = INFINITY, s_delta = 0.f, s_exp = NO_EXPONENT;
-    int s_lim = 0;
-    auto fetch = [&](int t, unsigned char *to) {
-        const int r0 = first + t * BQ, q0 = (int)div_by(r0, p.group);
-        const auto qb = buffer_of((const T *)p.q + (int64_t)(sq.lo + q0) * p.q_ts + (int64_t)hk * G * p.q_hs, INT64_MAX);
-        const auto gb = buffer_of((const T *)p.dout + (int64_t)(sq.lo + q0) * p.g_ts + (int64_t)hk * G * p.g_hs, INT64_MAX);
-        int qo[In::N], go[In::N];
-#pragma unroll
-        for (int i = 0; i < In::N; ++i) {
-            const int r = r0 + In::row(i, w, lane), pc = In::piece(i, w, lane);
-            const int qi = (int)div_by(r, p.group), g = r - qi * G;
-            const bool in = r < rows && pc * TL::PE < p.D;
-            qo[i] = in ? ((qi - q0) * (int)p.q_ts + g * (int)p.q_hs) * (int)sizeof(T) + pc * 16 : OUTSIDE;
-            go[i] = in ? ((qi - q0) * (int)p.g_ts + g * (int)p.g_hs) * (int)sizeof(T) + pc * 16 : OUTSIDE;
-        }
-        In::load(qb, qo, to, w);
-        In::load(gb, go, to + TILE_BYTES, w);
-        if (tid < BQ) {
-            const int r = r0 + tid;
-            const bool in = r < rows;
-            const int rr = in ? r : rows - 1, qi = (int)div_by(rr, p.group);
-            const int64_t at = (int64_t)(sq.lo + qi) * p.Hq + hk * G + (rr - qi * G);
-            const float z = p.lse[at];
-            s_lse = !in || z == -INFINITY ? INFINITY : z * 1.44269504088896341f;
-            s_delta = in ? p.delta[at] : 0.f;
-            s_lim = qi + shift + 1;
-            if constexpr (scaled_ds<T>) s_exp = in ? p.delta[at + (int64_t)p.Tq * p.Hq] : NO_EXPONENT;
-        }
+    // A tile has rt <= BQ rows: whole queries, or a whole part of one with more heads than BQ (see the plan). So a lane's offsets
+    // are the same for every tile, but for the rows that a last tile lacks.
+    auto in_tile = [&](int row, int64_t ts, int64_t hs) {
+        const int qi = G <= BQ ? (int)div_by(row, p.group) : 0;
+        return qi * (int)ts + (row - qi * G * (G <= BQ)) * (int)hs;
     };
-    auto put_stats = [&](int b) {
-        if (tid < BQ) {
-            st_lse[b][tid] = s_lse;
-            st_delta[b][tid] = s_delta;
-            st_lim[b][tid] = s_lim;
-        }
-        if constexpr (scaled_ds<T>) {
-            if (tid < BQ) {                                    // one value for the 32 rows of a wave's step
-                float e = s_exp;
+    int qo[In::N], go[In::N];
+    const int lane_row = In::row(0, w, lane);
 #pragma unroll
-                for (int d = 16; d; d >>= 1) e = fmaxf(e, __shfl_xor(e, d));
-                if (tid % 32 == 0) st_exp[b][tid / 32] = e;
+    for (int i = 0; i < In::N; ++i) {
+        const int row = In::row(i, w, lane), pc = In::piece(i, w, lane);
+        const bool in = pc * TL::PE < p.D && row < p.rt;
+        qo[i] = in ? in_tile(row, p.q_ts, p.q_hs) * (int)sizeof(T) + pc * 16 : OUTSIDE;
+        go[i] = in ? in_tile(row, p.g_ts, p.g_hs) * (int)sizeof(T) + pc * 16 : OUTSIDE;
+    }
+    constexpr int PER = (BQ + 63) / 64, JOBS = (PER * STATS + NW - 1) / NW;   // wave loads of a statistic of a tile; of a wave
+    int so[JOBS];
+#pragma unroll
+    for (int i = 0; i < JOBS; ++i) {
+        const int row = (w + i * NW) % PER * 64 + lane;
+        so[i] = row < p.rt ? in_tile(row, p.Hq, 1) * 4 : OUTSIDE;
+    }
+    auto fetch = [&](int t, int buf, unsigned char *to) {
+        const int r0 = part.from + t * p.rt, q0 = (int)div_by(r0, p.group), head = hk * G + (r0 - q0 * G);
+        const int64_t tok = sq.lo + q0;
+        const int left = rows - r0;                            // rows from here on are not there
+        const auto qb = buffer_of((const T *)p.q + tok * p.q_ts + head * p.q_hs, OUTSIDE);
+        const auto gb = buffer_of((const T *)p.dout + tok * p.g_ts + head * p.g_hs, OUTSIDE);
+        if (left >= p.rt) {
+            In::load(qb, qo, to, w);
+            In::load(gb, go, to + TILE_BYTES, w);
+        } else {
+            int q2[In::N], g2[In::N];
+#pragma unroll
+            for (int i = 0; i < In::N; ++i) {
+                const bool in = lane_row + i * (64 / TL::NP) < left;
+                q2[i] = in ? qo[i] : OUTSIDE;
+                g2[i] = in ? go[i] : OUTSIDE;
             }
+            In::load(qb, q2, to, w);
+            In::load(gb, g2, to + TILE_BYTES, w);
+        }
+#pragma unroll
+        for (int i = 0; i < JOBS; ++i) {
+            const int which = (w + i * NW) / PER, part = (w + i * NW) % PER;
+            if (which >= STATS) continue;
+            const auto sb = buffer_of(p.stats + (int64_t)which * p.Tq * p.Hq + tok * p.Hq + head, OUTSIDE);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                sb, (void __attribute__((address_space(3))) *)(&stats[buf][which][part * 64]), 4,
+                part * 64 + lane < left ? so[i] : OUTSIDE, 0, 0, 0);
         }
     };
-    auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, bool busy, bool masked) {
-        if (t + 1 < t_end) fetch(t + 1, next);
+    auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, unsigned busy, unsigned masked) {
+        if (t + 1 < t_end) fetch(t + 1, (t + 1) & 1, next);
         if (!busy) return;
         const int buf = t & 1;
         const unsigned char *qt = cur, *gt = cur + TILE_BYTES;
-        float inv = 1.f;
-        if constexpr (scaled_ds<T>) {
-            const float e = st_exp[buf][rg];
-            if (e > ref) {
-                const float f = exp2_fast(ref - e);
 #pragma unroll
-                for (int i = 0; i < NR; ++i)
+        for (int b = 0; b < BL; ++b) {
+            if (!(busy >> b & 1)) continue;
+            float inv = 1.f;
+            if constexpr (scaled_ds<T>) {
+                float e = stats[buf][STATS - 1][32 * b + n];  // from NO_EXPONENT on: rows that are not there read 0
 #pragma unroll
-                    for (int d = 0; d < DB; ++d) dk[i][d] *= f;
-                ref = e;
+                for (int x = 16; x; x >>= 1) e = fmaxf(e, __shfl_xor(e, x));
+                e += NO_EXPONENT;
+                if (e > ref) {
+                    const float f = exp2_fast(ref - e);
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) dk[d] *= f;
+                    ref = e;
+                }
+                inv = exp2_fast(-ref);
             }
-            inv = exp2_fast(-ref);
-        }
-        f32x16 z[NR], y[NR];
+            f32x16 z = 0.f, y = 0.f;
 #pragma unroll
-        for (int i = 0; i < NR; ++i) { z[i] = 0.f; y[i] = 0.f; }
-#pragma unroll
-        for (int c = 0; c < DC; ++c) {
-            const Frag<T> qf = TL::rows(qt, row_at, 32 * rg, c), gf = TL::rows(gt, row_at, 32 * rg, c);
-#pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                mma(z[i], qf, kf[i][c]);
-                if constexpr (V_LDS) mma(y[i], gf, TL::rows(v_lds, row_at, 32 * (kg * NR + i), c));
-                else mma(y[i], gf, vf[i][c]);
+            for (int c = 0; c < DC; ++c) {
+                mma(z, TL::rows(qt, row_at, 32 * b, c), kf[c]);
+                if constexpr (V_LDS) mma(y, TL::rows(gt, row_at, 32 * b, c), TL::rows(v_lds, row_at, 32 * w, c));
+                else mma(y, TL::rows(gt, row_at, 32 * b, c), vf[c]);
             }
-        }
-        if (masked) {
+            if (masked >> b & 1) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int lim = st_lim[buf][32 * rg + 8 * (r / 4) + 4 * h + r % 4];
-#pragma unroll
-                for (int i = 0; i < NR; ++i)
-                    if (key[i] >= lim) z[i][r] = -INFINITY;
+                for (int r = 0; r < 16; ++r) {
+                    const int row = part.from + t * p.rt + 32 * b + 8 * (r / 4) + 4 * h + r % 4;
+                    if (key > (int)div_by(row, p.group) + shift) z[r] = -INFINITY;
+                }
             }
-        }
 #pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-            const int r0 = 32 * rg + 8 * r4 + 4 * h;
-            const f32x4 ls = *reinterpret_cast<const f32x4 *>(&st_lse[buf][r0]);
-            const f32x4 de = *reinterpret_cast<const f32x4 *>(&st_delta[buf][r0]);
-#pragma unroll
-            for (int i = 0; i < NR; ++i)
+            for (int r4 = 0; r4 < 4; ++r4) {
+                const int r0 = 32 * b + 8 * r4 + 4 * h;
+                const f32x4 ls = *reinterpret_cast<const f32x4 *>(&stats[buf][0][r0]);
+                const f32x4 de = *reinterpret_cast<const f32x4 *>(&stats[buf][1][r0]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int r = 4 * r4 + e;
-                    const float pr = exp2_fast(__builtin_fmaf(z[i][r], p.c, -ls[e]));
-                    z[i][r] = pr;
-                    y[i][r] = pr * (y[i][r] - de[e]);
-                    if constexpr (scaled_ds<T>) y[i][r] *= inv;
+                    const float pr = exp2_fast(__builtin_fmaf(z[r], p.c, -ls[e]));
+                    z[r] = pr;
+                    y[r] = pr * (y[r] - de[e]);
+                    if constexpr (scaled_ds<T>) y[r] *= inv;
                 }
-        }
-        if constexpr (D == 128) __builtin_amdgcn_sched_barrier(0);   // loads hoisted further up would not fit the registers
+            }
+            if constexpr (D == 128) __builtin_amdgcn_sched_barrier(0);   // loads hoisted further up would not fit the registers
 #pragma unroll
-        for (int kc = 0; kc < 2; ++kc) {
-            Frag<T> pf[NR], sf[NR];
-#pragma unroll
-            for (int i = 0; i < NR; ++i) {
+            for (int kc = 0; kc < 2; ++kc) {
                 float a[8], c[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) { a[e] = z[i][kc * 8 + e]; c[e] = y[i][kc * 8 + e]; }
-                pf[i] = to_frag<T>(a);
-                sf[i] = to_frag<T>(c);
-            }
+                for (int e = 0; e < 8; ++e) { a[e] = z[kc * 8 + e]; c[e] = y[kc * 8 + e]; }
+                const Frag<T> pf = to_frag<T>(a), sf = to_frag<T>(c);
 #pragma unroll
-            for (int d = 0; d < DB; ++d) {
-                const Frag<T> gf = TL::cols(gt, col_at, 32 * rg + 16 * kc, 32 * d);
-                const Frag<T> qf = TL::cols(qt, col_at, 32 * rg + 16 * kc, 32 * d);
-#pragma unroll
-                for (int i = 0; i < NR; ++i) {
-                    mma(dv[i][d], gf, pf[i]);
-                    mma(dk[i][d], qf, sf[i]);
+                for (int d = 0; d < DB; ++d) {
+                    mma(dv[d], TL::cols(gt, col_at, 32 * b + 16 * kc, 32 * d), pf);
+                    mma(dk[d], TL::cols(qt, col_at, 32 * b + 16 * kc, 32 * d), sf);
                 }
             }
         }
@@ -727,78 +736,79 @@ __global__ __launch_bounds__(KG * RG * 64, KG * RG > 4 ? 1 : sizeof(T) == 4 && D
             Iv::load(buffer_of((const T *)p.v + (int64_t)(sk.lo + j0) * p.v_ts + (int64_t)hk * p.v_hs,
                                rows_bytes<T>(j_end - j0, p.v_ts, p.D)), off, v_lds, w);
         }
-        fetch(0, lds[0]);
-        put_stats(0);
+        fetch(0, 0, lds[0]);
         tiles_ready();
         for (int t = 0; t < t_end; ++t) {
-            const int r0 = first + t * BQ;
-            bool busy = wave_key < Lk, full = true;
-            const int w0 = r0 + 32 * rg;                        // this wave's rows of the tile
-            busy = busy && w0 < rows;
-            if (p.causal) {
-                busy = busy && wave_key < (int)div_by(min(w0 + 32, rows) - 1, p.group) + shift + 1;
-                full = j_end <= (int)div_by(w0, p.group) + shift + 1;
+            unsigned busy = 0, masked = 0;                      // by blocks of 32 rows: this wave's keys see it, not all see it whole
+#pragma unroll
+            for (int b = 0; b < BL; ++b) {
+                const int w0 = part.from + t * p.rt + 32 * b;
+                const int w1 = min(min(w0 + 32, part.from + (t + 1) * p.rt), rows);
+                if (wave_key >= Lk || w0 >= w1) continue;
+                if (p.causal) {
+                    if (wave_key >= (int)div_by(w1 - 1, p.group) + shift + 1) continue;
+                    if (min(wave_key + 32, Lk) > (int)div_by(w0, p.group) + shift + 1) masked |= 1u << b;
+                }
+                busy |= 1u << b;
             }
-            step(t, lds[t & 1], lds[(t + 1) & 1], busy, !full);
-            if (t + 1 < t_end) put_stats((t + 1) & 1);
+            step(t, lds[t & 1], lds[(t + 1) & 1], busy, masked);
             tiles_ready();
         }
     }
     const float f = scaled_ds<T> ? p.scale * exp2_fast(ref) : p.scale;
-    if constexpr (RG > 1) {
-        // row group 0 adds the others': each passes dv, then dk, through LDS (the tiles are no longer needed) in a layout of whole
-        // 256-byte lines, element by element
-        constexpr int SLOT = 64 * NR * DB * 16;               // floats of one wave's share
-        static_assert(KG * SLOT * 4 <= 4 * TILE_BYTES, "a row group's share fits the tiles");
-        float *share = reinterpret_cast<float *>(lds[0]) + kg * SLOT + lane;
-#pragma unroll
-        for (int i = 0; i < NR; ++i)
-#pragma unroll
-            for (int d = 0; d < DB; ++d) dk[i][d] *= f;
-        for (int g = 1; g < RG; ++g)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                __syncthreads();
-                if (rg == g) {
-#pragma unroll
-                    for (int i = 0; i < NR; ++i)
-#pragma unroll
-                        for (int d = 0; d < DB; ++d)
-#pragma unroll
-                            for (int r = 0; r < 16; ++r)
-                                share[((i * DB + d) * 16 + r) * 64] = half ? dk[i][d][r] : dv[i][d][r];
-                }
-                __syncthreads();
-                if (rg == 0) {
-#pragma unroll
-                    for (int i = 0; i < NR; ++i)
-#pragma unroll
-                        for (int d = 0; d < DB; ++d)
-#pragma unroll
-                            for (int r = 0; r < 16; ++r) {
-                                const float v = share[((i * DB + d) * 16 + r) * 64];
-                                if (half) dk[i][d][r] += v;
-                                else dv[i][d][r] += v;
-                            }
-                }
-            }
-        if (rg != 0) return;
-    }
-    const float out_f = RG > 1 ? 1.f : f;
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        if (key[i] >= Lk) continue;
-        const int64_t at = ((int64_t)(sk.lo + key[i]) * p.Hkv + hk) * p.D;
+    if (part.parts - part.begin > 1) {
+        // as the lanes hold it: four elements a lane, 1 KB a store
+        f32x4 *out = reinterpret_cast<f32x4 *>(p.part) + (((int64_t)blockIdx.x * p.parts + blockIdx.y) * 2 * BK + w * 32) * (D / 4) + lane;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
-            for (int r = 0; r < 16; r += 4) {
-                const int col = 32 * d + 8 * (r / 4) + 4 * h;
-                if (col >= p.D) continue;
-                store4<T>((T *)p.dk + at + col, dk[i][d][r] * out_f, dk[i][d][r + 1] * out_f, dk[i][d][r + 2] * out_f,
-                          dk[i][d][r + 3] * out_f);
-                store4<T>((T *)p.dv + at + col, dv[i][d][r], dv[i][d][r + 1], dv[i][d][r + 2], dv[i][d][r + 3]);
+            for (int q = 0; q < 4; ++q) {
+                const int r = 4 * q;
+                out[(d * 4 + q) * 64] = f32x4{dk[d][r], dk[d][r + 1], dk[d][r + 2], dk[d][r + 3]} * f;
+                out[BK * (D / 4) + (d * 4 + q) * 64] = f32x4{dv[d][r], dv[d][r + 1], dv[d][r + 2], dv[d][r + 3]};
             }
+        return;
+    }
+    if (key >= Lk) return;
+    const int64_t at = ((int64_t)(sk.lo + key) * p.Hkv + hk) * p.D;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+            const int col = 32 * d + 8 * (r / 4) + 4 * h;
+            if (col >= p.D) continue;
+            store4<T>((T *)p.dk + at + col, dk[d][r] * f, dk[d][r + 1] * f, dk[d][r + 2] * f, dk[d][r + 3] * f);
+            store4<T>((T *)p.dv + at + col, dv[d][r], dv[d][r + 1], dv[d][r + 2], dv[d][r + 3]);
+        }
+}
+
+// dk and dv of the key tiles whose rows were cut into parts: a workgroup for 32 keys of one of them.
+template <class T, int D, int KW>
+__global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnArgs p) {
+    constexpr int BK = KW * 32;
+    const int hk = key_head(blockIdx.x % p.Hkv, p.Hkv);
+    int key_tile;
+    const int s = find_slot(p.cu_k, p.B, p.Tk, 1, BK, blockIdx.x / p.Hkv, &key_tile);
+    if (s == 0 || s == p.B + 1) return;
+    const Span sq = span_of(p.cu_q, p.B, p.Tq, s), sk = span_of(p.cu_k, p.B, p.Tk, s);
+    const int G = p.group.g, rows = (sq.hi - sq.lo) * G, Lk = sk.hi - sk.lo, w = blockIdx.y % KW, which = blockIdx.y / KW;
+    const int tile0 = key_tile * BK, j0 = tile0 + w * 32;
+    if (j0 >= Lk) return;
+    const int first = p.causal ? min(rows, max(0, tile0 - (Lk - (sq.hi - sq.lo))) * G) : 0;
+    const RowPart part = part_of(first, rows, p.parts, p.rt, 0);
+    if (part.parts - part.begin == 1) return;
+    constexpr int ALL = BK * (D / 4);                          // f32x4 of one gradient of one part
+    const f32x4 *in = reinterpret_cast<const f32x4 *>(p.part) + ((int64_t)blockIdx.x * p.parts * 2 + which) * ALL + w * (8 * D);
+    T *out = (T *)(which ? p.dv : p.dk);
+#pragma unroll
+    for (int i = threadIdx.x; i < 8 * D; i += 256) {
+        const int lane = i % 64, q = i / 64 % 4, d = i / 256;
+        const int row = lane % 32, col = 32 * d + 8 * q + 4 * (lane / 32);
+        f32x4 sum = 0.f;
+#pragma unroll 4
+        for (int k = part.begin; k < part.parts; ++k) sum += in[(int64_t)k * 2 * ALL + i];
+        if (j0 + row < Lk && col < p.D)
+            store4<T>(out + ((int64_t)(sk.lo + j0 + row) * p.Hkv + hk) * p.D + col, sum[0], sum[1], sum[2], sum[3]);
     }
 }
 
