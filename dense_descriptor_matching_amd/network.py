@@ -11,6 +11,7 @@ the B + 1 places where they begin and end. The lengths stay on the device: no ca
 from __future__ import annotations
 
 import ctypes as C
+import functools
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -43,14 +44,23 @@ def declare(lib):
 
 def _call(dev, what, *args):
     """Enqueue on the tensors' device and its current stream."""
-    f = getattr(_api.lib(), what)
-    if torch.cuda.current_device() == dev.index:
-        rc = f(*args, torch.cuda.current_stream().cuda_stream)
+    f, at = getattr(_api.lib(), what), dev.index
+    if torch.cuda.current_device() == at:
+        rc = f(*args, torch.cuda.current_stream(at).cuda_stream)
     else:
         with torch.cuda.device(dev):
-            rc = f(*args, torch.cuda.current_stream().cuda_stream)
+            rc = f(*args, torch.cuda.current_stream(at).cuda_stream)
     if rc != 0:
         raise _api.DDMError(rc, what)
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(what, *sizes):
+    """The library's workspace size for these sizes (a pure function of them)."""
+    n = getattr(_api.lib(), what)(*sizes)
+    if n == 0:
+        raise _api.DDMError(-4, f"{what} (unsupported sizes)")
+    return n
 
 
 def _tensor(t, name, dtype=None, dev=None, shape=None, contiguous=True):
@@ -93,10 +103,12 @@ def _heads_view(t, name):
 
 
 def _attention_sizes(q, k, v, cu_q, cu_k, scale):
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _tensor(t, name, None if name == "q" else q.dtype, q.device, contiguous=False)
-        if t.dim() != 3:
-            raise ValueError(f"{name} must be [tokens, heads, head dimension]")
+    _tensor(q, "q", contiguous=False)
+    dev, dt = q.device, q.dtype
+    _tensor(k, "k", dt, dev, contiguous=False)
+    _tensor(v, "v", dt, dev, contiguous=False)
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be [tokens, heads, head dimension]")
     Tq, Hq, D = q.shape
     Tk, Hkv, Dk = k.shape
     if v.shape != k.shape or Dk != D:
@@ -105,11 +117,11 @@ def _attention_sizes(q, k, v, cu_q, cu_k, scale):
         raise ValueError("the number of query heads must be a multiple of the number of key heads")
     if (cu_q is None) != (cu_k is None):
         raise ValueError("cu_q and cu_k come together")
-    B, pq = _cu(cu_q, "cu_q", q.device)
-    Bk, pk = _cu(cu_k, "cu_k", q.device)
+    B, pq = _cu(cu_q, "cu_q", dev)
+    Bk, pk = _cu(cu_k, "cu_k", dev)
     if B != Bk:
         raise ValueError("cu_q and cu_k must hold the same number of sequences")
-    return (B, Tq, Tk, Hq, Hkv, D, _DT[q.dtype]), pq, pk, float(D ** -0.5 if scale is None else scale)
+    return (B, Tq, Tk, Hq, Hkv, D, _DT[dt]), pq, pk, float(D ** -0.5 if scale is None else scale)
 
 
 def attention_forward(q, k, v, cu_q=None, cu_k=None, *, causal: bool = False, scale: float | None = None):
@@ -119,9 +131,7 @@ def attention_forward(q, k, v, cu_q=None, cu_k=None, *, causal: bool = False, sc
     ``scale`` defaults to D ** -0.5. Returns (out [Tq, Hq, D], lse float32 [Tq, Hq]); a query that sees no key gets 0 and
     -inf. The tensors may be views (of a packed qkv projection, say) whose rows are whole 16-byte pieces."""
     sizes, pq, pk, scale = _attention_sizes(q, k, v, cu_q, cu_k, scale)
-    nbytes = _api.lib().ddm_attention_forward_workspace_bytes(*sizes)
-    if nbytes == 0:
-        raise _api.DDMError(-4, "ddm_attention_forward_workspace_bytes (unsupported head dimension or sizes)")
+    nbytes = _workspace_bytes("ddm_attention_forward_workspace_bytes", *sizes)
     out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     ws = _api._workspace(nbytes, q.device)
@@ -137,9 +147,7 @@ def attention_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, *, causal:
     _tensor(dout, "dout", q.dtype, q.device, q.shape, contiguous=False)
     _tensor(out, "out", q.dtype, q.device, q.shape)
     _tensor(lse, "lse", torch.float32, q.device, q.shape[:2])
-    nbytes = _api.lib().ddm_attention_backward_workspace_bytes(*sizes)
-    if nbytes == 0:
-        raise _api.DDMError(-4, "ddm_attention_backward_workspace_bytes (unsupported head dimension or sizes)")
+    nbytes = _workspace_bytes("ddm_attention_backward_workspace_bytes", *sizes)
     dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
     dv = torch.empty(k.shape, dtype=q.dtype, device=q.device)
@@ -220,9 +228,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, wtype=None, need_dx: bool 
     dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
     dw = torch.empty(cols, dtype=wt, device=x.device) if need_dweight else None
     db = torch.empty(cols, dtype=wt, device=x.device) if need_dbias else None
-    nbytes = _api.lib().ddm_layer_norm_backward_workspace_bytes(N, cols, _DT[x.dtype])
-    if nbytes == 0:
-        raise _api.DDMError(-4, "ddm_layer_norm_backward_workspace_bytes (unsupported width)")
+    nbytes = _workspace_bytes("ddm_layer_norm_backward_workspace_bytes", N, cols, _DT[x.dtype])
     ws = _api._workspace(nbytes, x.device)
     _call(x.device, "ddm_layer_norm_backward", dy.data_ptr(), x.data_ptr(), ldx, _at(weight), mean.data_ptr(),
           rstd.data_ptr(), N, cols, _DT[x.dtype], _DT[wt], _at(dx), _at(dw), _at(db), ws.data_ptr(), nbytes)
@@ -260,10 +266,7 @@ def _match_sizes(a, b, cu):
     B, pcu = _cu(cu, "cu", a.device)
     P, d = a.shape
     sizes = (B, P, d, _DT[a.dtype])
-    nbytes = _api.lib().ddm_matching_loss_workspace_bytes(*sizes)
-    if nbytes == 0:
-        raise _api.DDMError(-4, "ddm_matching_loss_workspace_bytes (unsupported d or sizes)")
-    return sizes, pcu, nbytes
+    return sizes, pcu, _workspace_bytes("ddm_matching_loss_workspace_bytes", *sizes)
 
 
 def matching_loss_forward(a, b, cu=None, *, temperature: float = 0.07):
