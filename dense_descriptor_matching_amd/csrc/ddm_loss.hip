@@ -157,6 +157,9 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs p, float *loss,
 
 // Backward, one direction: dx of the rows, the gradient by the scores made tile by tile. fp16 holds it to few bits below 2^-14,
 // where a mean over many matches lies: there g is divided by a power of two next to its largest value in reach first.
+// The exponentials bound it, two a score. Where all lse in reach lie within 2^+-30 of a common e^mid, as they do for unit-norm rows
+// unless t is tiny, one is enough: e^{z - lse_y} = e^{z - lse_x} e^{lse_x - mid} e^{mid - lse_y}, the last two known by row and column
+// (what the first loses to underflow is below 2^-66 of g there). fp32 inputs, bound by their products, keep both.
 template <class T, int D, int BN>
 __global__ __launch_bounds__(256, 2) void loss_bwd_kernel(LossArgs p) {
     using TL = Tile<T, D>;
@@ -165,7 +168,7 @@ __global__ __launch_bounds__(256, 2) void loss_bwd_kernel(LossArgs p) {
     constexpr bool exact_exp = sizeof(T) == 4;
     __shared__ __attribute__((aligned(16))) unsigned char lds[2][BN * TL::ROW];
     __shared__ __attribute__((aligned(16))) float st_lse[2][BN], st_g[2][BN];
-    __shared__ float biggest[4];
+    __shared__ float reach[2][4];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     const int dir = blockIdx.z;
     int index;
@@ -181,19 +184,33 @@ __global__ __launch_bounds__(256, 2) void loss_bwd_kernel(LossArgs p) {
     const bool in = row < n;
     const float unit = exact_exp ? 1.f : LOG2E;                // exponents in natural or base-2 units
     const float slope = exact_exp ? p.inv_t : p.c;
-    float scale = 1.f;
-    if constexpr (scaled_ds<T>) {
-        float big = 0.f;
-        for (int j = from + tid; j < to; j += 256) big = fmaxf(big, fabsf(g[j]));
-        if (row0 + tid < n && tid < BM) big = fmaxf(big, fabsf(g[row0 + tid]));
+    float scale = 1.f, mid = 0.f;
+    bool near = false;
+    if constexpr (!exact_exp) {
+        mid = lse_x[row0] * LOG2E;
+        float big = 0.f, off = 0.f;
+        for (int j = from + tid; j < to; j += 256) {
+            off = fmaxf(off, fabsf(lse_y[j] * LOG2E - mid));
+            if constexpr (scaled_ds<T>) big = fmaxf(big, fabsf(g[j]));
+        }
+        if (tid < BM && row0 + tid < n) {
+            off = fmaxf(off, fabsf(lse_x[row0 + tid] * LOG2E - mid));
+            if constexpr (scaled_ds<T>) big = fmaxf(big, fabsf(g[row0 + tid]));
+        }
 #pragma unroll
-        for (int x = 32; x; x >>= 1) big = fmaxf(big, __shfl_xor(big, x));
-        if (lane == 0) biggest[w] = big;
+        for (int x = 32; x; x >>= 1) {
+            off = fmaxf(off, __shfl_xor(off, x));
+            if constexpr (scaled_ds<T>) big = fmaxf(big, __shfl_xor(big, x));
+        }
+        if (lane == 0) { reach[0][w] = off; reach[1][w] = big; }
         __syncthreads();
-        big = fmaxf(fmaxf(biggest[0], biggest[1]), fmaxf(biggest[2], biggest[3]));
-        if (big > 0.f) scale = exp2_fast(fminf(100.f, -(float)__builtin_amdgcn_frexp_expf(big)));
+        off = fmaxf(fmaxf(reach[0][0], reach[0][1]), fmaxf(reach[0][2], reach[0][3]));
+        big = fmaxf(fmaxf(reach[1][0], reach[1][1]), fmaxf(reach[1][2], reach[1][3]));
+        near = __builtin_amdgcn_readfirstlane(off < 30.f);
+        if (scaled_ds<T> && big > 0.f) scale = exp2_fast(fminf(100.f, -(float)__builtin_amdgcn_frexp_expf(big)));
     }
     const float my_g = in ? g[row] * scale : 0.f, half_g = 0.5f * my_g, my_lse = in ? lse_x[row] * unit : INFINITY;
+    const float lift = near && in ? exp2_fast(my_lse - mid) : 0.f;
     Frag<T> xf[DC];
 #pragma unroll
     for (int c = 0; c < DC; ++c) xf[c] = global_rows<T>(xs + (int64_t)(in ? row : n - 1) * p.ld, 16 * c + 8 * h, p.w, in);
@@ -214,35 +231,49 @@ __global__ __launch_bounds__(256, 2) void loss_bwd_kernel(LossArgs p) {
             const bool ok = j0 + tid < to;
             s_lse = ok ? lse_y[j0 + tid] * unit : INFINITY;
             s_g = ok ? 0.5f * scale * g[j0 + tid] : 0.f;
+            if (near && ok) s_g *= exp2_fast(mid - s_lse);
         }
     };
     auto put_stats = [&](int b) {
         if (tid < BN) { st_lse[b][tid] = s_lse; st_g[b][tid] = s_g; }
     };
-    auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, auto special) {
+    auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, bool special) {
         if (t + 1 < t_end) fetch(t + 1, next);
 #pragma unroll
         for (int b = 0; b < BN / 32; ++b) {
             f32x16 z = 0.f;
 #pragma unroll
             for (int c = 0; c < DC; ++c) mma(z, TL::rows(cur, row_at, 32 * b, c), xf[c]);
+            if (near) {
 #pragma unroll
-            for (int r4 = 0; r4 < 4; ++r4) {
-                const int k0 = 32 * b + 8 * r4 + 4 * h;
-                const f32x4 ly = *reinterpret_cast<const f32x4 *>(&st_lse[t & 1][k0]);
-                const f32x4 gy = *reinterpret_cast<const f32x4 *>(&st_g[t & 1][k0]);
+                for (int r4 = 0; r4 < 4; ++r4) {
+                    const f32x4 gy = *reinterpret_cast<const f32x4 *>(&st_g[t & 1][32 * b + 8 * r4 + 4 * h]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float v = z[4 * r4 + e];
-                    float ux = __builtin_fmaf(v, slope, -my_lse), uy = __builtin_fmaf(v, slope, -ly[e]);
-                    if constexpr (exact_exp) { ux *= LOG2E; uy *= LOG2E; }
-                    float dz = __builtin_fmaf(gy[e], exp2_fast(uy), half_g * exp2_fast(ux));
-                    if constexpr (decltype(special)::value) {
-                        const int j = from + t * BN + k0 + e;
-                        if (j == row) { diag = dz - my_g; dz = 0.f; }
-                        if (j >= to) dz = 0.f;
+                    for (int e = 0; e < 4; ++e)
+                        z[4 * r4 + e] = exp2_fast(__builtin_fmaf(z[4 * r4 + e], slope, -my_lse)) *
+                                        __builtin_fmaf(gy[e], lift, half_g);
+                }
+            } else {
+#pragma unroll
+                for (int r4 = 0; r4 < 4; ++r4) {
+                    const int k0 = 32 * b + 8 * r4 + 4 * h;
+                    const f32x4 ly = *reinterpret_cast<const f32x4 *>(&st_lse[t & 1][k0]);
+                    const f32x4 gy = *reinterpret_cast<const f32x4 *>(&st_g[t & 1][k0]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float v = z[4 * r4 + e];
+                        float ux = __builtin_fmaf(v, slope, -my_lse), uy = __builtin_fmaf(v, slope, -ly[e]);
+                        if constexpr (exact_exp) { ux *= LOG2E; uy *= LOG2E; }
+                        z[4 * r4 + e] = __builtin_fmaf(gy[e], exp2_fast(uy), half_g * exp2_fast(ux));
                     }
-                    z[4 * r4 + e] = dz;
+                }
+            }
+            if (special) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int j = from + t * BN + 32 * b + 8 * (r / 4) + 4 * h + r % 4;
+                    if (j == row) diag = z[r] - my_g;
+                    if (j == row || j >= to) z[r] = 0.f;
                 }
             }
 #pragma unroll
@@ -263,8 +294,7 @@ __global__ __launch_bounds__(256, 2) void loss_bwd_kernel(LossArgs p) {
         for (int t = 0; t < t_end; ++t) {
             const int j0 = from + t * BN;
             const bool special = j0 + BN > to || (j0 < row0 + BM && row0 < j0 + BN);
-            if (special) step(t, lds[t & 1], lds[(t + 1) & 1], std::integral_constant<bool, true>{});
-            else step(t, lds[t & 1], lds[(t + 1) & 1], std::integral_constant<bool, false>{});
+            step(t, lds[t & 1], lds[(t + 1) & 1], special);
             if (t + 1 < t_end) put_stats((t + 1) & 1);
             tiles_ready();
         }
