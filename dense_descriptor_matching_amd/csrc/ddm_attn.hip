@@ -85,20 +85,15 @@ hipError_t forward(const AttnArgs &a, const Plan &pl, hipStream_t s) {
     if (pl.split) {
         constexpr int BN = 32;
         const long long slots = slot_count(a.B, a.Tk, 1, pl.chunk);
-        hipLaunchKernelGGL((attn_fwd_kernel<T, D, 1, 1, BN, true>), dim3((unsigned)(slots * a.Hkv), pl.cap / SPLIT_ROWS),
+        hipLaunchKernelGGL((attn_fwd_kernel<T, D, 1, BN, true>), dim3((unsigned)(slots * a.Hkv), pl.cap / SPLIT_ROWS),
                            dim3(64), 0, s, a);
         if (hipError_t e = hipGetLastError()) return e;
         hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3((unsigned)((long long)a.Tq * a.Hq)), dim3(256), 0, s, a);
         return hipGetLastError();
     }
-    constexpr int BN = wide ? 64 : 32, NR = wide && D <= 64 ? 2 : 1;
-    const long long big = slot_count(a.B, a.Tq, G, 128 * NR) * a.Hkv;
-    if (false && (long long)a.Tq * G / 256 * a.Hkv >= 512) {
-        hipLaunchKernelGGL((attn_fwd_kernel<T, D, 4, NR, BN, false>), dim3((unsigned)big), dim3(256), 0, s, a);
-    } else {
-        const long long n = slot_count(a.B, a.Tq, G, 128) * a.Hkv;
-        hipLaunchKernelGGL((attn_fwd_kernel<T, D, 4, 1, BN, false>), dim3((unsigned)n), dim3(256), 0, s, a);
-    }
+    constexpr int BN = wide ? 64 : 32;
+    const long long n = slot_count(a.B, a.Tq, G, 128) * a.Hkv;
+    hipLaunchKernelGGL((attn_fwd_kernel<T, D, 4, BN, false>), dim3((unsigned)n), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -114,10 +109,10 @@ template <class T, int D>
 hipError_t backward(AttnArgs a, hipStream_t s) {
     const int G = a.group.g;
     constexpr bool wide = sizeof(T) == 2;
-    constexpr int BN = wide ? 64 : 32, NR = 1;
+    constexpr int BN = wide ? 64 : 32;
     if (a.Tq) {
-        const long long n = slot_count(a.B, a.Tq, G, 128 * NR) * a.Hkv;
-        hipLaunchKernelGGL((attn_dq_kernel<T, D, 4, NR, BN>), dim3((unsigned)n), dim3(256), 0, s, a);
+        const long long n = slot_count(a.B, a.Tq, G, 128) * a.Hkv;
+        hipLaunchKernelGGL((attn_dq_kernel<T, D, 4, BN>), dim3((unsigned)n), dim3(256), 0, s, a);
         if (hipError_t e = hipGetLastError()) return e;
     }
     if (a.Tk) {

@@ -72,16 +72,15 @@ __device__ __forceinline__ void store4(T *p, float a, float b, float c, float d)
 }
 
 // --------------------------------------------------------------------------------------------------------- forward
-// A workgroup takes BM = 32 NW NR rows (each wave NR blocks of 32) and walks over the keys in tiles of BN, which lie in
-// LDS twice over: while one is used, the next is on its way through registers. Running maximum m (in units of log2) and
-// sum l per row; the accumulator is rescaled only when a row's maximum has grown by more than 2^8 since the last time
-// (any reference gives the same quotient; p stays below 2^8, far inside fp16 and bf16).
-// p is rounded to the inputs' type for the second product, which the matrix cores take; l sums it before that.
+// A workgroup takes BM = 32 NW rows (each wave 32) and walks over the keys in tiles of BN, which have two places in LDS: while one
+// is used, the next is on its way. Running maximum m (in units of log2) and sum l per row; the accumulator is rescaled only when
+// a row's maximum has grown by more than 8 since the last time (any reference gives the same quotient; p stays below 2^8, far
+// inside fp16 and bf16). p is rounded to the inputs' type for the second product, which the matrix cores take; l sums it before that.
 // SPLIT: the workgroup takes a chunk of the keys, for few rows and many keys; attn_join joins the chunks.
-template <class T, int D, int NW, int NR, int BN, bool SPLIT>
+template <class T, int D, int NW, int BN, bool SPLIT>
 __global__ __launch_bounds__(NW * 64, 2) void attn_fwd_kernel(AttnArgs p) {
     using TL = Tile<T, D>;
-    constexpr int BM = NW * NR * 32, KB = BN / 32, DC = D / 16, DB = D / 32;
+    constexpr int BM = NW * 32, KB = BN / 32, DC = D / 16, DB = D / 32;
     constexpr int TILE_BYTES = BN * TL::ROW;
     __shared__ __attribute__((aligned(16))) unsigned char lds[2][2 * TILE_BYTES];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -129,42 +128,28 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_fwd_kernel(AttnArgs p) {
     for (;;) {
         const int row0 = row_tile * BM;
         if (row0 >= rows) return;
-        // rows of this wave
-        Frag<T> qf[NR][DC];
-        int lim[NR], tok[NR], head[NR];
-        int top = 0, low = k_to;
+        const int row = row0 + w * 32 + n;                   // this lane's
+        const bool in = row < rows;
+        const int rr = in ? row : rows - 1, qi = (int)div_by(rr, p.group), head = hk * G + (rr - qi * G);
+        const int lim = p.causal ? min(k_to, qi + shift + 1) : k_to;
+        const T *qr = (const T *)p.q + (int64_t)(sq.lo + qi) * p.q_ts + (int64_t)head * p.q_hs;
+        Frag<T> qf[DC];
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            const int r = row0 + (w * NR + i) * 32 + n;
-            const bool in = r < rows;
-            const int rr = in ? r : rows - 1, qi = (int)div_by(rr, p.group);
-            head[i] = hk * G + (rr - qi * G);
-            tok[i] = in ? sq.lo + qi : -1;
-            lim[i] = p.causal ? min(k_to, qi + shift + 1) : k_to;
-            const T *qr = (const T *)p.q + (int64_t)(sq.lo + qi) * p.q_ts + (int64_t)head[i] * p.q_hs;
-#pragma unroll
-            for (int c = 0; c < DC; ++c) qf[i][c] = global_rows<T>(qr, 16 * c + 8 * h, p.D, in);
-        }
+        for (int c = 0; c < DC; ++c) qf[c] = global_rows<T>(qr, 16 * c + 8 * h, p.D, in);
+        int top = k_to, low = k_to;                          // keys that the last and the first row see
         if (p.causal) {
             top = min(k_to, (int)div_by(min(row0 + BM, rows) - 1, p.group) + shift + 1);
             low = min(k_to, (int)div_by(row0, p.group) + shift + 1);
-        } else {
-            top = k_to;
         }
         const int t_end = top > k_from ? (top - k_from + BN - 1) / BN : 0;
         int wave_top = 0;                                    // keys from here on no row of this wave sees
-        if (const int last = min(row0 + (w + 1) * NR * 32, rows) - 1; last >= row0 + w * NR * 32)
+        if (const int last = min(row0 + (w + 1) * 32, rows) - 1; last >= row0 + w * 32)
             wave_top = p.causal ? min(k_to, (int)div_by(last, p.group) + shift + 1) : k_to;
 
-        f32x16 o[NR][DB];
-        float m[NR], l[NR];
+        f32x16 o[DB];
+        float m = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            m[i] = -INFINITY;
-            l[i] = 0.f;
-#pragma unroll
-            for (int d = 0; d < DB; ++d) o[i][d] = 0.f;
-        }
+        for (int d = 0; d < DB; ++d) o[d] = 0.f;
 
         auto fetch = [&](int t, unsigned char *to) {
             const int j0 = k_from + t * BN, left = min(k_to - j0, BN);
@@ -175,69 +160,53 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_fwd_kernel(AttnArgs p) {
             if (t + 1 < t_end) fetch(t + 1, next);
             if (k_from + t * BN >= wave_top) return;
             const unsigned char *kt = cur, *vt = cur + TILE_BYTES;
-            f32x16 z[NR][KB];
+            f32x16 z[KB];
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
+                z[b] = 0.f;
 #pragma unroll
-                for (int i = 0; i < NR; ++i) z[i][b] = 0.f;
-#pragma unroll
-                for (int c = 0; c < DC; ++c) {
-                    const Frag<T> kf = TL::rows(kt, row_at, 32 * b, c);
-#pragma unroll
-                    for (int i = 0; i < NR; ++i) mma(z[i][b], kf, qf[i][c]);
-                }
+                for (int c = 0; c < DC; ++c) mma(z[b], TL::rows(kt, row_at, 32 * b, c), qf[c]);
             }
-#pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                if (masked) {
-                    const int j0 = k_from + t * BN + 4 * h;
-#pragma unroll
-                    for (int b = 0; b < KB; ++b)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            if (j0 + 32 * b + 8 * (r / 4) + r % 4 >= lim[i]) z[i][b][r] = -INFINITY;
-                }
-                float mx = z[i][0][0];
+            if (masked) {
+                const int j0 = k_from + t * BN + 4 * h;
 #pragma unroll
                 for (int b = 0; b < KB; ++b)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) mx = fmaxf(mx, z[i][b][r]);
-                mx = half_max(mx) * p.c;
-                if (__any(mx > m[i] + 8.f)) {
-                    const float next = fmaxf(m[i], mx);
-                    const float a = next == -INFINITY ? 1.f : exp2_fast(m[i] - next);
-                    l[i] *= a;
-#pragma unroll
-                    for (int d = 0; d < DB; ++d) o[i][d] *= a;
-                    m[i] = next;
-                }
-                const float ref = m[i] == -INFINITY ? 0.f : m[i];
-                float sum = 0.f;
-#pragma unroll
-                for (int b = 0; b < KB; ++b)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        z[i][b][r] = exp2_fast(__builtin_fmaf(z[i][b][r], p.c, -ref));
-                        sum += z[i][b][r];
-                    }
-                l[i] += sum;
+                    for (int r = 0; r < 16; ++r)
+                        if (j0 + 32 * b + 8 * (r / 4) + r % 4 >= lim) z[b][r] = -INFINITY;
             }
+            float mx = z[0][0];
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) mx = fmaxf(mx, z[b][r]);
+            mx = half_max(mx) * p.c;
+            if (__any(mx > m + 8.f)) {
+                const float next = fmaxf(m, mx);
+                const float a = next == -INFINITY ? 1.f : exp2_fast(m - next);
+                l *= a;
+#pragma unroll
+                for (int d = 0; d < DB; ++d) o[d] *= a;
+                m = next;
+            }
+            const float ref = m == -INFINITY ? 0.f : m;
+            float sum = 0.f;
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    z[b][r] = exp2_fast(__builtin_fmaf(z[b][r], p.c, -ref));
+                    sum += z[b][r];
+                }
+            l += sum;
 #pragma unroll
             for (int kc = 0; kc < BN / 16; ++kc) {
-                Frag<T> pf[NR];
+                float x[8];
 #pragma unroll
-                for (int i = 0; i < NR; ++i) {
-                    float x[8];
+                for (int e = 0; e < 8; ++e) x[e] = z[kc / 2][(kc & 1) * 8 + e];
+                const Frag<T> pf = to_frag<T>(x);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = z[i][kc / 2][(kc & 1) * 8 + e];
-                    pf[i] = to_frag<T>(x);
-                }
-#pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    const Frag<T> vf = TL::cols(vt, col_at, 16 * kc, 32 * d);
-#pragma unroll
-                    for (int i = 0; i < NR; ++i) mma(o[i][d], vf, pf[i]);
-                }
+                for (int d = 0; d < DB; ++d) mma(o[d], TL::cols(vt, col_at, 16 * kc, 32 * d), pf);
             }
         };
 
@@ -251,39 +220,31 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_fwd_kernel(AttnArgs p) {
             }
         }
 
-        // the row's sum over both lane halves; row n of block i is this lane's column
+        // the row's sum over both lane halves; the row is this lane's column
+        const float sum = half_sum(l);
+        if (in && whole) {
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            const int64_t at = (int64_t)(sq.lo + qi) * p.Hq + head;
+            T *orow = (T *)p.out + at * p.D;
 #pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            const float sum = half_sum(l[i]);
-            if (tok[i] < 0) continue;
-            if (whole) {
-                const float inv = sum > 0.f ? 1.f / sum : 0.f;
-                T *orow = (T *)p.out + ((int64_t)tok[i] * p.Hq + head[i]) * p.D;
+            for (int d = 0; d < DB; ++d)
 #pragma unroll
-                for (int d = 0; d < DB; ++d)
+                for (int r = 0; r < 16; r += 4) {
+                    const int col = 32 * d + 8 * (r / 4) + 4 * h;
+                    if (col < p.D)
+                        store4<T>(orow + col, o[d][r] * inv, o[d][r + 1] * inv, o[d][r + 2] * inv, o[d][r + 3] * inv);
+                }
+            if (h == 0) p.lse[at] = sum > 0.f ? (m + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f : -INFINITY;
+        } else if (in) {
+            float *part = p.part + ((int64_t)blockIdx.x * p.cap + row) * (p.D + 4);
 #pragma unroll
-                    for (int r = 0; r < 16; r += 4) {
-                        const int col = 32 * d + 8 * (r / 4) + 4 * h;
-                        if (col < p.D)
-                            store4<T>(orow + col, o[i][d][r] * inv, o[i][d][r + 1] * inv, o[i][d][r + 2] * inv,
-                                      o[i][d][r + 3] * inv);
-                    }
-                if (h == 0)
-                    p.lse[(int64_t)tok[i] * p.Hq + head[i]] =
-                        sum > 0.f ? (m[i] + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f : -INFINITY;
-            } else {
-                const int r0 = row0 + (w * NR + i) * 32 + n;
-                float *part = p.part + ((int64_t)blockIdx.x * p.cap + r0) * (p.D + 4);
+            for (int d = 0; d < DB; ++d)
 #pragma unroll
-                for (int d = 0; d < DB; ++d)
-#pragma unroll
-                    for (int r = 0; r < 16; r += 4) {
-                        const int col = 32 * d + 8 * (r / 4) + 4 * h;
-                        if (col < p.D)
-                            store4<float>(part + 4 + col, o[i][d][r], o[i][d][r + 1], o[i][d][r + 2], o[i][d][r + 3]);
-                    }
-                if (h == 0) { part[0] = m[i]; part[1] = sum; }
-            }
+                for (int r = 0; r < 16; r += 4) {
+                    const int col = 32 * d + 8 * (r / 4) + 4 * h;
+                    if (col < p.D) store4<float>(part + 4 + col, o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]);
+                }
+            if (h == 0) { part[0] = m; part[1] = sum; }
         }
         if constexpr (!SPLIT) return;
         // rows past the split ones (longer sequences than the call's average): whole tiles, shared out over the chunks
@@ -368,10 +329,10 @@ constexpr float NO_EXPONENT = -100.f;
 // dq and D_i, one row block at a time as in the forward pass: S and dO V^T of 32 keys from two key tiles' rows, then dS
 // times K from the key tile's columns. No sum crosses workgroups, so the result does not depend on their order; the price
 // is that S and dO V^T are computed here and again in attn_dkv_kernel (7 products instead of 5).
-template <class T, int D, int NW, int NR, int BN>
+template <class T, int D, int NW, int BN>
 __global__ __launch_bounds__(NW * 64, 2) void attn_dq_kernel(AttnArgs p) {
     using TL = Tile<T, D>;
-    constexpr int BM = NW * NR * 32, DC = D / 16, DB = D / 32;
+    constexpr int BM = NW * 32, DC = D / 16, DB = D / 32;
     constexpr int TILE_BYTES = BN * TL::ROW;
     __shared__ __attribute__((aligned(16))) unsigned char lds[2][2 * TILE_BYTES];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -397,49 +358,41 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dq_kernel(AttnArgs p) {
     }
     const int row_at = TL::row_base(lane), col_at = TL::col_base(lane);
 
-    Frag<T> qf[NR][DC], gf[NR][DC];
-    int lim[NR];
-    int64_t at[NR];
-    float lse[NR], delta[NR], inv[NR];
+    const int r = row0 + w * 32 + n;
+    const bool in = r < rows;
+    const int rr = in ? r : rows - 1, qi = (int)div_by(rr, p.group), head = hk * G + (rr - qi * G);
+    const int lim = p.causal ? min(Lk, qi + shift + 1) : Lk;
+    const int64_t tok = sq.lo + qi, at = tok * p.Hq + head;
+    const T *qr = (const T *)p.q + tok * p.q_ts + (int64_t)head * p.q_hs;
+    const T *gr = (const T *)p.dout + tok * p.g_ts + (int64_t)head * p.g_hs;
+    const T *orow = (const T *)p.o + at * p.D;
+    Frag<T> qf[DC], gf[DC];
+    float delta = 0.f, big = 0.f;
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        const int r = row0 + (w * NR + i) * 32 + n;
-        const bool in = r < rows;
-        const int rr = in ? r : rows - 1, qi = (int)div_by(rr, p.group), head = hk * G + (rr - qi * G);
-        const int64_t tok = sq.lo + qi;
-        lim[i] = p.causal ? min(Lk, qi + shift + 1) : Lk;
-        at[i] = in ? tok * p.Hq + head : -1;
-        const T *qr = (const T *)p.q + tok * p.q_ts + (int64_t)head * p.q_hs;
-        const T *gr = (const T *)p.dout + tok * p.g_ts + (int64_t)head * p.g_hs;
-        const T *orow = (const T *)p.o + (tok * p.Hq + head) * p.D;
-        float sum = 0.f, big = 0.f;
+    for (int c = 0; c < DC; ++c) {
+        qf[c] = global_rows<T>(qr, 16 * c + 8 * h, p.D, in);
+        gf[c] = global_rows<T>(gr, 16 * c + 8 * h, p.D, in);
+        const Frag<T> of = global_rows<T>(orow, 16 * c + 8 * h, p.D, in);
 #pragma unroll
-        for (int c = 0; c < DC; ++c) {
-            qf[i][c] = global_rows<T>(qr, 16 * c + 8 * h, p.D, in);
-            gf[i][c] = global_rows<T>(gr, 16 * c + 8 * h, p.D, in);
-            const Frag<T> of = global_rows<T>(orow, 16 * c + 8 * h, p.D, in);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                sum = __builtin_fmaf((float)gf[i][c][e], (float)of[e], sum);
-                if constexpr (scaled_ds<T>) big = fmaxf(big, fabsf((float)gf[i][c][e]));
-            }
+        for (int e = 0; e < 8; ++e) {
+            delta = __builtin_fmaf((float)gf[c][e], (float)of[e], delta);
+            if constexpr (scaled_ds<T>) big = fmaxf(big, fabsf((float)gf[c][e]));
         }
-        delta[i] = half_sum(sum);
-        const float z = in ? p.lse[at[i]] : -INFINITY;
-        lse[i] = z == -INFINITY ? INFINITY : z * 1.44269504088896341f;      // a row that sees no key: every P is 0
-        inv[i] = 1.f;
-        float ex = NO_EXPONENT;
-        if constexpr (scaled_ds<T>) {
-            big = half_max(big);
-            if (big > 0.f) ex = fmaxf(NO_EXPONENT, (float)__builtin_amdgcn_frexp_expf(big));
-            inv[i] = exp2_fast(-ex);
-        }
-        if (in && h == 0) {
-            const int64_t all = (int64_t)p.Tq * p.Hq;
-            p.stats[at[i]] = lse[i];
-            p.stats[at[i] + all] = delta[i];
-            if constexpr (scaled_ds<T>) p.stats[at[i] + 2 * all] = ex - NO_EXPONENT;
-        }
+    }
+    delta = half_sum(delta);
+    const float z = in ? p.lse[at] : -INFINITY;
+    const float lse = z == -INFINITY ? INFINITY : z * 1.44269504088896341f;      // a row that sees no key: every P is 0
+    float inv = 1.f, ex = NO_EXPONENT;
+    if constexpr (scaled_ds<T>) {
+        big = half_max(big);
+        if (big > 0.f) ex = fmaxf(NO_EXPONENT, (float)__builtin_amdgcn_frexp_expf(big));
+        inv = exp2_fast(-ex);
+    }
+    if (in && h == 0) {
+        const int64_t all = (int64_t)p.Tq * p.Hq;
+        p.stats[at] = lse;
+        p.stats[at + all] = delta;
+        if constexpr (scaled_ds<T>) p.stats[at + 2 * all] = ex - NO_EXPONENT;
     }
     int top = Lk, low = Lk;
     if (p.causal) {
@@ -448,14 +401,12 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dq_kernel(AttnArgs p) {
     }
     const int t_end = top > 0 ? (top + BN - 1) / BN : 0;
     int wave_top = 0;
-    if (const int last = min(row0 + (w + 1) * NR * 32, rows) - 1; last >= row0 + w * NR * 32)
+    if (const int last = min(row0 + (w + 1) * 32, rows) - 1; last >= row0 + w * 32)
         wave_top = p.causal ? min(Lk, (int)div_by(last, p.group) + shift + 1) : Lk;
 
-    f32x16 dq[NR][DB];
+    f32x16 dq[DB];
 #pragma unroll
-    for (int i = 0; i < NR; ++i)
-#pragma unroll
-        for (int d = 0; d < DB; ++d) dq[i][d] = 0.f;
+    for (int d = 0; d < DB; ++d) dq[d] = 0.f;
 
     auto fetch = [&](int t, unsigned char *to) {
         const int j0 = t * BN, left = min(Lk - j0, BN);
@@ -468,50 +419,32 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dq_kernel(AttnArgs p) {
         const unsigned char *kt = cur, *vt = cur + TILE_BYTES;
 #pragma unroll
         for (int b = 0; b < BN / 32; ++b) {
-            f32x16 z[NR], y[NR];
-#pragma unroll
-            for (int i = 0; i < NR; ++i) { z[i] = 0.f; y[i] = 0.f; }
+            f32x16 z = 0.f, y = 0.f;
 #pragma unroll
             for (int c = 0; c < DC; ++c) {
-                const Frag<T> kf = TL::rows(kt, row_at, 32 * b, c), vf = TL::rows(vt, row_at, 32 * b, c);
-#pragma unroll
-                for (int i = 0; i < NR; ++i) {
-                    mma(z[i], kf, qf[i][c]);
-                    mma(y[i], vf, gf[i][c]);
-                }
+                mma(z, TL::rows(kt, row_at, 32 * b, c), qf[c]);
+                mma(y, TL::rows(vt, row_at, 32 * b, c), gf[c]);
             }
 #pragma unroll
-            for (int i = 0; i < NR; ++i)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float pr = exp2_fast(__builtin_fmaf(z[i][r], p.c, -lse[i]));
-                    float ds = pr * (y[i][r] - delta[i]);
-                    if constexpr (scaled_ds<T>) ds *= inv[i];
-                    z[i][r] = ds;
-                }
+            for (int r = 0; r < 16; ++r) {
+                const float pr = exp2_fast(__builtin_fmaf(z[r], p.c, -lse));
+                float ds = pr * (y[r] - delta);
+                if constexpr (scaled_ds<T>) ds *= inv;
+                z[r] = ds;
+            }
             if (masked) {
 #pragma unroll
-                for (int i = 0; i < NR; ++i)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (t * BN + 32 * b + 4 * h + 8 * (r / 4) + r % 4 >= lim[i]) z[i][r] = 0.f;
+                for (int r = 0; r < 16; ++r)
+                    if (t * BN + 32 * b + 4 * h + 8 * (r / 4) + r % 4 >= lim) z[r] = 0.f;
             }
 #pragma unroll
             for (int kc = 0; kc < 2; ++kc) {
-                Frag<T> sf[NR];
+                float v[8];
 #pragma unroll
-                for (int i = 0; i < NR; ++i) {
-                    float v[8];
+                for (int e = 0; e < 8; ++e) v[e] = z[kc * 8 + e];
+                const Frag<T> sf = to_frag<T>(v);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = z[i][kc * 8 + e];
-                    sf[i] = to_frag<T>(v);
-                }
-#pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    const Frag<T> kf = TL::cols(kt, col_at, 32 * b + 16 * kc, 32 * d);
-#pragma unroll
-                    for (int i = 0; i < NR; ++i) mma(dq[i][d], kf, sf[i]);
-                }
+                for (int d = 0; d < DB; ++d) mma(dq[d], TL::cols(kt, col_at, 32 * b + 16 * kc, 32 * d), sf);
             }
         }
     };
@@ -524,20 +457,17 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dq_kernel(AttnArgs p) {
             tiles_ready();
         }
     }
+    if (!in) return;
+    const float f = scaled_ds<T> ? p.scale / inv : p.scale;
+    T *row = (T *)p.dq + at * p.D;
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        if (at[i] < 0) continue;
-        const float f = scaled_ds<T> ? p.scale / inv[i] : p.scale;
-        T *row = (T *)p.dq + at[i] * p.D;
+    for (int d = 0; d < DB; ++d)
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-            for (int r = 0; r < 16; r += 4) {
-                const int col = 32 * d + 8 * (r / 4) + 4 * h;
-                if (col < p.D)
-                    store4<T>(row + col, dq[i][d][r] * f, dq[i][d][r + 1] * f, dq[i][d][r + 2] * f, dq[i][d][r + 3] * f);
-            }
-    }
+        for (int r = 0; r < 16; r += 4) {
+            const int col = 32 * d + 8 * (r / 4) + 4 * h;
+            if (col < p.D)
+                store4<T>(row + col, dq[d][r] * f, dq[d][r + 1] * f, dq[d][r + 2] * f, dq[d][r + 3] * f);
+        }
 }
 
 // dk and dv: a workgroup of KW waves keeps 32 KW keys (their K, and V where there is room, as operands in registers) and walks
