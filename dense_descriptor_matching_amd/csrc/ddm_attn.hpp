@@ -116,13 +116,6 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_fwd_kernel(AttnArgs p) {
     }
     const T *kb = (const T *)p.k + (int64_t)sk.lo * p.k_ts + (int64_t)hk * p.k_hs;
     const T *vb = (const T *)p.v + (int64_t)sk.lo * p.v_ts + (int64_t)hk * p.v_hs;
-    using In = Dma<T, D, NW, BN>;
-    int koff[In::N], voff[In::N];
-#pragma unroll
-    for (int i = 0; i < In::N; ++i) {
-        koff[i] = In::offset(i, w, lane, p.k_ts, p.D);
-        voff[i] = In::offset(i, w, lane, p.v_ts, p.D);
-    }
     const int row_at = TL::row_base(lane), col_at = TL::col_base(lane);
 
     for (;;) {
@@ -151,13 +144,14 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_fwd_kernel(AttnArgs p) {
 #pragma unroll
         for (int d = 0; d < DB; ++d) o[d] = 0.f;
 
-        auto fetch = [&](int t, unsigned char *to) {
-            const int j0 = k_from + t * BN, left = min(k_to - j0, BN);
-            In::load(buffer_of(kb + (int64_t)j0 * p.k_ts, rows_bytes<T>(left, p.k_ts, p.D)), koff, to, w);
-            In::load(buffer_of(vb + (int64_t)j0 * p.v_ts, rows_bytes<T>(left, p.v_ts, p.D)), voff, to + TILE_BYTES, w);
+        Walk<T, D, NW, BN> ks(kb + (int64_t)k_from * p.k_ts, k_to - k_from, p.k_ts, p.D, w, lane);
+        Walk<T, D, NW, BN> vs(vb + (int64_t)k_from * p.v_ts, k_to - k_from, p.v_ts, p.D, w, lane);
+        auto fetch = [&](unsigned char *to) {
+            ks.next(to, w);
+            vs.next(to + TILE_BYTES, w);
         };
         auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, bool masked) {
-            if (t + 1 < t_end) fetch(t + 1, next);
+            if (t + 1 < t_end) fetch(next);
             if (k_from + t * BN >= wave_top) return;
             const unsigned char *kt = cur, *vt = cur + TILE_BYTES;
             f32x16 z[KB];
@@ -211,7 +205,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_fwd_kernel(AttnArgs p) {
         };
 
         if (t_end > 0) {
-            fetch(0, lds[0]);
+            fetch(lds[0]);
             tiles_ready();
             const int t_full = max(0, min(t_end, (low - k_from) / BN));      // tiles that every row sees whole
             for (int t = 0; t < t_end; ++t) {
@@ -349,13 +343,6 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dq_kernel(AttnArgs p) {
     if (row0 >= rows) return;
     const T *kb = (const T *)p.k + (int64_t)sk.lo * p.k_ts + (int64_t)hk * p.k_hs;
     const T *vb = (const T *)p.v + (int64_t)sk.lo * p.v_ts + (int64_t)hk * p.v_hs;
-    using In = Dma<T, D, NW, BN>;
-    int koff[In::N], voff[In::N];
-#pragma unroll
-    for (int i = 0; i < In::N; ++i) {
-        koff[i] = In::offset(i, w, lane, p.k_ts, p.D);
-        voff[i] = In::offset(i, w, lane, p.v_ts, p.D);
-    }
     const int row_at = TL::row_base(lane), col_at = TL::col_base(lane);
 
     const int r = row0 + w * 32 + n;
@@ -408,13 +395,13 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dq_kernel(AttnArgs p) {
 #pragma unroll
     for (int d = 0; d < DB; ++d) dq[d] = 0.f;
 
-    auto fetch = [&](int t, unsigned char *to) {
-        const int j0 = t * BN, left = min(Lk - j0, BN);
-        In::load(buffer_of(kb + (int64_t)j0 * p.k_ts, rows_bytes<T>(left, p.k_ts, p.D)), koff, to, w);
-        In::load(buffer_of(vb + (int64_t)j0 * p.v_ts, rows_bytes<T>(left, p.v_ts, p.D)), voff, to + TILE_BYTES, w);
+    Walk<T, D, NW, BN> ks(kb, Lk, p.k_ts, p.D, w, lane), vs(vb, Lk, p.v_ts, p.D, w, lane);
+    auto fetch = [&](unsigned char *to) {
+        ks.next(to, w);
+        vs.next(to + TILE_BYTES, w);
     };
     auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, bool masked) {
-        if (t + 1 < t_end) fetch(t + 1, next);
+        if (t + 1 < t_end) fetch(next);
         if (t * BN >= wave_top) return;
         const unsigned char *kt = cur, *vt = cur + TILE_BYTES;
 #pragma unroll
@@ -449,7 +436,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dq_kernel(AttnArgs p) {
         }
     };
     if (t_end > 0) {
-        fetch(0, lds[0]);
+        fetch(lds[0]);
         tiles_ready();
         const int t_full = max(0, min(t_end, low / BN));
         for (int t = 0; t < t_end; ++t) {

@@ -45,7 +45,6 @@ __device__ __forceinline__ void piece_of(int n, int S, int s, int tile, int *fro
 template <class T, int D, int BN>
 __global__ __launch_bounds__(256, 2) void loss_fwd_kernel(LossArgs p) {
     using TL = Tile<T, D>;
-    using In = Dma<T, D, 4, BN>;
     constexpr int DC = D / 16, KB = BN / 32, BM = 128;
     __shared__ __attribute__((aligned(16))) unsigned char lds[2][BN * TL::ROW];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
@@ -63,18 +62,12 @@ __global__ __launch_bounds__(256, 2) void loss_fwd_kernel(LossArgs p) {
     Frag<T> xf[DC];
 #pragma unroll
     for (int c = 0; c < DC; ++c) xf[c] = global_rows<T>(xs + (int64_t)(in ? row : n - 1) * p.ld, 16 * c + 8 * h, p.w, in);
-    int off[In::N];
-#pragma unroll
-    for (int i = 0; i < In::N; ++i) off[i] = In::offset(i, w, lane, p.ld, p.w);
+    Walk<T, D, 4, BN> tiles(ys + (int64_t)from * p.ld, to - from, p.ld, p.w, w, lane);
     const int row_at = TL::row_base(lane);
     float m = -INFINITY, l = 0.f, hit = -INFINITY;
     const int t_end = (to - from + BN - 1) / BN;
-    auto fetch = [&](int t, unsigned char *dst) {
-        const int j0 = from + t * BN;
-        In::load(buffer_of(ys + (int64_t)j0 * p.ld, rows_bytes<T>(min(to - j0, BN), p.ld, p.w)), off, dst, w);
-    };
     auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, auto special) {
-        if (t + 1 < t_end) fetch(t + 1, next);
+        if (t + 1 < t_end) tiles.next(next, w);
         f32x16 z[KB];
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
@@ -113,7 +106,7 @@ __global__ __launch_bounds__(256, 2) void loss_fwd_kernel(LossArgs p) {
         m = next_m;
     };
     if (t_end > 0) {
-        fetch(0, lds[0]);
+        tiles.next(lds[0], w);
         tiles_ready();
         for (int t = 0; t < t_end; ++t) {
             const int j0 = from + t * BN;
@@ -163,7 +156,6 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs p, float *loss,
 template <class T, int D, int BN>
 __global__ __launch_bounds__(256, 2) void loss_bwd_kernel(LossArgs p) {
     using TL = Tile<T, D>;
-    using In = Dma<T, D, 4, BN>;
     constexpr int DC = D / 16, DB = D / 32, BM = 128;
     constexpr bool exact_exp = sizeof(T) == 4;
     __shared__ __attribute__((aligned(16))) unsigned char lds[2][BN * TL::ROW];
@@ -214,9 +206,7 @@ __global__ __launch_bounds__(256, 2) void loss_bwd_kernel(LossArgs p) {
     Frag<T> xf[DC];
 #pragma unroll
     for (int c = 0; c < DC; ++c) xf[c] = global_rows<T>(xs + (int64_t)(in ? row : n - 1) * p.ld, 16 * c + 8 * h, p.w, in);
-    int off[In::N];
-#pragma unroll
-    for (int i = 0; i < In::N; ++i) off[i] = In::offset(i, w, lane, p.ld, p.w);
+    Walk<T, D, 4, BN> tiles(ys + (int64_t)from * p.ld, to - from, p.ld, p.w, w, lane);
     const int row_at = TL::row_base(lane), col_at = TL::col_base(lane);
     float diag = 0.f;                                          // dz_ii, kept out of the rounded products: it is the largest
     f32x16 dx[DB];
@@ -226,7 +216,7 @@ __global__ __launch_bounds__(256, 2) void loss_bwd_kernel(LossArgs p) {
     float s_lse = INFINITY, s_g = 0.f;
     auto fetch = [&](int t, unsigned char *dst) {
         const int j0 = from + t * BN;
-        In::load(buffer_of(ys + (int64_t)j0 * p.ld, rows_bytes<T>(min(to - j0, BN), p.ld, p.w)), off, dst, w);
+        tiles.next(dst, w);
         if (tid < BN) {
             const bool ok = j0 + tid < to;
             s_lse = ok ? lse_y[j0 + tid] * unit : INFINITY;

@@ -151,6 +151,34 @@ struct Dma {
     }
 };
 
+// The tiles of ROWS rows of a strided matrix, one after another from `at` on; `rows` counts those that are left.
+template <class T, int D, int NW, int ROWS>
+struct Walk {
+    using In = Dma<T, D, NW, ROWS>;
+    const T *at;
+    int64_t pitch;                                     // elements from one tile to the next
+    int off[In::N], rows, lane_row;
+    __device__ __forceinline__ Walk(const T *first, int rows, int64_t ts, int d, int w, int lane)
+        : at(first), pitch(ROWS * ts), rows(rows), lane_row(In::row(0, w, lane)) {
+#pragma unroll
+        for (int i = 0; i < In::N; ++i) off[i] = In::offset(i, w, lane, ts, d);
+    }
+    // The next tile; rows that are not there are zeros. Whole tiles cost a few scalar instructions.
+    __device__ __forceinline__ void next(unsigned char *to, int w) {
+        const auto b = buffer_of(at, OUTSIDE);
+        if (rows >= ROWS) {
+            In::load(b, off, to, w);
+        } else {
+            int o[In::N];
+#pragma unroll
+            for (int i = 0; i < In::N; ++i) o[i] = lane_row + i * (64 / In::TL::NP) < rows ? off[i] : OUTSIDE;
+            In::load(b, o, to, w);
+        }
+        at += pitch;
+        rows -= ROWS;
+    }
+};
+
 // This wave's loads to LDS have landed, then everyone's.
 __device__ __forceinline__ void tiles_ready() {
     __builtin_amdgcn_s_waitcnt(0x0f70);                // vmcnt(0)
