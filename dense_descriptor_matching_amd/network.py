@@ -64,6 +64,7 @@ def _workspace_bytes(what, *sizes):
 
 
 def _tensor(t, name, dtype=None, dev=None, shape=None, contiguous=True):
+    """t, checked: a device tensor of the dtype (None: any supported), device and shape asked for."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a device tensor")
     if dtype is None:
@@ -73,7 +74,7 @@ def _tensor(t, name, dtype=None, dev=None, shape=None, contiguous=True):
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if dev is not None and t.device != dev:
         raise ValueError(f"tensors on {dev} and {t.device}: one device per call")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -132,9 +133,9 @@ def attention_forward(q, k, v, cu_q=None, cu_k=None, *, causal: bool = False, sc
     -inf. The tensors may be views (of a packed qkv projection, say) whose rows are whole 16-byte pieces."""
     sizes, pq, pk, scale = _attention_sizes(q, k, v, cu_q, cu_k, scale)
     nbytes = _workspace_bytes("ddm_attention_forward_workspace_bytes", *sizes)
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    ws = _api._workspace(nbytes, q.device)
+    out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    lse = q.new_empty(q.shape[:2], dtype=torch.float32)
+    ws = q.new_empty(nbytes, dtype=torch.uint8)
     _call(q.device, "ddm_attention_forward", *_heads_view(q, "q"), *_heads_view(k, "k"), *_heads_view(v, "v"), pq, pk,
           *sizes, int(causal), scale, out.data_ptr(), lse.data_ptr(), ws.data_ptr(), nbytes)
     return out, lse
@@ -148,10 +149,8 @@ def attention_backward(dout, q, k, v, out, lse, cu_q=None, cu_k=None, *, causal:
     _tensor(out, "out", q.dtype, q.device, q.shape)
     _tensor(lse, "lse", torch.float32, q.device, q.shape[:2])
     nbytes = _workspace_bytes("ddm_attention_backward_workspace_bytes", *sizes)
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    dv = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    ws = _api._workspace(nbytes, q.device)
+    dq, dk, dv = (torch.empty_like(t, memory_format=torch.contiguous_format) for t in (q, k, v))
+    ws = q.new_empty(nbytes, dtype=torch.uint8)
     _call(q.device, "ddm_attention_backward", *_heads_view(dout, "dout"), *_heads_view(q, "q"), *_heads_view(k, "k"),
           *_heads_view(v, "v"), out.data_ptr(), lse.data_ptr(), pq, pk, *sizes, int(causal), scale, dq.data_ptr(),
           dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), nbytes)
@@ -190,7 +189,7 @@ def _norm_rows(x, weight, bias):
     wtype = torch.float32
     for t, name in ((weight, "weight"), (bias, "bias")):
         if t is not None:
-            wtype = _tensor(t, name, None, x.device, (cols,)).dtype
+            wtype = _tensor(t, name, None, x.device, x.shape[-1:]).dtype
     if weight is not None and bias is not None and weight.dtype != bias.dtype:
         raise TypeError("weight and bias must share their dtype")
     if wtype not in (torch.float32, x.dtype):
@@ -206,9 +205,9 @@ def _at(t):
 def layer_norm_forward(x, weight=None, bias=None, *, eps: float = 1e-6):
     """Layer norm over the last dimension. Returns (y like x, mean, rstd float32 over the rows)."""
     N, cols, ldx, wtype = _norm_rows(x, weight, bias)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    rstd = torch.empty_like(mean)
     _call(x.device, "ddm_layer_norm_forward", x.data_ptr(), ldx, _at(weight), _at(bias), N, cols, _DT[x.dtype],
           _DT[wtype], float(eps), y.data_ptr(), mean.data_ptr(), rstd.data_ptr())
     return y, mean, rstd
@@ -225,11 +224,11 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, wtype=None, need_dx: bool 
     _tensor(dy, "dy", x.dtype, x.device, x.shape)
     _tensor(mean, "mean", torch.float32, x.device, x.shape[:-1])
     _tensor(rstd, "rstd", torch.float32, x.device, x.shape[:-1])
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
-    dw = torch.empty(cols, dtype=wt, device=x.device) if need_dweight else None
-    db = torch.empty(cols, dtype=wt, device=x.device) if need_dbias else None
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
+    dw = x.new_empty(cols, dtype=wt) if need_dweight else None
+    db = x.new_empty(cols, dtype=wt) if need_dbias else None
     nbytes = _workspace_bytes("ddm_layer_norm_backward_workspace_bytes", N, cols, _DT[x.dtype])
-    ws = _api._workspace(nbytes, x.device)
+    ws = x.new_empty(nbytes, dtype=torch.uint8)
     _call(x.device, "ddm_layer_norm_backward", dy.data_ptr(), x.data_ptr(), ldx, _at(weight), mean.data_ptr(),
           rstd.data_ptr(), N, cols, _DT[x.dtype], _DT[wt], _at(dx), _at(dw), _at(db), ws.data_ptr(), nbytes)
     return dx, dw, db
@@ -273,8 +272,9 @@ def matching_loss_forward(a, b, cu=None, *, temperature: float = 0.07):
     """Symmetric softmax loss of matched descriptors a, b [P, d]: row p of one is to find row p of the other among the
     rows of its set (an image pair's matches; ``cu`` bounds the sets). Returns (loss, lse_a, lse_b), float32 [P]."""
     sizes, pcu, nbytes = _match_sizes(a, b, cu)
-    loss, lse_a, lse_b = torch.empty(3, a.shape[0], dtype=torch.float32, device=a.device).unbind(0)
-    ws = _api._workspace(nbytes, a.device)
+    loss = a.new_empty(a.shape[:1], dtype=torch.float32)
+    lse_a, lse_b = torch.empty_like(loss), torch.empty_like(loss)
+    ws = a.new_empty(nbytes, dtype=torch.uint8)
     _call(a.device, "ddm_matching_loss_forward", a.data_ptr(), b.data_ptr(), pcu, *sizes, float(temperature),
           loss.data_ptr(), lse_a.data_ptr(), lse_b.data_ptr(), ws.data_ptr(), nbytes)
     return loss, lse_a, lse_b
@@ -286,7 +286,7 @@ def matching_loss_backward(dloss, a, b, lse_a, lse_b, cu=None, *, temperature: f
     for t, name in ((dloss, "dloss"), (lse_a, "lse_a"), (lse_b, "lse_b")):
         _tensor(t, name, torch.float32, a.device, a.shape[:1])
     da, db = torch.empty_like(a), torch.empty_like(b)
-    ws = _api._workspace(nbytes, a.device)
+    ws = a.new_empty(nbytes, dtype=torch.uint8)
     _call(a.device, "ddm_matching_loss_backward", dloss.data_ptr(), a.data_ptr(), b.data_ptr(), lse_a.data_ptr(),
           lse_b.data_ptr(), pcu, *sizes, float(temperature), da.data_ptr(), db.data_ptr(), ws.data_ptr(), nbytes)
     return da, db
