@@ -32,7 +32,7 @@ Plan make_plan(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int D) {
     // Split the keys where whole rows would leave most of the 256 CUs without work: few workgroups of 128 rows, and keys
     // enough per sequence for two chunks.
     const long long wgs = (rows / 128 + B) * Hkv;
-    p.split = rows <= 64ll * B && wgs < 1024 && Tk / B >= 128;
+    p.split = rows <= 64ll * B && wgs < 1024 && Tk / B >= 128 && (long long)Tq * Hq < 1 << 24;
     if (p.split) {
         // some 2048 workgroups of one wave over all keys, in whole tiles of 64 keys
         const long long avg = ((long long)Tk * Hkv + 2047) / 2048;
@@ -64,17 +64,19 @@ int check(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int D) {
     if (B < 1 || Tq < 0 || Tk < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv) return DDM_ERR_INVALID;
     if (D < 1 || D > DDM_MAX_D || D * esize(dtype) % 16) return DDM_ERR_UNSUPPORTED;
     const long long G = Hq / Hkv;
-    if ((long long)Tq * Hq >= INT_MAX || B > (1 << 20) || (long long)Tq * G * G >= (1ll << 31) || Tk >= INT_MAX - (1 << 22)) return DDM_ERR_INVALID;
-    if (((long long)Tq * G / 32 + B + 2) * Hkv >= INT_MAX || ((long long)Tk / 32 + B + 2) * Hkv >= INT_MAX)
-        return DDM_ERR_INVALID;
+    if (B > (1 << 20) || (long long)Tq * G * G >= (1ll << 31) || Tk >= INT_MAX - (1 << 22)) return DDM_ERR_INVALID;
+    // a launch has fewer than 2^32 threads
+    if (slot_count(B, Tq, (int)G, 128) * Hkv >= 1 << 24 || slot_count(B, Tk, 1, KEYS) * Hkv >= 1 << 24) return DDM_ERR_INVALID;
     return DDM_OK;
 }
 
-// Rows are whole 16-byte pieces at 16-byte boundaries, and 64 of them lie within 31-bit offsets.
-bool bad_view(const void *p, int64_t ts, int64_t hs, int heads, int dtype) {
+// Rows are whole 16-byte pieces at 16-byte boundaries, and 64 tokens of a tile, with `heads` heads of each, lie within 31-bit
+// offsets.
+bool bad_view(const void *p, int64_t ts, int64_t hs, int dtype, int heads = 1) {
     const int e = esize(dtype);
-    if (!p || (uintptr_t)p % 16 || ts < 0 || hs < 0 || ts * e % 16 || hs * e % 16) return true;
-    return ts * e >= (1ll << 24) || hs * e >= (1ll << 24) || hs * e * heads >= (1ll << 29);
+    if (!p || (uintptr_t)p % 16 || ts < 0 || hs < 0 || ts >= (1ll << 40) || hs >= (1ll << 40)) return true;
+    if (ts * e % 16 || hs * e % 16 || ts * e >= (1ll << 24)) return true;
+    return heads > 1 && hs * e >= (1ll << 29) / heads;
 }
 bool bad_ptr(const void *p) { return !p || (uintptr_t)p % 16; }
 
@@ -157,8 +159,8 @@ int ddm_attention_forward(const void *q, int64_t q_ts, int64_t q_hs, const void 
     if (!(scale > 0) || !std::isfinite(scale) || (causal != 0 && causal != 1)) return DDM_ERR_INVALID;
     if ((!cu_q || !cu_k) && B != 1) return DDM_ERR_INVALID;
     if (Tq == 0) return DDM_OK;
-    if (bad_view(q, q_ts, q_hs, Hq, dtype) || bad_ptr(out) || bad_ptr(lse)) return DDM_ERR_INVALID;
-    if (Tk && (bad_view(k, k_ts, k_hs, Hkv, dtype) || bad_view(v, v_ts, v_hs, Hkv, dtype))) return DDM_ERR_INVALID;
+    if (bad_view(q, q_ts, q_hs, dtype) || bad_ptr(out) || bad_ptr(lse)) return DDM_ERR_INVALID;
+    if (Tk && (bad_view(k, k_ts, k_hs, dtype) || bad_view(v, v_ts, v_hs, dtype))) return DDM_ERR_INVALID;
     const Plan pl = make_plan(dtype, B, Tq, Tk, Hq, Hkv, D);
     if (pl.bytes && (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < pl.bytes)) return DDM_ERR_WORKSPACE;
     AttnArgs a{};
@@ -188,10 +190,10 @@ int ddm_attention_backward(const void *dout, int64_t g_ts, int64_t g_hs, const v
     if (int rc = check(dtype, B, Tq, Tk, Hq, Hkv, D)) return rc;
     if (!(scale > 0) || !std::isfinite(scale) || (causal != 0 && causal != 1)) return DDM_ERR_INVALID;
     if ((!cu_q || !cu_k) && B != 1) return DDM_ERR_INVALID;
-    if (Tq && (bad_view(q, q_ts, q_hs, Hq, dtype) || bad_view(dout, g_ts, g_hs, Hq, dtype) || bad_ptr(out) || bad_ptr(lse) ||
+    if (Tq && (bad_view(q, q_ts, q_hs, dtype, Hq / Hkv) || bad_view(dout, g_ts, g_hs, dtype, Hq / Hkv) || bad_ptr(out) || bad_ptr(lse) ||
                bad_ptr(dq)))
         return DDM_ERR_INVALID;
-    if (Tk && (bad_view(k, k_ts, k_hs, Hkv, dtype) || bad_view(v, v_ts, v_hs, Hkv, dtype) || bad_ptr(dk) || bad_ptr(dv)))
+    if (Tk && (bad_view(k, k_ts, k_hs, dtype) || bad_view(v, v_ts, v_hs, dtype) || bad_ptr(dk) || bad_ptr(dv)))
         return DDM_ERR_INVALID;
     const BackPlan bp = make_back_plan(dtype, B, Tq, Tk, Hq, Hkv, D);
     if (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < bp.bytes) return DDM_ERR_WORKSPACE;

@@ -272,7 +272,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
     if (sq == 0 || sq == p.B + 1) k.hi = k.lo;
     const int G = p.group.g, hk = head / G, r = (tok - q.lo) * G + head % G;
     const int chunks = (k.hi - k.lo + p.chunk - 1) / p.chunk;
-    if (chunks > 0 && r >= p.cap) return;                       // written whole
+    if (r < 0 || (chunks > 0 && r >= p.cap)) return;            // cu out of order; rows that were written whole
     const int slot0 = k.lo / p.chunk + sq;
     const float *part = p.part + (((int64_t)slot0 * p.Hkv + hk) * p.cap + r) * (p.D + 4);
     const int64_t pitch = (int64_t)p.Hkv * p.cap * (p.D + 4);

@@ -374,7 +374,7 @@ Plan make_plan(int B, int P, int d, int dtype) {
 int check(int B, int P, int d, int dtype) {
     if (dtype != DDM_F32 && dtype != DDM_F16 && dtype != DDM_BF16) return DDM_ERR_UNSUPPORTED;
     if (d < 1 || d > DDM_MAX_D) return DDM_ERR_UNSUPPORTED;
-    if (B < 1 || B > (1 << 20) || P < 0 || P > (1 << 28)) return DDM_ERR_INVALID;
+    if (B < 1 || B > (1 << 20) || P < 0 || P > (1 << 24)) return DDM_ERR_INVALID;
     return DDM_OK;
 }
 bool off(const void *p, int e) { return !p || (uintptr_t)p % e; }

@@ -187,8 +187,8 @@ __device__ __forceinline__ void tiles_ready() {
 
 // ----------------------------------------------------------------------------------------------------- packed sets
 // Sequence s of the boundaries 0, cu[0], ..., cu[B], T is [lo, hi); s = 0 and s = B + 1 are the tokens before and after
-// every sequence. cu == nullptr stands for one sequence of all T tokens. Contents are clamped, so that no bad value
-// of cu leads outside the tensor.
+// every sequence. cu == nullptr stands for one sequence of all T tokens. Contents are clamped and no length is negative, so
+// that no bad value of cu leads outside the tensor.
 struct Span { int lo, hi; };
 
 __device__ __forceinline__ int bound_at(const int32_t *cu, int B, int T, int s) {
@@ -218,7 +218,8 @@ __device__ __forceinline__ int find_slot(const int32_t *cu, int B, int T, int mu
         if (c < 64) break;
     }
     const int s = __builtin_amdgcn_readfirstlane(n - 1);
-    *index = slot - ((int)((uint32_t)(bound_at(cu, B, T, s) * mul) / (uint32_t)tile) + s);
+    // at least 0 also where cu decreases somewhere, so that no slot begins before its sequence
+    *index = max(0, slot - ((int)((uint32_t)(bound_at(cu, B, T, s) * mul) / (uint32_t)tile) + s));
     return s;
 }
 inline __host__ __device__ long long slot_count(int B, int T, int mul, int tile) {

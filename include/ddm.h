@@ -307,7 +307,7 @@ int ddm_mutual_nn_ex(const void *D1, int H1, int W1, const void *D2, int H2, int
  * the matching loss, each with its gradient. Conventions as above, and:
  *  - Packed sets: sequences (sets of matches) of different lengths lie one after another along the first axis; cu is device
  *    int32[B + 1], non-decreasing, sequence b = [cu[b], cu[b+1]). NULL cu means one sequence of everything (B = 1). Contents
- *    of cu outside [0, T] are clamped, so no value leads outside a tensor. Values of elements inside a sequence must be
+ *    of cu outside [0, T] are clamped and none leads outside a tensor, but out of order they leave outputs unwritten. Values of elements inside a sequence must be
  *    finite; elements outside every sequence influence nothing (their own outputs are written, as zeros).
  *  - 16-byte aligned pointers unless a function says otherwise. Statistics, sums and gradients' accumulators are fp32;
  *    outputs are rounded once, to nearest even. No atomics: results do not depend on the order of workgroups.
@@ -318,7 +318,8 @@ int ddm_mutual_nn_ex(const void *D1, int H1, int W1, const void *D2, int H2, int
  * over the keys j of query i's sequence; with causal = 1 over j <= i + Lk - Lq (positions in the sequence, so that the last
  * query sees every key). A query that sees no key gets out = 0, lse = -inf and gives no gradient.
  *   q            [Tq][Hq][D], row (t, h) at q + (t * q_ts + h * q_hs) elements, D elements contiguous; k, v [Tk][Hkv][D] and
- *                dout [Tq][Hq][D] likewise; strides non-negative, whole 16-byte pieces, below 16 MB
+ *                dout [Tq][Hq][D] likewise; strides non-negative and whole 16-byte pieces; a token stride below 16 MB, and
+ *                in backward the heads of q's and dout's groups within 512 MB
  *   out, dq, dk, dv  contiguous, in the inputs' type;  lse  float [Tq][Hq]
  *   D            1..DDM_MAX_D with D * element size a multiple of 16 (else DDM_ERR_UNSUPPORTED)
  *   scale        > 0
@@ -359,7 +360,7 @@ int ddm_layer_norm_backward(const void *dy, const void *x, int64_t ldx, const vo
  *   da_i = sum_j dz_ij b_j / temperature,  db_j = sum_i dz_ij a_i / temperature
  * where g = dloss (float [P]) is the gradient by the losses (float [P]). The score matrix is never stored.
  *   1 <= d <= DDM_MAX_D; contiguous rows; a and b at any whole element, da and db 16-byte aligned; temperature > 0;
- *   0 <= P <= 2^28.
+ *   0 <= P <= 2^24.
  * Rows outside every set: loss and lse 0, gradients 0. */
 size_t ddm_matching_loss_workspace_bytes(int B, int P, int d, int dtype);
 int ddm_matching_loss_forward(const void *a, const void *b, const int32_t *cu, int B, int P, int d, int dtype,

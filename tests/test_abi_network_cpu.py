@@ -48,6 +48,7 @@ def test_attention_workspace_and_gradient_pointers(L):
     assert _attn(L, backward=True, wsb=16) == -3
     assert _attn(L, backward=True, ws=None) == -3
     assert _attn(L, backward=True, ws=FAKE + 4) == -3
+    assert _attn(L, backward=True, qh=1 << 28) == -1        # a group's heads beyond 31-bit offsets
     for n in ("g", "dq", "dk", "dv"):
         assert _attn(L, backward=True, **{n: None}) == -1
     assert _attn(L, Tq=2, Tk=5000, ws=None) == -3           # few rows over long keys: the parts lie in the workspace

@@ -252,6 +252,32 @@ def test_bad_boundaries_stay_inside(ddm):
         assert torch.equal(a[n], b[n])
 
 
+@pytest.mark.parametrize("cu", [[0, 90, 30, 100], [100, 0, 100, 0], [50, 40, 30, 20], [0, 100, 100, 0]])
+@pytest.mark.parametrize("lens", [((30, 30, 40), (30, 30, 40)), ((1, 0, 1), (400, 300, 500))])
+def test_boundaries_out_of_order_stay_inside(ddm, cu, lens):
+    """Decreasing boundaries give no defined values, but no length below zero and no place before a tensor: the calls end, and
+    later ones are right."""
+    x = make("bf16", 2, 2, 64, *lens, seed=18)
+    bad = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    run(ddm, dict(x, cu_q=bad, cu_k=bad), True, 0.125)
+    torch.cuda.synchronize()
+    good = run(ddm, x, True, 0.125)
+    check(good, *reference(x, True, 0.125, "bf16"), ALL)
+
+
+def test_heads_far_apart(ddm):
+    """Heads before tokens, 18 MB from one head to the next."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(19)
+    k, v = (torch.randn(2, 70000, 128, generator=g, device="cuda").bfloat16().transpose(0, 1) for _ in range(2))
+    x = make("bf16", 4, 2, 128, (100,), (100,), seed=19)
+    far = dict(x, k=k, v=v, cu_q=None, cu_k=None)
+    near = dict(far, k=k.contiguous(), v=v.contiguous())
+    a, b = run(ddm, far, False, 0.09), run(ddm, near, False, 0.09)
+    for n in ALL:
+        assert torch.equal(a[n], b[n])
+
+
 def test_same_bits_every_time_and_on_a_side_stream(ddm):
     x = make("bf16", 8, 2, 128, (500, 300), (500, 300), seed=13)
     a = run(ddm, x, True, 0.09)
