@@ -251,12 +251,14 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_fwd_kernel(AttnArgs p) {
     }
 }
 
-// Joins the chunks of the split form: a workgroup for each (query, head). Every chunk's weight first, one thread each; then DP
-// threads a chunk add up its row, 256 / DP chunks at a time, eight loads in flight a thread.
-constexpr int MAX_CHUNKS = 2064;          // of one sequence; the plan's chunks are at least 2048th parts of all keys
+// Joins the chunks of the split form: a workgroup for each (query, head). Every chunk's weight first, one thread each; then DP / 4
+// threads a chunk add up its row, 1024 / DP chunks at a time, eight 16-byte loads in flight a thread.
+constexpr int MAX_CHUNKS = 1040;          // of one sequence; the plan's chunks are at least 1024th parts of all keys
 template <class T, int DP>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
-    __shared__ float weight[MAX_CHUNKS], red[2][4], rows[256 / DP][DP];
+    constexpr int TP = DP / 4, GROUPS = 256 / TP;             // threads of a chunk, chunks at a time
+    __shared__ float weight[MAX_CHUNKS], red[2][4];
+    __shared__ __attribute__((aligned(16))) f32x4 rows[GROUPS][TP];
     const int tid = threadIdx.x, lane = tid & 63;
     const int tok = blockIdx.x / p.Hq, head = blockIdx.x % p.Hq;
     int sq = -1;                                                // the last sequence that begins at or before the token
@@ -298,18 +300,19 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
     if (lane == 0) red[1][tid >> 6] = sum;
     __syncthreads();
     sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-    const int col = tid % DP, g = tid / DP;
-    float a = 0.f;
+    const int col = tid % TP * 4, g = tid / TP;
+    f32x4 a = 0.f;
     if (col < p.D) {
 #pragma unroll 8
-        for (int c = g; c < chunks; c += 256 / DP) a = __builtin_fmaf(weight[c], part[c * pitch + 4 + col], a);
+        for (int c = g; c < chunks; c += GROUPS) a += weight[c] * *reinterpret_cast<const f32x4 *>(part + c * pitch + 4 + col);
     }
-    rows[g][col] = a;
+    rows[g][tid % TP] = a;
     __syncthreads();
     if (g == 0 && col < p.D) {
 #pragma unroll
-        for (int x = 1; x < 256 / DP; ++x) a += rows[x][col];
-        ((T *)p.out)[(int64_t)blockIdx.x * p.D + col] = (T)(sum > 0.f ? a / sum : 0.f);
+        for (int x = 1; x < GROUPS; ++x) a += rows[x][tid];
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        store4<T>((T *)p.out + (int64_t)blockIdx.x * p.D + col, a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
         if (col == 0) p.lse[blockIdx.x] = sum > 0.f ? (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f : -INFINITY;
     }
 }
