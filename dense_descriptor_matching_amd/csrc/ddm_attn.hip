@@ -29,10 +29,14 @@ Plan make_plan(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int D) {
     Plan p{};
     p.d = D <= 32 ? 32 : D <= 64 ? 64 : 128;
     const long long rows = (long long)Tq * (Hq / Hkv);
-    // Split the keys where whole rows would leave most of the 256 CUs without work: few workgroups of 128 rows, and keys
-    // enough per sequence for two chunks.
-    const long long wgs = (rows / 128 + B) * Hkv;
-    p.split = rows <= 64ll * B && wgs < 1024 && Tk / B >= 128 && (long long)Tq * Hq < 1 << 24;
+    // Split the keys where that is sooner done, in microseconds: a whole row tile walks over its keys at 0.85 a step of 64 where
+    // 512 workgroups of 128 rows run at once; split, a step of 32 rows takes its 3 ns of the whole card, and the second launch and
+    // the join take 10. (1 row of 12 heads of 64 over 8 x 1500 keys: 24 whole, 19 split; 64 rows over 8 x 1000: 19, 28; 100 rows
+    // of 16 heads over 40000: 531, 100; 1 row over 256 x 2000 keys of 8 heads of 128: 359, 432.)
+    const double mean_rows = (double)rows / B, steps = Tk / 64.0, wgs = ((double)rows / 128 + B) * Hkv;
+    const double whole = steps / B * 0.85 * std::max(1.0, wgs / 512);
+    const double apart = 10 + std::ceil(mean_rows / 32) * Hkv * steps * 0.003;
+    p.split = mean_rows <= 128 && whole > apart && (long long)Tq * Hq < 1 << 24;
     if (p.split) {
         // some 1024 workgroups of one wave over all keys, which the card holds at once with their tiles; whole tiles of 64 keys. 67469
         // keys of 8 heads of 128 bf16: 61 us, against 65 with 2048, 71 with 1152 and 64 with 512 (5.3 TB/s at 32 x 4096 keys)

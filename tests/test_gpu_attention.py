@@ -147,7 +147,7 @@ def test_head_layouts(ddm, dtype, heads, kv, dim):
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("lens", [((1, 1), (768, 768)), ((1,), (5000,)), ((1, 1, 1, 1), (3000, 64, 1, 0)),
-                                  ((1, 0, 2), (1000, 300, 129)), ((3, 40, 1), (2000, 100, 900)), ((2, 90, 1, 1), (700, 800, 3000, 5))])
+                                  ((1, 0, 2), (1000, 300, 129)), ((1, 0, 2, 1, 1), (9000, 2000, 1290, 0, 1)), ((3, 40, 1), (2000, 100, 900)), ((2, 90, 1, 1), (700, 800, 3000, 5))])
 @pytest.mark.parametrize("heads,kv,dim", [(4, 4, 64), (16, 2, 128), (6, 2, 24)])
 def test_few_rows_over_long_keys(ddm, dtype, causal, lens, heads, kv, dim):
     x = make(dtype, heads, kv, dim, *lens, seed=11)
