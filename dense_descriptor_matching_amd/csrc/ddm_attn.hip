@@ -50,13 +50,18 @@ Plan make_plan(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int D) {
     return p;
 }
 
-// Backward: the statistics of the rows, then the parts of the dk/dv kernel. Parts are taken where key tiles alone are few.
+// Backward: the statistics of the rows, then the parts of the dk/dv kernel. Parts are taken where key tiles alone are few and their
+// sequences have rows enough: so many that equal ones fill the card's 512 places (two workgroups of four waves to a CU) once (16
+// heads over 4 key heads of 128 bf16, 2 x 2048 tokens: 339 us for the whole call with 4 parts, 393 with 5, 362 with 7), or four times with
+// causal ones, whose rows differ (4096, 3001, 1024 and 513 tokens: 648 us with 3 parts, 627 with 6). The workspace holds
+// the larger number for either.
 struct BackPlan { int parts; size_t stats, bytes; };
-BackPlan make_back_plan(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int D) {
+BackPlan make_back_plan(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int D, int causal = 1) {
     BackPlan p{};
     const long long tiles = slot_count(B, Tk, 1, KEYS) * Hkv, rows = (long long)Tq * (Hq / Hkv);
-    p.parts = (int)std::min<long long>(std::max<long long>(1024 / tiles, 1), std::max<long long>(rows / PART_ROWS, 1));
-    p.parts = std::min(p.parts, 8);
+    const long long full = std::max<long long>((long long)Tk * Hkv / KEYS, 1);
+    const long long most = std::min<long long>(std::max<long long>(rows / B / PART_ROWS, 1), 8);
+    p.parts = (int)std::min<long long>(std::max<long long>((causal ? 2048 : 512) / full, 1), most);
     p.stats = ((size_t)Tq * Hq * sizeof(float) * (dtype == DDM_F16 ? 3 : 2) + 255) / 256 * 256;
     const int d = D <= 32 ? 32 : D <= 64 ? 64 : 128;
     p.bytes = p.stats + (p.parts > 1 ? (size_t)tiles * p.parts * 2 * KEYS * d * sizeof(float) : 0);
@@ -205,7 +210,7 @@ int ddm_attention_backward(const void *dout, int64_t g_ts, int64_t g_hs, const v
     const Plan pl = make_plan(dtype, B, Tq, Tk, Hq, Hkv, D);
     AttnArgs a{};
     a.q = q; a.k = k; a.v = v; a.o = out; a.dout = dout; a.lse = const_cast<float *>(lse); a.stats = (float *)workspace;
-    a.parts = bp.parts; a.part = (float *)((char *)workspace + bp.stats);
+    a.parts = make_back_plan(dtype, B, Tq, Tk, Hq, Hkv, D, causal).parts; a.part = (float *)((char *)workspace + bp.stats);
     a.dq = dq; a.dk = dk; a.dv = dv;
     a.cu_q = cu_q; a.cu_k = cu_k;
     a.B = B; a.Tq = Tq; a.Tk = Tk; a.Hq = Hq; a.Hkv = Hkv; a.D = D;
