@@ -29,17 +29,19 @@ Plan make_plan(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int D) {
     Plan p{};
     p.d = D <= 32 ? 32 : D <= 64 ? 64 : 128;
     const long long rows = (long long)Tq * (Hq / Hkv);
-    // Split the keys where that is sooner done, in microseconds: a whole row tile walks over its keys at 0.85 a step of 64 where
-    // 512 workgroups of 128 rows run at once; split, a step of 32 rows takes its 3 ns of the whole card, and the second launch and
-    // the join take 10. (1 row of 12 heads of 64 over 8 x 1500 keys: 24 whole, 19 split; 64 rows over 8 x 1000: 19, 28; 100 rows
-    // of 16 heads over 40000: 531, 100; 1 row over 256 x 2000 keys of 8 heads of 128: 359, 432.)
+    // Split the keys where that is sooner done, in microseconds: a whole row tile walks over its keys at 0.85 a step of
+    // 64 where 512 workgroups of 128 rows run at once; split, a step of 32 rows takes its 3 ns of the whole card, and
+    // the second launch and the join take 10. (1 row of 12 heads of 64 over 8 x 1500 keys: 24 whole, 19 split; 64 rows
+    // over 8 x 1000: 19, 28; 100 rows of 16 heads over 40000: 531, 100; 1 row over 256 x 2000 keys of 8 heads of 128:
+    // 359, 432.)
     const double mean_rows = (double)rows / B, steps = Tk / 64.0, wgs = ((double)rows / 128 + B) * Hkv;
     const double whole = steps / B * 0.85 * std::max(1.0, wgs / 512);
     const double apart = 10 + std::ceil(mean_rows / 32) * Hkv * steps * 0.003;
     p.split = mean_rows <= 128 && whole > apart && (long long)Tq * Hq < 1 << 24;
     if (p.split) {
-        // some 1024 workgroups of one wave over all keys, which the card holds at once with their tiles; whole tiles of 64 keys. 67469
-        // keys of 8 heads of 128 bf16: 61 us, against 65 with 2048, 71 with 1152 and 64 with 512 (5.3 TB/s at 32 x 4096 keys)
+        // some 1024 workgroups of one wave over all keys, which the card holds at once with their tiles; whole tiles of
+        // 64 keys. 67469 keys of 8 heads of 128 bf16: 61 us, against 65 with 2048, 71 with 1152 and 64 with 512 (5.3
+        // TB/s at 32 x 4096 keys)
         const long long avg = ((long long)Tk * Hkv + 1023) / 1024;
         p.chunk = (int)std::max<long long>((avg + 63) / 64 * 64, 64);
         const long long mean = (rows + B - 1) / B;
@@ -50,11 +52,11 @@ Plan make_plan(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int D) {
     return p;
 }
 
-// Backward: the statistics of the rows, then the parts of the dk/dv kernel. Parts are taken where key tiles alone are few and their
-// sequences have rows enough: so many that equal ones fill the card's 512 places (two workgroups of four waves to a CU) once (16
-// heads over 4 key heads of 128 bf16, 2 x 2048 tokens: 339 us for the whole call with 4 parts, 393 with 5, 362 with 7), or four times with
-// causal ones, whose rows differ (4096, 3001, 1024 and 513 tokens: 648 us with 3 parts, 627 with 6). The workspace holds
-// the larger number for either.
+// Backward: the statistics of the rows, then the parts of the dk/dv kernel. Parts are taken where key tiles alone are
+// few and their sequences have rows enough: so many that equal ones fill the card's 512 places (two workgroups of four
+// waves to a CU) once (16 heads over 4 key heads of 128 bf16, 2 x 2048 tokens: 339 us for the whole call with 4 parts,
+// 393 with 5, 362 with 7), or four times with causal ones, whose rows differ (4096, 3001, 1024 and 513 tokens: 648 us
+// with 3 parts, 627 with 6). The workspace holds the larger number for either.
 struct BackPlan { int parts; size_t stats, bytes; };
 BackPlan make_back_plan(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int D, int causal = 1) {
     BackPlan p{};
@@ -80,8 +82,8 @@ int check(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int D) {
     return DDM_OK;
 }
 
-// Rows are whole 16-byte pieces at 16-byte boundaries, and 64 tokens of a tile, with `heads` heads of each, lie within 31-bit
-// offsets.
+// Rows are whole 16-byte pieces at 16-byte boundaries, and 64 tokens of a tile, with `heads` heads of each, lie within
+// 31-bit offsets.
 bool bad_view(const void *p, int64_t ts, int64_t hs, int dtype, int heads = 1) {
     const int e = esize(dtype);
     if (!p || (uintptr_t)p % 16 || ts < 0 || hs < 0 || ts >= (1ll << 40) || hs >= (1ll << 40)) return true;
@@ -109,7 +111,8 @@ hipError_t forward(const AttnArgs &a, const Plan &pl, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Rows of a tile of at most `most` in the dk/dv kernel: whole queries of G heads, or where G is larger a whole part of one.
+// Rows of a tile of at most `most` in the dk/dv kernel: whole queries of G heads, or where G is larger a whole part of
+// one.
 int tile_rows(int most, int G) {
     if (G <= most) return most / G * G;
     int r = most;

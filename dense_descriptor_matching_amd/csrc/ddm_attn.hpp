@@ -38,7 +38,8 @@ __device__ __forceinline__ int64_t rows_bytes(int rows, int64_t ts, int d) {
     return rows <= 0 ? 0 : ((int64_t)(rows - 1) * ts + d) * (int64_t)sizeof(T);
 }
 
-// Operand rows straight from global memory: 8 elements at k positions 16 c + 8 h of a row, zeros past d or without a row.
+// Operand rows straight from global memory: 8 elements at k positions 16 c + 8 h of a row, zeros past d or without a
+// row.
 template <class T>
 __device__ __forceinline__ Frag<T> global_rows(const T *row, int k, int d, bool in) {
     Frag<T> f = {};
@@ -72,11 +73,19 @@ __device__ __forceinline__ void store4(T *p, float a, float b, float c, float d)
 }
 
 // --------------------------------------------------------------------------------------------------------- forward
-// A workgroup takes BM = 32 NW rows (each wave 32) and walks over the keys in tiles of BN, which have two places in LDS: while one
-// is used, the next is on its way. Running maximum m (in units of log2) and sum l per row; the accumulator is rescaled only when
-// a row's maximum has grown by more than 8 since the last time (any reference gives the same quotient; p stays below 2^8, far
-// inside fp16 and bf16). p is rounded to the inputs' type for the second product, which the matrix cores take; l sums it before that.
-// SPLIT: the workgroup takes a chunk of the keys, for few rows and many keys; attn_join joins the chunks.
+// A workgroup takes BM = 32 NW rows (each wave 32) and walks over the keys in tiles of BN, which have two places in
+// LDS: while one is used, the next is on its way. Running maximum m (in units of log2) and sum l per row; the
+// accumulator is rescaled only when a row's maximum has grown by more than 8 since the last time (any reference gives
+// the same quotient; p stays below 2^8, far inside fp16 and bf16). p is rounded to the inputs' type for the second
+// product, which the matrix cores take; l sums it before that. Bound by the matrix cores and the vector units together,
+// which overlap by a quarter here: 64 components are 16 matrix and some 16 vector cycles a score (the exponential alone
+// 8), 128 are 32 and 16. Four waves of 32 rows: two row blocks a wave, eight waves, 32 or 128 keys a tile, and scores
+// of the next tile begun before a tile's exponentials were all slower. Measured: 114 us for 32 x 768 tokens of 16 heads
+// of 64 fp16 (680 TFLOP/s), 345 us for 11949 causal tokens of 32 over 8 heads of 128 bf16 (955 TFLOP/s; a large library
+// product reaches 1185 here).
+// SPLIT: the workgroup takes a chunk of the keys, for few rows and many keys; attn_join joins the chunks. Bound by
+// memory: one wave with 32 KB of tiles, so that five are on a CU; 56 us for 67469 keys of 8 heads of 128 bf16 (276 MB,
+// 4.9 TB/s; a large copy 4.8).
 template <class T, int D, int NW, int BN, bool SPLIT>
 __global__ __launch_bounds__(NW * 64, 2) void attn_fwd_kernel(AttnArgs p) {
     using TL = Tile<T, D>;
@@ -251,8 +260,9 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_fwd_kernel(AttnArgs p) {
     }
 }
 
-// Joins the chunks of the split form: a workgroup for each (query, head). Every chunk's weight first, one thread each; then DP / 4
-// threads a chunk add up its row, 1024 / DP chunks at a time, eight 16-byte loads in flight a thread.
+// Joins the chunks of the split form: a workgroup for each (query, head). Every chunk's weight first, one thread each;
+// then DP / 4 threads a chunk add up its row, 1024 / DP chunks at a time, eight 16-byte loads in flight a thread. Bound
+// by latency: 5.7 us for 192 rows of up to 79 chunks.
 constexpr int MAX_CHUNKS = 1040;          // of one sequence; the plan's chunks are at least 1024th parts of all keys
 template <class T, int DP>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
@@ -318,8 +328,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
 }
 
 // -------------------------------------------------------------------------------------------------------- backward
-// fp16 holds dS to few bits once it is below 2^-14, which small gradients make it; there each row's dS is divided by the power
-// of two next to its largest |do| before it is rounded, and the products are multiplied back in fp32.
+// fp16 holds dS to few bits once it is below 2^-14, which small gradients make it; there each row's dS is divided by
+// the power of two next to its largest |do| before it is rounded, and the products are multiplied back in fp32.
 template <class T> constexpr bool scaled_ds = sizeof(T) == 2 && !std::is_same_v<T, __bf16>;
 constexpr float NO_EXPONENT = -100.f;
 
@@ -338,11 +348,13 @@ __device__ __forceinline__ float add_up(bf16x8 f, float x) {
 }
 
 // dq and D_i, one row block at a time as in the forward pass: S and dO V^T of 32 keys from two key tiles' rows, then dS
-// times K from the key tile's columns. No sum crosses workgroups, so the result does not depend on their order; the price
-// is that S and dO V^T are computed here and again in attn_dkv_kernel (7 products instead of 5).
-// A row's dS sum to zero before they are rounded, and keys tend to share a mean: rounded (and with a D_i from the rounded out),
-// the sum r is not zero and would carry that mean into dq. So dq is taken as sum_j dS_ij (k_j - c) with c the mean of the
-// sequence's first keys, that is less r c at the end (keys of mean 1 and spread 1, bfloat16: error 0.0038 -> 0.0026 of dq's norm).
+// times K from the key tile's columns. No sum crosses workgroups, so the result does not depend on their order; the
+// price is that S and dO V^T are computed here and again in attn_dkv_kernel (7 products instead of 5). A row's dS sum
+// to zero before they are rounded, and keys tend to share a mean: rounded (and with a D_i from the rounded out), the
+// sum r is not zero and would carry that mean into dq. So dq is taken as sum_j dS_ij (k_j - c) with c the mean of the
+// sequence's first keys, that is less r c at the end (keys of mean 1 and spread 1, bfloat16: error 0.0038 -> 0.0026 of
+// dq's norm). Measured: 203 us for 8634 causal tokens of 16 over 4 heads of 128 bf16 (820 TFLOP/s), 46 us for 6446
+// tokens over 6453 of 12 heads of 64 (500 TFLOP/s); bound as the forward pass is.
 template <class T, int D, int NW, int BN>
 __global__ __launch_bounds__(NW * 64, 2) void attn_dq_kernel(AttnArgs p) {
     using TL = Tile<T, D>;
@@ -491,12 +503,16 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_dq_kernel(AttnArgs p) {
         }
 }
 
-// dk and dv: a workgroup of KW waves keeps 32 KW keys (their K, and V where there is room, as operands in registers) and walks
-// over the rows of the key head's whole group in tiles of BQ = 32 BL, Q and dO in LDS. S = Q K^T and dO V^T come out with the keys
-// as columns, so P and dS feed the products with dO and Q (read as columns) without leaving their lanes.
-// Where there are few key tiles, or causal ones with very different numbers of rows, a sequence's rows are cut into up to `most`
-// parts of at least PART_ROWS, at the same rows for every tile, so that workgroups that run together read the same rows through
-// their L2. The parts' sums go to the workspace in fp32 and attn_dkv_join_kernel adds them in order.
+// dk and dv: a workgroup of KW waves keeps 32 KW keys (their K, and V where there is room, as operands in registers)
+// and walks over the rows of the key head's whole group in tiles of BQ = 32 BL, Q and dO in LDS. S = Q K^T and dO V^T
+// come out with the keys as columns, so P and dS feed the products with dO and Q (read as columns) without leaving
+// their lanes. Where there are few key tiles, or causal ones with very different numbers of rows, a sequence's rows are
+// cut into up to `most` parts of at least PART_ROWS, at the same rows for every tile, so that workgroups that run
+// together read the same rows through their L2. The parts' sums go to the workspace in fp32 and attn_dkv_join_kernel
+// adds them in order. Four waves in step, two workgroups to a CU; eight waves that also share out the rows of a tile
+// were slower (376 us against 330 for the whole call at 2 x 2048 x 16 heads of 128) but where one sequence of 768
+// tokens is all there is (50, 61). Measured: 330 us for the causal tokens named above (670 TFLOP/s), 576 us for 2 x
+// 4096 of 16 heads of 128 (955 TFLOP/s), 56 us for the 12 heads of 64 (555).
 constexpr int PART_ROWS = 512;
 struct RowPart { int from, to, begin, parts; };    // rows of one part for a tile; the tile's first part and the end of its parts
 __device__ __forceinline__ RowPart part_of(int first, int rows, int most, int rt, int part) {
@@ -561,8 +577,8 @@ __global__ __launch_bounds__(KW * 64, sizeof(T) == 4 && D == 128 ? 1 : 2) void a
 
     using In = Dma<T, D, NW, BQ>;
     const int row_at = TL::row_base(lane), col_at = TL::col_base(lane);
-    // A tile has rt <= BQ rows: whole queries, or a whole part of one with more heads than BQ (see the plan). So a lane's offsets
-    // are the same for every tile, but for the rows that a last tile lacks.
+    // A tile has rt <= BQ rows: whole queries, or a whole part of one with more heads than BQ (see the plan). So a
+    // lane's offsets are the same for every tile, but for the rows that a last tile lacks.
     auto in_tile = [&](int row, int64_t ts, int64_t hs) {
         const int qi = G <= BQ ? (int)div_by(row, p.group) : 0;
         return qi * (int)ts + (row - qi * G * (G <= BQ)) * (int)hs;
@@ -733,7 +749,8 @@ __global__ __launch_bounds__(KW * 64, sizeof(T) == 4 && D == 128 ? 1 : 2) void a
         }
 }
 
-// dk and dv of the key tiles whose rows were cut into parts: a workgroup for 32 keys of one of them.
+// dk and dv of the key tiles whose rows were cut into parts: a workgroup for 32 keys of one of them. Bound by memory:
+// 16 us for up to 3 parts of 8634 x 4 heads of 128.
 template <class T, int D, int KW>
 __global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnArgs p) {
     constexpr int BK = KW * 32;

@@ -3,10 +3,10 @@
 //   z_ij = a_i . b_j / t,  loss_i = (lse_a_i + lse_b_i) / 2 - z_ii
 //   dz_ij = (g_i e^{z_ij - lse_a_i} + g_j e^{z_ij - lse_b_j}) / 2 - g_i [i = j]
 //   da_i = sum_j dz_ij b_j / t,  db_j = sum_i dz_ij a_i / t
-// within each packed set. Scores exist only as matrix-core tiles. With some 24 to 64 components a score costs far less on the
-// matrix cores than its exponentials on the vector units, so each direction has its own pass: rows of one side
-// stay in registers and the other side's go by, and no sum crosses workgroups except over the S pieces that a set's columns
-// are cut into when there are too few rows to fill the card; those are joined in order.
+// within each packed set. Scores exist only as matrix-core tiles. With some 24 to 64 components a score costs far less
+// on the matrix cores than its exponentials on the vector units, so each direction has its own pass: rows of one side
+// stay in registers and the other side's go by, and no sum crosses workgroups except over the S pieces that a set's
+// columns are cut into when there are too few rows to fill the card; those are joined in order.
 #include "../../include/ddm.h"
 #include "ddm_attn.hpp"
 
@@ -40,8 +40,11 @@ __device__ __forceinline__ void piece_of(int n, int S, int s, int tile, int *fro
     *to = min(n, *from + each);
 }
 
-// Forward, one direction (blockIdx.z): rows x of one side, columns y of the other. As attention's forward without values;
-// the maximum is exact here, since the loss of a clear match is the logarithm of a sum next to 1.
+// Forward, one direction (blockIdx.z): rows x of one side, columns y of the other. As attention's forward without
+// values; the maximum is exact here, since the loss of a clear match is the logarithm of a sum next to 1. Bound by the
+// vector units, 3.75 instructions and an exponential (four more's time) a score, and the matrix cores behind them: 127
+// us for 2 x 16384 x 16384 scores of 64 components (bf16), 73 us for 16 sets of up to 4096 matches of 24 (fp16; 3.2e8
+// scores).
 template <class T, int D, int BN>
 __global__ __launch_bounds__(256, 2) void loss_fwd_kernel(LossArgs p) {
     using TL = Tile<T, D>;
@@ -99,8 +102,8 @@ __global__ __launch_bounds__(256, 2) void loss_fwd_kernel(LossArgs p) {
         for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                // with the match among them the largest score counts as exactly 1; elsewhere ref's rounding is a common factor
-                // of 1 + 2^-20 at most on what is added, and saves an instruction a score
+                // with the match among them the largest score counts as exactly 1; elsewhere ref's rounding is a common
+                // factor of 1 + 2^-20 at most on what is added, and saves an instruction a score
                 if constexpr (decltype(special)::value) sum += exp2_fast((z[b][r] - next_m) * p.c);
                 else s4[r % 4] += exp2_fast(__builtin_fmaf(z[b][r], p.c, -ref));
             }
@@ -151,11 +154,14 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs p, float *loss,
     loss[i] = any ? 0.5f * __builtin_fmaf((top[0] - hit) + (top[1] - hit), p.inv_t, (log_sum[0] + log_sum[1]) * LN2) : 0.f;
 }
 
-// Backward, one direction: dx of the rows, the gradient by the scores made tile by tile. fp16 holds it to few bits below 2^-14,
-// where a mean over many matches lies: there g is divided by a power of two next to its largest value in reach first.
-// The exponentials bound it, two a score. Where all lse in reach lie within 2^+-30 of a common e^mid, as they do for unit-norm rows
-// unless t is tiny, one is enough: e^{z - lse_y} = e^{z - lse_x} e^{lse_x - mid} e^{mid - lse_y}, the last two known by row and column
-// (what the first loses to underflow is below 2^-66 of g there). fp32 inputs, bound by their products, keep both.
+// Backward, one direction: dx of the rows, the gradient by the scores made tile by tile. fp16 holds it to few bits
+// below 2^-14, where a mean over many matches lies: there g is divided by a power of two next to its largest value in
+// reach first. The exponentials bound it, two a score. Where all lse in reach lie within 2^+-30 of a common e^mid, as
+// they do for unit-norm rows unless t is tiny, one is enough: e^{z - lse_y} = e^{z - lse_x} e^{lse_x - mid} e^{mid -
+// lse_y}, the last two known by row and column (what the first loses to underflow is below 2^-66 of g there). fp32
+// inputs, bound by their products, keep both. Measured on the same: 212 us (298 with two exponentials) and 121 us
+// (161). More registers for more tiles at once cost the third wave of a SIMD and were slower (372 us for forward and
+// gradient against 298).
 template <class T, int D, int BN>
 __global__ __launch_bounds__(256, 2) void loss_bwd_kernel(LossArgs p) {
     using TL = Tile<T, D>;
@@ -432,7 +438,8 @@ int ddm_matching_loss_forward(const void *a, const void *b, const int32_t *cu, i
     const hipError_t e = with_type(dtype, pl.dp, [&](auto t, auto dp) {
         using T = decltype(t);
         if (hipError_t r = rows_for<T>(p, pl, ws, stream)) return r;
-        // 16-bit rows: tiles of 128 columns (16384 x 64 bf16: 106 us against 131 with 64); fp32 ones would fill LDS with one workgroup
+        // 16-bit rows: tiles of 128 columns (16384 x 64 bf16, with the gradient: 300 us against 325 with 64, 342 with
+        // 32); fp32 ones would fill LDS with one workgroup
         constexpr int BN = sizeof(T) == 4 ? 64 : 128;
         hipLaunchKernelGGL((loss_fwd_kernel<T, decltype(dp)::value, BN>), dim3((unsigned)slot_count(B, P, 1, 128), pl.S, 2),
                            dim3(256), 0, stream, p);

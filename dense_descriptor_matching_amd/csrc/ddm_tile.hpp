@@ -1,12 +1,12 @@
 // ddm_tile.hpp -- 32 x 32 matrix-core tiles, LDS tiles and packed sets, shared by the attention and matching-loss
 // kernels.
 //
-// A product C[m][n] = sum_k A[m][k] B[n][k] runs in steps of 16 along k. Lane l of a wave holds row l % 32 of A and of B and,
-// with h = l / 32, eight of the step's k positions; any assignment of k positions to (h, element) is right as long as
-// A and B agree. C element r of lane l is column n = l % 32, row m = 8 (r / 4) + 4 h + r % 4.
-// So the transposed score tile (m = key, n = query) holds one query's scores in two lanes: a row's softmax statistics
-// need one exchange between lane halves, and its elements 8t..8t+7 are, as they lie, the B operand of a product over keys
-// 16t + 4h + {0..3} and 16t + 8 + 4h + {0..3}: probabilities go from one product to the next in registers.
+// A product C[m][n] = sum_k A[m][k] B[n][k] runs in steps of 16 along k. Lane l of a wave holds row l % 32 of A and of
+// B and, with h = l / 32, eight of the step's k positions; any assignment of k positions to (h, element) is right as
+// long as A and B agree. C element r of lane l is column n = l % 32, row m = 8 (r / 4) + 4 h + r % 4. So the transposed
+// score tile (m = key, n = query) holds one query's scores in two lanes: a row's softmax statistics need one exchange
+// between lane halves, and its elements 8t..8t+7 are, as they lie, the B operand of a product over keys 16t + 4h +
+// {0..3} and 16t + 8 + 4h + {0..3}: probabilities go from one product to the next in registers.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <cstdint>
@@ -51,8 +51,8 @@ __device__ __forceinline__ Frag<T> to_frag(const float (&x)[8]) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Over the two lanes n and n + 32: v_permlane32_swap of a value with itself leaves the low half's in one register and the
-// high half's in the other, in both lanes.
+// Over the two lanes n and n + 32: v_permlane32_swap of a value with itself leaves the low half's in one register and
+// the high half's in the other, in both lanes.
 __device__ __forceinline__ float half_max(float x) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
@@ -63,8 +63,8 @@ __device__ __forceinline__ float half_sum(float x) {
 }
 
 // ------------------------------------------------------------------------------------------------------ LDS tiles
-// A tile holds rows of D elements as 16-byte pieces; piece p of row r lies at place p ^ swizzle(r) of its row, so that both
-// the reads of one piece column over 32 rows and the transposing reads of four rows spread over the banks.
+// A tile holds rows of D elements as 16-byte pieces; piece p of row r lies at place p ^ swizzle(r) of its row, so that
+// both the reads of one piece column over 32 rows and the transposing reads of four rows spread over the banks.
 template <class T, int D>
 struct Tile {
     static constexpr int PE = 16 / (int)sizeof(T);   // elements of a piece
@@ -79,8 +79,8 @@ struct Tile {
     }
     __device__ static __forceinline__ int place(int r, int p) { return r * ROW + ((p ^ swizzle(r)) << 4); }
 
-    // Operand rows: lane's row r0 + l % 32, k positions 16 c + 8 h + 0..7. at = row_base(lane); r0 is a multiple of 32, which
-    // leaves the swizzle alone, and the k step only flips piece bits of the address.
+    // Operand rows: lane's row r0 + l % 32, k positions 16 c + 8 h + 0..7. at = row_base(lane); r0 is a multiple of 32,
+    // which leaves the swizzle alone, and the k step only flips piece bits of the address.
     __device__ static __forceinline__ int row_base(int lane) { return place(lane & 31, (PE == 8 ? 1 : 2) * (lane >> 5)); }
     __device__ static __forceinline__ Frag<T> rows(const unsigned char *t, int at, int r0, int c) {
         if constexpr (sizeof(T) == 2) {
@@ -91,9 +91,10 @@ struct Tile {
             return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
         }
     }
-    // Operand of the tile's transpose: lane's column d0 + l % 32, k positions = rows r0 + 4 h + {0..3}, r0 + 8 + 4 h + {0..3}.
-    // 16-bit: ds_read_b64_tr_b16 hands lane i of 16 the i-th column of the 4 x 16 block whose 8-byte quarters of rows the
-    // 16 lanes point at. at = col_base(lane); r0 is a multiple of 16, d0 of 32; eight rows on, one swizzle bit flips.
+    // Operand of the tile's transpose: lane's column d0 + l % 32, k positions = rows r0 + 4 h + {0..3}, r0 + 8 + 4 h +
+    // {0..3}. 16-bit: ds_read_b64_tr_b16 hands lane i of 16 the i-th column of the 4 x 16 block whose 8-byte quarters
+    // of rows the 16 lanes point at. at = col_base(lane); r0 is a multiple of 16, d0 of 32; eight rows on, one swizzle
+    // bit flips.
     __device__ static __forceinline__ int col_base(int lane) {
         const int h = lane >> 5, i = lane & 15;
         if constexpr (sizeof(T) == 2) return place(4 * h + (i >> 2), ((lane & 16) >> 3) + ((i >> 1) & 1)) + 8 * (i & 1);
@@ -118,16 +119,17 @@ struct Tile {
     }
 };
 
-// Buffer loads with bounds: every dword at or past `bytes` reads as zero. A buffer ends at OUTSIDE at the latest, so that a piece
-// placed there is outside with all of its dwords.
+// Buffer loads with bounds: every dword at or past `bytes` reads as zero. A buffer ends at OUTSIDE at the latest, so
+// that a piece placed there is outside with all of its dwords.
 constexpr int OUTSIDE = 0x7ffffff0;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, int64_t bytes) {
     const int n = (int)(bytes < 0 ? 0 : bytes > OUTSIDE ? OUTSIDE : bytes);
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, n, 0x00027000);
 }
 
-// A tile of ROWS rows from global memory straight to LDS (buffer_load_dwordx4 ... lds): a wave's 64 lanes fill 64 consecutive
-// places, and each lane names the piece that belongs there. Pieces past the row's elements or the buffer's bytes are zeros.
+// A tile of ROWS rows from global memory straight to LDS (buffer_load_dwordx4 ... lds): a wave's 64 lanes fill 64
+// consecutive places, and each lane names the piece that belongs there. Pieces past the row's elements or the buffer's
+// bytes are zeros.
 template <class T, int D, int NW, int ROWS>
 struct Dma {
     using TL = Tile<T, D>;
@@ -187,8 +189,8 @@ __device__ __forceinline__ void tiles_ready() {
 
 // ----------------------------------------------------------------------------------------------------- packed sets
 // Sequence s of the boundaries 0, cu[0], ..., cu[B], T is [lo, hi); s = 0 and s = B + 1 are the tokens before and after
-// every sequence. cu == nullptr stands for one sequence of all T tokens. Contents are clamped and no length is negative, so
-// that no bad value of cu leads outside the tensor.
+// every sequence. cu == nullptr stands for one sequence of all T tokens. Contents are clamped and no length is
+// negative, so that no bad value of cu leads outside the tensor.
 struct Span { int lo, hi; };
 
 __device__ __forceinline__ int bound_at(const int32_t *cu, int B, int T, int s) {

@@ -305,9 +305,10 @@ int ddm_mutual_nn_ex(const void *D1, int H1, int W1, const void *D2, int H2, int
  * Operators of the transformer that produces descriptor maps and of its training ("MASt3R" note on cv-learn.com, section
  * 手法とアーキテクチャ: ViT encoder, cross-attention decoders, matching head, InfoNCE matching loss): attention, layer norm and
  * the matching loss, each with its gradient. Conventions as above, and:
- *  - Packed sets: sequences (sets of matches) of different lengths lie one after another along the first axis; cu is device
- *    int32[B + 1], non-decreasing, sequence b = [cu[b], cu[b+1]). NULL cu means one sequence of everything (B = 1). Contents
- *    of cu outside [0, T] are clamped and none leads outside a tensor, but out of order they leave outputs unwritten. Values of elements inside a sequence must be
+ *  - Packed sets: sequences (sets of matches) of different lengths lie one after another along the first
+ *    axis; cu is device int32[B + 1], non-decreasing, sequence b = [cu[b], cu[b+1]). NULL cu means one
+ *    sequence of everything (B = 1). Contents of cu outside [0, T] are clamped and none leads outside a
+ *    tensor, but out of order they leave outputs unwritten. Values of elements inside a sequence must be
  *    finite; elements outside every sequence influence nothing (their own outputs are written, as zeros).
  *  - 16-byte aligned pointers unless a function says otherwise. Statistics, sums and gradients' accumulators are fp32;
  *    outputs are rounded once, to nearest even. No atomics: results do not depend on the order of workgroups.
