@@ -8,7 +8,7 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "ddm.hip")
-NET_SRCS = [os.path.join(HERE, "csrc", f) for f in ("ddm_attn.hip", "ddm_norm.hip", "ddm_loss.hip")]
+NET_SRCS = [os.path.join(HERE, "csrc", "net", f) for f in ("ddm_attn.hip", "ddm_norm.hip", "ddm_loss.hip")]
 OBJ_DIR = os.path.join(HERE, "build")
 LIB = os.path.join(HERE, "libddm.so")
 

@@ -1,5 +1,5 @@
 // ddm_attn.hip -- host side of ddm_attention_*: checks, variants and launches.
-#include "../../include/ddm.h"
+#include "../../../include/ddm.h"
 #include "ddm_attn.hpp"
 
 #include <algorithm>

@@ -7,7 +7,7 @@
 // on the matrix cores than its exponentials on the vector units, so each direction has its own pass: rows of one side
 // stay in registers and the other side's go by, and no sum crosses workgroups except over the S pieces that a set's
 // columns are cut into when there are too few rows to fill the card; those are joined in order.
-#include "../../include/ddm.h"
+#include "../../../include/ddm.h"
 #include "ddm_attn.hpp"
 
 #include <algorithm>

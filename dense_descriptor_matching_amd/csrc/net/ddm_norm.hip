@@ -10,7 +10,7 @@
 // order. Measured at 24576 x 1024 bf16: forward 17.7 us (100 MB, 5.7 TB/s; a copy of 2 x 200 MB reaches 5.4 here),
 // backward 31.6 us (150 MB, 4.8 TB/s) and 4.2 us for the last sums; grids of 1024 to all workgroups, and half or twice
 // the backward ones, made no difference.
-#include "../../include/ddm.h"
+#include "../../../include/ddm.h"
 
 #include <hip/hip_runtime.h>
 
