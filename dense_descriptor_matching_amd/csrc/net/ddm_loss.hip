@@ -4,9 +4,10 @@
 //   dz_ij = (g_i e^{z_ij - lse_a_i} + g_j e^{z_ij - lse_b_j}) / 2 - g_i [i = j]
 //   da_i = sum_j dz_ij b_j / t,  db_j = sum_i dz_ij a_i / t
 // within each packed set. Scores exist only as matrix-core tiles. With some 24 to 64 components a score costs far less
-// on the matrix cores than its exponentials on the vector units, so each direction has its own pass: rows of one side
-// stay in registers and the other side's go by, and no sum crosses workgroups except over the S pieces that a set's
-// columns are cut into when there are too few rows to fill the card; those are joined in order.
+// on the matrix cores than its exponentials on the vector units. In general each direction has its own pass: rows of
+// one side stay in registers and the other side's go by, and no sum crosses workgroups except over the S pieces that a
+// set's columns are cut into when there are too few rows to fill the card; those are joined in order. Forward, sets
+// whose scores cannot leave +-32 need no maximum, and one exponential a score serves both directions (one_pass()).
 #include "../../../include/ddm.h"
 #include "ddm_attn.hpp"
 
@@ -28,6 +29,9 @@ struct LossArgs {
     float c, inv_t;                  // c = log2(e) / t
     float2 *ml;                      // forward: [2][S][P] largest a_i.b_j and the sum of exponentials about it
     float *hit;                      // forward: a_i.b_i
+    float *top;                      // [2][slots] largest |a_i|^2, |b_i|^2 of 128 rows, or null: no set takes one pass
+    float *row_sum, *col_sum;        // one pass: [row_pieces][P], [ONE_CHUNKS][P] sums of e^z without the match
+    int slots, one_slots, pieces, one_pieces;
     const float *g, *lse_a, *lse_b;  // backward
     void *da, *db;
     float *part;                     // backward: [2][S][P][DP], or null: written straight to da, db
@@ -40,23 +44,184 @@ __device__ __forceinline__ void piece_of(int n, int S, int s, int tile, int *fro
     *to = min(n, *from + each);
 }
 
-// Forward, one direction (blockIdx.z): rows x of one side, columns y of the other. As attention's forward without
-// values; the maximum is exact here, since the loss of a clear match is the logarithm of a sum next to 1. Bound by the
-// vector units, 3.75 instructions and an exponential (four more's time) a score, and the matrix cores behind them: 127
-// us for 2 x 16384 x 16384 scores of 64 components (bf16), 73 us for 16 sets of up to 4096 matches of 24 (fp16; 3.2e8
-// scores).
+// Largest |a_i|^2 (blockIdx.y = 0) or |b_i|^2 (1) of each slot of 128 rows: two lanes a row, 16 bytes a load.
+template <class T>
+__global__ __launch_bounds__(256) void loss_top_kernel(LossArgs p) {
+    constexpr int PE = 16 / sizeof(T);
+    __shared__ float wave_top[4];
+    int index;
+    const int s = find_slot(p.cu, p.B, p.P, 1, 128, blockIdx.x, &index);
+    const Span span = span_of(p.cu, p.B, p.P, s);
+    const int row = index * 128 + (threadIdx.x >> 1);
+    if (index * 128 >= span.hi - span.lo) return;
+    float sq = 0.f;
+    if (row < span.hi - span.lo) {
+        const T *x = (const T *)(blockIdx.y ? p.b : p.a) + (int64_t)(span.lo + row) * p.ld;
+        for (int c = (threadIdx.x & 1) * PE; c < p.w; c += 2 * PE) {
+            union { u32x4 u; T e[PE]; } v;
+            v.u = *reinterpret_cast<const u32x4 *>(x + c);
+#pragma unroll
+            for (int e = 0; e < PE; ++e) sq = __builtin_fmaf((float)v.e[e], (float)v.e[e], sq);
+        }
+    }
+    sq += __shfl_xor(sq, 1);
+#pragma unroll
+    for (int x = 32; x > 1; x >>= 1) sq = fmaxf(sq, __shfl_xor(sq, x));
+    if ((threadIdx.x & 63) == 0) wave_top[threadIdx.x >> 6] = sq;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        p.top[(int64_t)blockIdx.y * p.slots + blockIdx.x] = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
+}
+
+// Whether set s takes one pass: |z_ij| <= |a_i| |b_j| / t is at most 32, so that e^z and sums of up to ONE_N of them, and
+// those by e^-z_ii, stay inside fp32's range; and it is not too long for its sums' places. For the whole workgroup.
+constexpr int ONE_ROWS = 256, ONE_CHUNKS = 128, ONE_N = ONE_ROWS * ONE_CHUNKS, ONE_COLS = 1024;
+__device__ __forceinline__ bool takes_one_pass(const LossArgs &p, int s, Span span, float (*red)[4]) {
+    const int n = span.hi - span.lo;
+    if (!p.top || s == 0 || s == p.B + 1 || n > ONE_N) return false;
+    const float *at = p.top + span.lo / 128 + s;
+    float ta = 0.f, tb = 0.f;
+    for (int i = threadIdx.x; i < (n + 127) / 128; i += 256) {
+        ta = fmaxf(ta, at[i]);
+        tb = fmaxf(tb, at[p.slots + i]);
+    }
+#pragma unroll
+    for (int x = 32; x; x >>= 1) {
+        ta = fmaxf(ta, __shfl_xor(ta, x));
+        tb = fmaxf(tb, __shfl_xor(tb, x));
+    }
+    __syncthreads();                                           // red may still be read from before
+    if ((threadIdx.x & 63) == 0) { red[0][threadIdx.x >> 6] = ta; red[1][threadIdx.x >> 6] = tb; }
+    __syncthreads();
+    ta = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    tb = fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3]));
+    return __builtin_amdgcn_readfirstlane(ta * tb * (p.inv_t * p.inv_t) <= 1024.f);
+}
+// Its columns in pieces: p.one_pieces of them, or of at most ONE_COLS each; at least 128.
+__device__ __forceinline__ int one_piece(const LossArgs &p, int n) {
+    return min(ONE_COLS, ((n + p.one_pieces - 1) / p.one_pieces + 127) / 128 * 128);
+}
+
+// 16 elements over 32 lanes: at each exchange a lane hands over the half of the elements that it stops summing, and ends
+// with element (lane / 2) % 16 over the lanes of its parity.
+template <int K>
+__device__ __forceinline__ void hand_over(float (&v)[16], int lane) {
+    const bool up = lane & (2 * K);
+#pragma unroll
+    for (int r = 0; r < K; ++r) {
+        const float give = up ? v[r] : v[r + K], keep = up ? v[r + K] : v[r];
+        v[r] = keep + __shfl_xor(give, 2 * K);
+    }
+    if constexpr (K > 1) hand_over<K / 2>(v, lane);
+}
+
+// Forward, both directions at once: rows a of one chunk, columns b of one piece. e^z is summed as it is, without a
+// maximum: a wave keeps 32 rows, whose sums gather in the 16 elements of its score tiles over all columns, and adds each
+// tile's column sums (16 of a column's 32 in each lane half) to its own row of LDS. The match itself is left out:
+// lse - z_ii = log1p(e^-z_ii sum of the others) is exact where that is small. Per score 4 instructions and one
+// exponential, for which two passes take twice 3.75 and one.
+template <class T, int D, int BN>
+__global__ __launch_bounds__(256, 2) void loss_one_kernel(LossArgs p) {
+    using TL = Tile<T, D>;
+    constexpr int DC = D / 16, KB = BN / 32, BM = 128;
+    // one array: of several, the compiler would take the loads to LDS to alias what is read from the others
+    constexpr int TILE = BN * TL::ROW;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[2 * TILE + 4 * ONE_COLS * 4 + 32];
+    float *const col = (float *)(lds + 2 * TILE);
+    float (*const red)[4] = (float (*)[4])(col + 4 * ONE_COLS);
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
+    int chunk;
+    const int s = find_slot(p.cu, p.B, p.P, 1, ONE_ROWS, blockIdx.x, &chunk), piece = blockIdx.y;
+    const Span span = span_of(p.cu, p.B, p.P, s);
+    const int n = span.hi - span.lo;
+    if ((int64_t)chunk * ONE_ROWS >= n) return;
+    const int each = one_piece(p, n), from = min((int64_t)n, (int64_t)piece * each), to = min(n, from + each);
+    if (from >= n || !takes_one_pass(p, s, span, red)) return;
+    const T *xs = (const T *)p.a + (int64_t)span.lo * p.ld, *ys = (const T *)p.b + (int64_t)span.lo * p.ld;
+    const int row_at = TL::row_base(lane);
+    for (int j = lane; j < to - from; j += 64) col[w * ONE_COLS + j] = 0.f;
+    for (int row0 = chunk * ONE_ROWS; row0 < min(n, (chunk + 1) * ONE_ROWS); row0 += BM) {
+        const int wave0 = row0 + 32 * w, row = wave0 + (lane & 31);
+        Frag<T> xf[DC];
+#pragma unroll
+        for (int c = 0; c < DC; ++c) xf[c] = global_rows<T>(xs + (int64_t)min(row, n - 1) * p.ld, 16 * c + 8 * h, p.w, row < n);
+        Walk<T, D, 4, BN> tiles(ys + (int64_t)from * p.ld, to - from, p.ld, p.w, w, lane);
+        const int t_end = (to - from + BN - 1) / BN;
+        f32x16 sum = 0.f;
+        auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next,
+                        float *__restrict my_col, auto special) {
+            if (t + 1 < t_end) tiles.next(next, w);
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+                float *at = my_col + t * BN + 32 * b + (lane & 31);
+                const float before = *at;
+                f32x16 z = 0.f;
+#pragma unroll
+                for (int c = 0; c < DC; ++c) mma(z, xf[c], TL::rows(cur, row_at, 32 * b, c));
+                const int j = from + t * BN + 32 * b + (lane & 31);
+                float hit = 0.f;
+                bool has = false;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    float e = exp2_fast(z[r] * p.c);
+                    if constexpr (decltype(special)::value) {
+                        const int i = wave0 + 8 * (r / 4) + 4 * h + r % 4;
+                        if (i == j) { hit = z[r]; has = true; }
+                        if (i == j || i >= n || j >= to) e = 0.f;
+                    }
+                    z[r] = e;
+                }
+                sum += z;
+                float c4[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) c4[r] = (z[r] + z[r + 4]) + (z[r + 8] + z[r + 12]);
+                const float total = half_sum((c4[0] + c4[1]) + (c4[2] + c4[3]));
+                if constexpr (decltype(special)::value) {
+                    if (has && j < to) p.hit[span.lo + j] = hit;
+                }
+                *at = before + total;                          // the same from both lane halves
+            }
+        };
+        tiles.next(lds, w);
+        tiles_ready();
+        for (int t = 0; t < t_end; ++t) {
+            const int j0 = from + t * BN;
+            const bool special = j0 + BN > to || row0 + BM > n || (j0 < row0 + BM && row0 < j0 + BN);
+            if (special) step(t, lds + (t & 1) * TILE, lds + (~t & 1) * TILE, col + w * ONE_COLS, std::integral_constant<bool, true>{});
+            else step(t, lds + (t & 1) * TILE, lds + (~t & 1) * TILE, col + w * ONE_COLS, std::integral_constant<bool, false>{});
+            tiles_ready();
+        }
+        float v[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] = sum[r];
+        hand_over<8>(v, lane);
+        v[0] += __shfl_xor(v[0], 1);
+        const int r = (lane >> 1) & 15, i = wave0 + 8 * (r / 4) + 4 * h + r % 4;
+        if (!(lane & 1) && i < n) p.row_sum[(int64_t)piece * p.P + span.lo + i] = v[0];
+    }
+    for (int j = tid; j < to - from; j += 256)
+        p.col_sum[(int64_t)chunk * p.P + span.lo + from + j] = (col[j] + col[ONE_COLS + j]) + (col[2 * ONE_COLS + j] + col[3 * ONE_COLS + j]);
+}
+
+// Forward, one direction (blockIdx.z), of the sets that do not take one pass: rows x of one side, columns y of the other.
+// As attention's forward without values; the maximum is exact here, since the loss of a clear match is the logarithm of
+// a sum next to 1. Bound by the vector units, 3.75 instructions and an exponential (four more's time) a score, and the matrix cores
+// behind them: 127 us for 2 x 16384 x 16384 scores of 64 components (bf16), 73 us for 16 sets of up to 4096 matches of
+// 24 (fp16; 3.2e8 scores).
 template <class T, int D, int BN>
 __global__ __launch_bounds__(256, 2) void loss_fwd_kernel(LossArgs p) {
     using TL = Tile<T, D>;
     constexpr int DC = D / 16, KB = BN / 32, BM = 128;
-    __shared__ __attribute__((aligned(16))) unsigned char lds[2][BN * TL::ROW];
+    constexpr int TILE = BN * TL::ROW;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[2 * TILE + 32];      // one array, as above
+    float (*const red)[4] = (float (*)[4])(lds + 2 * TILE);
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     const int dir = blockIdx.z;
     int index;
     const int s = find_slot(p.cu, p.B, p.P, 1, BM, blockIdx.x, &index);
     const Span span = span_of(p.cu, p.B, p.P, s);
     const int n = span.hi - span.lo, row0 = index * BM;
-    if (row0 >= n) return;
+    if (row0 >= n || takes_one_pass(p, s, span, red)) return;
     int from = 0, to = 0;
     if (s != 0 && s != p.B + 1) piece_of(n, p.S, blockIdx.y, BN, &from, &to);
     const T *xs = (const T *)(dir ? p.b : p.a) + (int64_t)span.lo * p.ld, *ys = (const T *)(dir ? p.a : p.b) + (int64_t)span.lo * p.ld;
@@ -112,13 +277,13 @@ __global__ __launch_bounds__(256, 2) void loss_fwd_kernel(LossArgs p) {
         m = next_m;
     };
     if (t_end > 0) {
-        tiles.next(lds[0], w);
+        tiles.next(lds, w);
         tiles_ready();
         for (int t = 0; t < t_end; ++t) {
             const int j0 = from + t * BN;
             const bool special = j0 + BN > to || (j0 < row0 + BM && row0 < j0 + BN);
-            if (special) step(t, lds[t & 1], lds[(t + 1) & 1], std::integral_constant<bool, true>{});
-            else step(t, lds[t & 1], lds[(t + 1) & 1], std::integral_constant<bool, false>{});
+            if (special) step(t, lds + (t & 1) * TILE, lds + (~t & 1) * TILE, std::integral_constant<bool, true>{});
+            else step(t, lds + (t & 1) * TILE, lds + (~t & 1) * TILE, std::integral_constant<bool, false>{});
             tiles_ready();
         }
     }
@@ -132,16 +297,38 @@ __global__ __launch_bounds__(256, 2) void loss_fwd_kernel(LossArgs p) {
 }
 
 __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs p, float *loss, float *lse_a, float *lse_b) {
-    const int i = blockIdx.x * 256 + threadIdx.x;
-    if (i >= p.P) return;
+    __shared__ float red[2][4];
+    int index;
+    const int s = find_slot(p.cu, p.B, p.P, 1, 256, blockIdx.x, &index);
+    const Span span = span_of(p.cu, p.B, p.P, s);
+    const int n = span.hi - span.lo;
+    if ((int64_t)index * 256 >= n) return;
+    const bool one = takes_one_pass(p, s, span, red);
+    const int i = span.lo + index * 256 + threadIdx.x;
+    if (i >= span.hi) return;
+    if (one) {
+        const int each = one_piece(p, n), pieces = (n + each - 1) / each, chunks = (n + ONE_ROWS - 1) / ONE_ROWS;
+        float a = 0.f, b = 0.f;
+#pragma unroll 8
+        for (int k = 0; k < pieces; ++k) a += p.row_sum[(int64_t)k * p.P + i];
+#pragma unroll 8
+        for (int k = 0; k < chunks; ++k) b += p.col_sum[(int64_t)k * p.P + i];
+        const float hit = p.hit[i], by = exp2_fast(-hit * p.c);
+        a = log1pf(a * by);
+        b = log1pf(b * by);
+        lse_a[i] = __builtin_fmaf(hit, p.inv_t, a);
+        lse_b[i] = __builtin_fmaf(hit, p.inv_t, b);
+        loss[i] = 0.5f * (a + b);
+        return;
+    }
     float top[2], log_sum[2];
     bool any = false;
     for (int dir = 0; dir < 2; ++dir) {
         const float2 *ml = p.ml + (int64_t)dir * p.S * p.P + i;
         float m = -INFINITY, l = 0.f;
-        for (int s = 0; s < p.S; ++s) m = fmaxf(m, ml[(int64_t)s * p.P].x);
-        for (int s = 0; s < p.S; ++s) {
-            const float2 v = ml[(int64_t)s * p.P];
+        for (int k = 0; k < p.S; ++k) m = fmaxf(m, ml[(int64_t)k * p.P].x);
+        for (int k = 0; k < p.S; ++k) {
+            const float2 v = ml[(int64_t)k * p.P];
             if (v.y > 0.f) l += v.y * exp2_fast((v.x - m) * p.c);
         }
         any = l > 0.f;
@@ -167,9 +354,10 @@ __global__ __launch_bounds__(256, 2) void loss_bwd_kernel(LossArgs p) {
     using TL = Tile<T, D>;
     constexpr int DC = D / 16, DB = D / 32, BM = 128;
     constexpr bool exact_exp = sizeof(T) == 4;
-    __shared__ __attribute__((aligned(16))) unsigned char lds[2][BN * TL::ROW];
-    __shared__ __attribute__((aligned(16))) float st_lse[2][BN], st_g[2][BN];
-    __shared__ float reach[2][4];
+    constexpr int TILE = BN * TL::ROW;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[2 * TILE + 4 * BN * 4 + 32];      // one array, as above
+    float (*const st)[2 * BN] = (float (*)[2 * BN])(lds + 2 * TILE);                 // lse, then g, of a tile's columns
+    float (*const reach)[4] = (float (*)[4])(lds + 2 * TILE + 4 * BN * 4);
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     const int dir = blockIdx.z;
     int index;
@@ -228,15 +416,19 @@ __global__ __launch_bounds__(256, 2) void loss_bwd_kernel(LossArgs p) {
         tiles.next(dst, w);
         if (tid < BN) {
             const bool ok = j0 + tid < to;
-            s_lse = ok ? lse_y[j0 + tid] * unit : INFINITY;
-            s_g = ok ? 0.5f * scale * g[j0 + tid] : 0.f;
-            if (near && ok) s_g *= exp2_fast(mid - s_lse);
+            s_lse = ok ? lse_y[j0 + tid] : INFINITY;
+            s_g = ok ? g[j0 + tid] : 0.f;
         }
     };
-    auto put_stats = [&](int b) {
-        if (tid < BN) { st_lse[b][tid] = s_lse; st_g[b][tid] = s_g; }
+    auto put_stats = [&](int b) {                              // after the step: nothing waits for these loads before it
+        if (tid < BN) {
+            const float l = s_lse * unit, half = 0.5f * scale * s_g;
+            st[b][tid] = l;
+            st[b][BN + tid] = near && s_lse < INFINITY ? half * exp2_fast(mid - l) : half;
+        }
     };
-    auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next, bool special) {
+    auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next,
+                    const float *__restrict st_lse, bool special) {
         if (t + 1 < t_end) fetch(t + 1, next);
 #pragma unroll
         for (int b = 0; b < BN / 32; ++b) {
@@ -246,7 +438,7 @@ __global__ __launch_bounds__(256, 2) void loss_bwd_kernel(LossArgs p) {
             if (near) {
 #pragma unroll
                 for (int r4 = 0; r4 < 4; ++r4) {
-                    const f32x4 gy = *reinterpret_cast<const f32x4 *>(&st_g[t & 1][32 * b + 8 * r4 + 4 * h]);
+                    const f32x4 gy = *reinterpret_cast<const f32x4 *>(st_lse + BN + 32 * b + 8 * r4 + 4 * h);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         z[4 * r4 + e] = exp2_fast(__builtin_fmaf(z[4 * r4 + e], slope, -my_lse)) *
@@ -256,8 +448,8 @@ __global__ __launch_bounds__(256, 2) void loss_bwd_kernel(LossArgs p) {
 #pragma unroll
                 for (int r4 = 0; r4 < 4; ++r4) {
                     const int k0 = 32 * b + 8 * r4 + 4 * h;
-                    const f32x4 ly = *reinterpret_cast<const f32x4 *>(&st_lse[t & 1][k0]);
-                    const f32x4 gy = *reinterpret_cast<const f32x4 *>(&st_g[t & 1][k0]);
+                    const f32x4 ly = *reinterpret_cast<const f32x4 *>(st_lse + k0);
+                    const f32x4 gy = *reinterpret_cast<const f32x4 *>(st_lse + BN + k0);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float v = z[4 * r4 + e];
@@ -287,13 +479,13 @@ __global__ __launch_bounds__(256, 2) void loss_bwd_kernel(LossArgs p) {
         }
     };
     if (t_end > 0) {
-        fetch(0, lds[0]);
+        fetch(0, lds);
         put_stats(0);
         tiles_ready();
         for (int t = 0; t < t_end; ++t) {
             const int j0 = from + t * BN;
             const bool special = j0 + BN > to || (j0 < row0 + BM && row0 < j0 + BN);
-            step(t, lds[t & 1], lds[(t + 1) & 1], special);
+            step(t, lds + (t & 1) * TILE, lds + (~t & 1) * TILE, st[t & 1], special);
             if (t + 1 < t_end) put_stats((t + 1) & 1);
             tiles_ready();
         }
@@ -356,7 +548,9 @@ int esize(int dtype) { return dtype == DDM_F32 ? 4 : 2; }
 struct Plan {
     int dp, S;                       // padded components, pieces of a set's columns
     bool direct;                     // backward writes da and db straight away
-    size_t rows, ml, hit, part, bytes;
+    bool one;                        // sets may take one pass
+    int slots, one_slots, pieces, one_pieces;
+    size_t rows, ml, hit, part, top, row_sum, col_sum, bytes;
 };
 
 // Some 512 row tiles of 128 and pieces: two directions make 1024 workgroups, four on each CU.
@@ -373,6 +567,14 @@ Plan make_plan(int B, int P, int d, int dtype) {
     p.ml = take(2 * (size_t)p.S * P * sizeof(float2));
     p.hit = take((size_t)P * 4);
     p.part = take(p.direct ? 0 : 2 * (size_t)p.S * P * p.dp * 4);
+    p.one = P >= 4096;
+    p.slots = (int)slot_count(B, P, 1, 128);
+    p.one_slots = (int)slot_count(B, P, 1, ONE_ROWS);
+    p.one_pieces = (int)std::min<long long>(std::max<long long>(1024 / (P / ONE_ROWS + B), 1), 32);
+    p.pieces = std::max(p.one_pieces, (std::min(P, ONE_N) + ONE_COLS - 1) / ONE_COLS);
+    p.top = take(p.one ? 2 * (size_t)p.slots * 4 : 0);
+    p.row_sum = take(p.one ? (size_t)p.pieces * P * 4 : 0);
+    p.col_sum = take(p.one ? (size_t)std::min(ONE_CHUNKS, (P + ONE_ROWS - 1) / ONE_ROWS) * P * 4 : 0);
     p.bytes = std::max<size_t>(at, 256);
     return p;
 }
@@ -435,16 +637,27 @@ int ddm_matching_loss_forward(const void *a, const void *b, const int32_t *cu, i
     p.a = a; p.b = b; p.cu = cu; p.B = B; p.P = P; p.d = d; p.S = pl.S;
     p.c = (float)(1.4426950408889634 / temperature); p.inv_t = (float)(1.0 / temperature);
     p.ml = (float2 *)(ws + pl.ml); p.hit = (float *)(ws + pl.hit);
+    p.slots = pl.slots; p.one_slots = pl.one_slots; p.pieces = pl.pieces; p.one_pieces = pl.one_pieces;
+    if (pl.one) {
+        p.top = (float *)(ws + pl.top); p.row_sum = (float *)(ws + pl.row_sum); p.col_sum = (float *)(ws + pl.col_sum);
+    }
     const hipError_t e = with_type(dtype, pl.dp, [&](auto t, auto dp) {
         using T = decltype(t);
         if (hipError_t r = rows_for<T>(p, pl, ws, stream)) return r;
         // 16-bit rows: tiles of 128 columns (16384 x 64 bf16, with the gradient: 300 us against 325 with 64, 342 with
         // 32); fp32 ones would fill LDS with one workgroup
         constexpr int BN = sizeof(T) == 4 ? 64 : 128;
-        hipLaunchKernelGGL((loss_fwd_kernel<T, decltype(dp)::value, BN>), dim3((unsigned)slot_count(B, P, 1, 128), pl.S, 2),
-                           dim3(256), 0, stream, p);
+        if (pl.one) {
+            hipLaunchKernelGGL((loss_top_kernel<T>), dim3(pl.slots, 2), dim3(256), 0, stream, p);
+            if (hipError_t r = hipGetLastError()) return r;
+            hipLaunchKernelGGL((loss_one_kernel<T, decltype(dp)::value, 64>), dim3(pl.one_slots, pl.pieces), dim3(256), 0,
+                               stream, p);
+            if (hipError_t r = hipGetLastError()) return r;
+        }
+        hipLaunchKernelGGL((loss_fwd_kernel<T, decltype(dp)::value, BN>), dim3(pl.slots, pl.S, 2), dim3(256), 0, stream, p);
         if (hipError_t r = hipGetLastError()) return r;
-        hipLaunchKernelGGL(loss_join_kernel, dim3((P + 255) / 256), dim3(256), 0, stream, p, loss, lse_a, lse_b);
+        hipLaunchKernelGGL(loss_join_kernel, dim3((unsigned)slot_count(B, P, 1, 256)), dim3(256), 0, stream, p, loss, lse_a,
+                           lse_b);
         return hipGetLastError();
     });
     return e == hipSuccess ? DDM_OK : DDM_ERR_HIP;

@@ -1,7 +1,7 @@
 """The matching loss and its gradient against the definition in 64 bits.
 
 Tolerances per element: scores of unit-norm rows divided by the temperature t carry e = (d + 4 + 4 max|z|) 2^-24 of absolute error
-from 32-bit products and exponents, which the losses and the lse take over twice and every exponential relatively; sums over
+(d times the largest |a_i| |b_j| where rows are scaled) from 32-bit products and exponents, which the losses and the lse take over twice and every exponential relatively; sums over
 n columns add (n / 8 + 16) 2^-24 relatively (partial sums of lanes and tiles). Off the diagonal the gradient by a score is rounded once to the inputs' type
 (u = 2^-8 bfloat16, 2^-11 float16, and 2^-25 of the largest dloss at least in float16) before it multiplies the other side's
 rows; da and db are rounded once.
@@ -47,7 +47,7 @@ def run(ddm, x, t=0.07):
     return dict(loss=loss, lse_a=la, lse_b=lb, da=da, db=db)
 
 
-def check(got, x, dtype, t=0.07):
+def check(got, x, dtype, t=0.07, norms=1.0):
     u = U[dtype]
     cu = x["cu"].tolist()
     d = x["a"].shape[1]
@@ -58,7 +58,7 @@ def check(got, x, dtype, t=0.07):
         a, b, g = (x[k][lo:hi].double() for k in ("a", "b", "g"))
         z = a @ b.T / t
         la, lb = torch.logsumexp(z, 1), torch.logsumexp(z, 0)
-        e = (d + 4 + 4 * float(z.abs().max())) * E
+        e = (d * norms + 4 + 4 * float(z.abs().max())) * E
         s = 2 * e + (n / 8 + 16) * E
         pa, pb = torch.exp(z - la[:, None]) * g[:, None] / 2, torch.exp(z - lb[None, :]) * g[None, :] / 2
         dz = pa + pb - torch.diag(g)
@@ -91,6 +91,58 @@ def test_larger_sets(ddm, dtype):
     for lens in ((4000, 2500, 77), (128,) * 520):
         x = make(dtype, 24, lens, seed=1)
         check(run(ddm, x), x, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("d", [16, 33, 64, 128])
+@pytest.mark.parametrize("lens", [(4200,), (1025, 0, 513, 1, 3000, 128, 127)])
+def test_one_pass(ddm, dtype, d, lens):
+    """From 4096 matches on one exponential of a score serves both directions."""
+    x = make(dtype, d, lens, seed=11)
+    check(run(ddm, x), x, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_one_and_two_passes_together(ddm, dtype):
+    """Scores of some sets lie within 32 and those of others do not."""
+    lens = (2000, 1500, 1, 0, 700, 300)
+    x = make(dtype, 24, lens, seed=12, noise=0.8)
+    for i in (1, 4):
+        lo, hi = sum(lens[:i]), sum(lens[:i + 1])
+        x["a"][lo:hi] *= 3
+        x["b"][lo:hi] *= 3
+    check(run(ddm, x), x, dtype, norms=9.0)
+
+
+def test_a_set_too_long_for_one_pass(ddm):
+    x = make("f16", 16, (32769, 500), seed=13, scale=16.0)
+    check(run(ddm, x), x, "f16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_clear_matches(ddm, dtype):
+    x = make(dtype, 64, (4500, 1), seed=14, noise=0.05)
+    got = run(ddm, x)
+    check(got, x, dtype)
+    assert got["loss"][-1].item() == 0
+
+
+def test_one_pass_has_the_same_bits_in_graph_replays_and_between_other_rows(ddm):
+    x = make("bf16", 24, (3000, 2500), seed=15, pad=9)
+    want = run(ddm, x)
+    for n in ("a", "b", "g"):
+        x[n][:9], x[n][-9:] = float("nan"), float("inf")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(ddm, x)
+    for _ in range(3):
+        for t in got.values():
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in ALL:
+            assert torch.equal(got[n][9:-9], want[n][9:-9])
+            assert (got[n][:9] == 0).all() and (got[n][-9:] == 0).all()
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
