@@ -118,13 +118,16 @@ __device__ __forceinline__ void hand_over(float (&v)[16], int lane) {
 // Forward, both directions at once: rows a of one chunk, columns b of one piece. e^z is summed as it is, without a
 // maximum: a wave keeps 32 rows, whose sums gather in the 16 elements of its score tiles over all columns, and adds each
 // tile's column sums (16 of a column's 32 in each lane half) to its own row of LDS. The match itself is left out:
-// lse - z_ii = log1p(e^-z_ii sum of the others) is exact where that is small. Per score 4 instructions and one
-// exponential, for which two passes take twice 3.75 and one.
+// lse - z_ii = log1p(e^-z_ii sum of the others) is exact where that is small. Per score 3.1 instructions and one
+// exponential, for which two passes take twice 3.75 and one. With the gradient: 16384 x 64 bf16 269 us against 319 in two
+// passes, 16 sets of up to 4096 x 24 fp16 168 against 177. Chunks of 256 rows: with 512 there are 1024 workgroups, whose
+// last third the card runs alone (287 us).
 template <class T, int D, int BN>
 __global__ __launch_bounds__(256, 2) void loss_one_kernel(LossArgs p) {
     using TL = Tile<T, D>;
     constexpr int DC = D / 16, KB = BN / 32, BM = 128;
-    // one array: of several, the compiler would take the loads to LDS to alias what is read from the others
+    // One array: of several, the compiler takes the loads to LDS to alias what is read, and waits for the next tile in
+    // every step (295 against 287 us for the first of the two above).
     constexpr int TILE = BN * TL::ROW;
     __shared__ __attribute__((aligned(16))) unsigned char lds[2 * TILE + 4 * ONE_COLS * 4 + 32];
     float *const col = (float *)(lds + 2 * TILE);
@@ -205,9 +208,9 @@ __global__ __launch_bounds__(256, 2) void loss_one_kernel(LossArgs p) {
 
 // Forward, one direction (blockIdx.z), of the sets that do not take one pass: rows x of one side, columns y of the other.
 // As attention's forward without values; the maximum is exact here, since the loss of a clear match is the logarithm of
-// a sum next to 1. Bound by the vector units, 3.75 instructions and an exponential (four more's time) a score, and the matrix cores
-// behind them: 127 us for 2 x 16384 x 16384 scores of 64 components (bf16), 73 us for 16 sets of up to 4096 matches of
-// 24 (fp16; 3.2e8 scores).
+// a sum next to 1. Bound by the vector units, 3.75 instructions and an exponential (four more's time) a score, and the
+// matrix cores behind them: 127 us for 2 x 16384 x 16384 scores of 64 components (bf16), 73 us for 16 sets of up to 4096
+// matches of 24 (fp16; 3.2e8 scores). Where every set takes one pass its workgroups end at once (5 us).
 template <class T, int D, int BN>
 __global__ __launch_bounds__(256, 2) void loss_fwd_kernel(LossArgs p) {
     using TL = Tile<T, D>;
@@ -346,7 +349,7 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs p, float *loss,
 // reach first. The exponentials bound it, two a score. Where all lse in reach lie within 2^+-30 of a common e^mid, as
 // they do for unit-norm rows unless t is tiny, one is enough: e^{z - lse_y} = e^{z - lse_x} e^{lse_x - mid} e^{mid -
 // lse_y}, the last two known by row and column (what the first loses to underflow is below 2^-66 of g there). fp32
-// inputs, bound by their products, keep both. Measured on the same: 212 us (298 with two exponentials) and 121 us
+// inputs, bound by their products, keep both. Measured on the same: 196 us (298 with two exponentials) and 111 us
 // (161). More registers for more tiles at once cost the third wave of a SIMD and were slower (372 us for forward and
 // gradient against 298).
 template <class T, int D, int BN>
@@ -567,6 +570,7 @@ Plan make_plan(int B, int P, int d, int dtype) {
     p.ml = take(2 * (size_t)p.S * P * sizeof(float2));
     p.hit = take((size_t)P * 4);
     p.part = take(p.direct ? 0 : 2 * (size_t)p.S * P * p.dp * 4);
+    // From 4096 matches on the two launches more are paid back: 4096 x 24 bf16 51.5 us against 51.7, 3000 49 against 48.
     p.one = P >= 4096;
     p.slots = (int)slot_count(B, P, 1, 128);
     p.one_slots = (int)slot_count(B, P, 1, ONE_ROWS);
