@@ -514,8 +514,8 @@ __global__ __launch_bounds__(NW * 64, sizeof(T) == 2 && D == 64 ? 3 : 2) void at
 // together read the same rows through their L2. The parts' sums go to the workspace in fp32 and attn_dkv_join_kernel
 // adds them in order. Four waves in step, two workgroups to a CU; eight waves that also share out the rows of a tile
 // were slower (376 us against 330 for the whole call at 2 x 2048 x 16 heads of 128) but where one sequence of 768
-// tokens is all there is (50, 61). Measured: 330 us for the causal tokens named above (670 TFLOP/s), 576 us for 2 x
-// 4096 of 16 heads of 128 (955 TFLOP/s), 56 us for the 12 heads of 64 (555).
+// tokens is all there is (50, 61). Measured: 293 us for the causal tokens named above (755 TFLOP/s), 576 us for 2 x
+// 4096 of 16 heads of 128 (955 TFLOP/s), 53 us for the 12 heads of 64 (585).
 constexpr int PART_ROWS = 512;
 struct RowPart { int from, to, begin, parts; };    // rows of one part for a tile; the tile's first part and the end of its parts
 __device__ __forceinline__ RowPart part_of(int first, int rows, int most, int rt, int part) {
