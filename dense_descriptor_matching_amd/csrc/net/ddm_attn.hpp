@@ -333,39 +333,23 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
 template <class T> constexpr bool scaled_ds = sizeof(T) == 2 && !std::is_same_v<T, __bf16>;
 constexpr float NO_EXPONENT = -100.f;
 
-// x plus the eight elements of a fragment.
-__device__ __forceinline__ float add_up(f16x8 f, float x) {
-    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) x = __builtin_amdgcn_fdot2(h2{f[e], f[e + 1]}, h2{(_Float16)1.f, (_Float16)1.f}, x, false);
-    return x;
-}
-__device__ __forceinline__ float add_up(bf16x8 f, float x) {
-    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-#pragma unroll
-    for (int e = 0; e < 8; e += 2) x = __builtin_amdgcn_fdot2_f32_bf16(b2{f[e], f[e + 1]}, b2{(__bf16)1.f, (__bf16)1.f}, x, false);
-    return x;
-}
-
 // dq and D_i, one row block at a time as in the forward pass: S and dO V^T of 32 keys from two key tiles' rows, then dS
 // times K from the key tile's columns. No sum crosses workgroups, so the result does not depend on their order; the
 // price is that S and dO V^T are computed here and again in attn_dkv_kernel (7 products instead of 5). A row's dS sum
-// to zero before they are rounded, and keys tend to share a mean: rounded (and with a D_i from the rounded out), the
-// sum r is not zero and would carry that mean into dq. So dq is taken as sum_j dS_ij (k_j - c) with c the mean of the
-// sequence's first keys, that is less r c at the end (keys of mean 1 and spread 1, bfloat16: error 0.0038 -> 0.0026 of
-// dq's norm). Measured: 203 us for 8634 causal tokens of 16 over 4 heads of 128 bf16 (820 TFLOP/s), 46 us for 6446
-// tokens over 6453 of 12 heads of 64 (500 TFLOP/s); bound as the forward pass is.
+// to zero before they are rounded and about to zero after (D_i is taken from the rounded out), so that a mean which all
+// keys share reaches dq by the sum of the roundings: with keys of mean 1 and spread 1 the error is 0.0038 of dq's norm in
+// bfloat16, with keys of mean 0 0.0024. No centre is subtracted from the keys: one that lies far from those that a row
+// attends carries that sum into dq without bound. Measured: 200 us for 8634 causal tokens of 16 over 4 heads of 128 bf16
+// (830 TFLOP/s), 47 us for 6446 tokens over 6453 of 12 heads of 64 (490 TFLOP/s); bound as the forward pass is.
 template <class T, int D, int NW, int BN>
 __global__ __launch_bounds__(NW * 64, sizeof(T) == 2 && D == 64 ? 3 : 2) void attn_dq_kernel(AttnArgs p) {
     using TL = Tile<T, D>;
     constexpr int BM = NW * 32, DC = D / 16, DB = D / 32;
     constexpr int TILE_BYTES = BN * TL::ROW;
-    constexpr bool CENTRED = sizeof(T) == 2;
     // One array: of several, the compiler takes the loads to LDS to alias what is read, and waits for the next tile in
     // every step (training, with the dk/dv kernel's: 32 x 768 tokens of 64 bf16 446 us against 451, of 32 105 against 112).
     // 64 components in 16 bits: held to the registers of three waves a SIMD (cross pairs 122 us, with two 128).
-    __shared__ __attribute__((aligned(16))) unsigned char lds[4 * TILE_BYTES + (CENTRED ? D * 4 : 16)];
-    float *const centre = (float *)(lds + 4 * TILE_BYTES);
+    __shared__ __attribute__((aligned(16))) unsigned char lds[4 * TILE_BYTES];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = lane >> 5, n = lane & 31;
     const int G = p.group.g;
@@ -431,7 +415,6 @@ __global__ __launch_bounds__(NW * 64, sizeof(T) == 2 && D == 64 ? 3 : 2) void at
     f32x16 dq[DB];
 #pragma unroll
     for (int d = 0; d < DB; ++d) dq[d] = 0.f;
-    float rest = 0.f;                                        // sum of the rounded dS
 
     Walk<T, D, NW, BN> ks(kb, Lk, p.k_ts, p.D, w, lane), vs(vb, Lk, p.v_ts, p.D, w, lane);
     auto fetch = [&](unsigned char *to) {
@@ -468,7 +451,6 @@ __global__ __launch_bounds__(NW * 64, sizeof(T) == 2 && D == 64 ? 3 : 2) void at
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = z[kc * 8 + e];
                 const Frag<T> sf = to_frag<T>(v);
-                if constexpr (CENTRED) rest = add_up(sf, rest);
 #pragma unroll
                 for (int d = 0; d < DB; ++d) mma(dq[d], TL::cols(kt, col_at, 32 * b + 16 * kc, 32 * d), sf);
             }
@@ -477,20 +459,12 @@ __global__ __launch_bounds__(NW * 64, sizeof(T) == 2 && D == 64 ? 3 : 2) void at
     if (t_end > 0) {
         fetch(lds);
         tiles_ready();
-        if (CENTRED && tid < D) {                            // read again only after the loop's barriers
-            const int few = min(Lk, 8);
-            float sum = 0.f;
-            for (int i = 0; i < few; ++i)
-                sum += (float)*reinterpret_cast<const T *>(lds + TL::place(i, tid / TL::PE) + tid % TL::PE * sizeof(T));
-            centre[tid] = sum / (float)few;
-        }
         const int t_full = max(0, min(t_end, low / BN));
         for (int t = 0; t < t_end; ++t) {
             step(t, lds + (t & 1) * 2 * TILE_BYTES, lds + (~t & 1) * 2 * TILE_BYTES, t >= t_full);
             tiles_ready();
         }
     }
-    rest = lim < 64 ? 0.f : half_sum(rest);                  // for rows of few keys, the first ones' mean need not be near theirs
     if (!in) return;
     const float f = scaled_ds<T> ? p.scale / inv : p.scale;
     T *row = (T *)p.dq + at * p.D;
@@ -500,9 +474,7 @@ __global__ __launch_bounds__(NW * 64, sizeof(T) == 2 && D == 64 ? 3 : 2) void at
         for (int r = 0; r < 16; r += 4) {
             const int col = 32 * d + 8 * (r / 4) + 4 * h;
             if (col >= p.D) continue;
-            f32x4 v = {dq[d][r], dq[d][r + 1], dq[d][r + 2], dq[d][r + 3]};
-            if (CENTRED && t_end > 0) v -= rest * *reinterpret_cast<const f32x4 *>(&centre[col]);
-            store4<T>(row + col, v[0] * f, v[1] * f, v[2] * f, v[3] * f);
+            store4<T>(row + col, dq[d][r] * f, dq[d][r + 1] * f, dq[d][r + 2] * f, dq[d][r + 3] * f);
         }
 }
 
