@@ -333,9 +333,9 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs p, float *loss,
         for (int k = 0; k < p.S; ++k) m = fmaxf(m, ml[(int64_t)k * p.P].x);
         for (int k = 0; k < p.S; ++k) {
             const float2 v = ml[(int64_t)k * p.P];
-            if (v.y > 0.f) l += v.y * exp2_fast((v.x - m) * p.c);
+            if (v.y != 0.f) l += v.y * exp2_fast((v.x - m) * p.c);    // an empty piece has 0; NaN goes on into the loss
         }
-        any = l > 0.f;
+        any = l != 0.f;                                        // rows outside every set have no piece
         top[dir] = m;
         log_sum[dir] = __builtin_amdgcn_logf(l);
     }
@@ -428,7 +428,7 @@ __global__ __launch_bounds__(256, 2) void loss_bwd_kernel(LossArgs p) {
         if (tid < BN) {
             const float l = s_lse * unit, half = 0.5f * scale * s_g;
             st[b][tid] = l;
-            st[b][BN + tid] = near && s_lse < INFINITY ? half * exp2_fast(mid - l) : half;
+            st[b][BN + tid] = near && s_lse != INFINITY ? half * exp2_fast(mid - l) : half;    // NaN too
         }
     };
     auto step = [&](int t, const unsigned char *__restrict cur, unsigned char *__restrict next,

@@ -270,7 +270,8 @@ def _match_sizes(a, b, cu):
 
 def matching_loss_forward(a, b, cu=None, *, temperature: float = 0.07):
     """Symmetric softmax loss of matched descriptors a, b [P, d]: row p of one is to find row p of the other among the
-    rows of its set (an image pair's matches; ``cu`` bounds the sets). Returns (loss, lse_a, lse_b), float32 [P]."""
+    rows of its set (an image pair's matches; ``cu`` bounds the sets). Returns (loss, lse_a, lse_b), float32 [P]. Rows outside
+    every set have loss 0; NaN in a descriptor makes all losses of its set NaN."""
     sizes, pcu, nbytes = _match_sizes(a, b, cu)
     loss = a.new_empty(a.shape[:1], dtype=torch.float32)
     lse_a, lse_b = torch.empty_like(loss), torch.empty_like(loss)
