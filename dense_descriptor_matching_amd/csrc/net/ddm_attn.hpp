@@ -226,7 +226,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_fwd_kernel(AttnArgs p) {
         // the row's sum over both lane halves; the row is this lane's column
         const float sum = half_sum(l);
         if (in && whole) {
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;   // 0: no key seen; a NaN among the scores goes on into out and lse
             const int64_t at = (int64_t)(sq.lo + qi) * p.Hq + head;
             T *orow = (T *)p.out + at * p.D;
 #pragma unroll
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_fwd_kernel(AttnArgs p) {
                     if (col < p.D)
                         store4<T>(orow + col, o[d][r] * inv, o[d][r + 1] * inv, o[d][r + 2] * inv, o[d][r + 3] * inv);
                 }
-            if (h == 0) p.lse[at] = sum > 0.f ? (m + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f : -INFINITY;
+            if (h == 0) p.lse[at] = sum == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
         } else if (in) {
             float *part = p.part + ((int64_t)blockIdx.x * p.cap + row) * (p.D + 4);
 #pragma unroll
@@ -321,9 +321,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
     if (g == 0 && col < p.D) {
 #pragma unroll
         for (int x = 1; x < GROUPS; ++x) a += rows[x][tid];
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         store4<T>((T *)p.out + (int64_t)blockIdx.x * p.D + col, a[0] * inv, a[1] * inv, a[2] * inv, a[3] * inv);
-        if (col == 0) p.lse[blockIdx.x] = sum > 0.f ? (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f : -INFINITY;
+        if (col == 0) p.lse[blockIdx.x] = sum == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
     }
 }
 

@@ -130,7 +130,8 @@ def attention_forward(q, k, v, cu_q=None, cu_k=None, *, causal: bool = False, sc
 
     A query sees the keys of its sequence, with ``causal`` up to its own position counted from the sequences' ends.
     ``scale`` defaults to D ** -0.5. Returns (out [Tq, Hq, D], lse float32 [Tq, Hq]); a query that sees no key gets 0 and
-    -inf. The tensors may be views (of a packed qkv projection, say) whose rows are whole 16-byte pieces."""
+    -inf, one with a score of NaN gets NaN in both. The tensors may be views (of a packed qkv projection, say) whose rows
+    are whole 16-byte pieces."""
     sizes, pq, pk, scale = _attention_sizes(q, k, v, cu_q, cu_k, scale)
     nbytes = _workspace_bytes("ddm_attention_forward_workspace_bytes", *sizes)
     out = torch.empty_like(q, memory_format=torch.contiguous_format)

@@ -309,8 +309,9 @@ int ddm_mutual_nn_ex(const void *D1, int H1, int W1, const void *D2, int H2, int
  *    axis; cu is device int32[B + 1], non-decreasing, sequence b = [cu[b], cu[b+1]). NULL cu means one
  *    sequence of everything (B = 1). Contents of cu outside [0, T] are clamped and none leads outside a
  *    tensor, but out of order they leave outputs unwritten. Values of elements inside a sequence must be
- *    finite; NaN among a set's descriptors makes its losses and gradients NaN. Elements outside every
- *    sequence influence nothing (their own outputs are written, as zeros).
+ *    finite; NaN among them makes NaN of every out, lse, loss and gradient that depends on it, and can
+ *    make NaN of other gradients of that sequence. Elements outside every sequence influence nothing
+ *    (their own outputs are written, as zeros).
  *  - 16-byte aligned pointers unless a function says otherwise. Statistics, sums and gradients' accumulators are fp32;
  *    outputs are rounded once, to nearest even. No atomics: results do not depend on the order of workgroups.
  *  - Nothing is kept between calls; the calls launch kernels on `stream` only and can be captured into a HIP graph. */
