@@ -90,6 +90,10 @@ bool bad_view(const void *p, int64_t ts, int64_t hs, int dtype, int heads = 1) {
     if (ts * e % 16 || hs * e % 16 || ts * e >= (1ll << 24)) return true;
     return heads > 1 && hs * e >= (1ll << 29) / heads;
 }
+// The kernels' 32-bit scale and scale log2(e): as 0 or infinity they would make NaN of a hidden key's -inf or of a zero.
+bool bad_scale(double scale) {
+    return !(scale > 0) || !std::isnormal((float)scale) || !std::isnormal((float)(scale * 1.4426950408889634));
+}
 bool bad_ptr(const void *p) { return !p || (uintptr_t)p % 16; }
 
 template <class T, int D>
@@ -169,7 +173,7 @@ int ddm_attention_forward(const void *q, int64_t q_ts, int64_t q_hs, const void 
                           int Tq, int Tk, int Hq, int Hkv, int D, int dtype, int causal, double scale, void *out,
                           float *lse, void *workspace, size_t workspace_bytes, hipStream_t stream) {
     if (int rc = check(dtype, B, Tq, Tk, Hq, Hkv, D)) return rc;
-    if (!(scale > 0) || !std::isfinite(scale) || (causal != 0 && causal != 1)) return DDM_ERR_INVALID;
+    if (bad_scale(scale) || (causal != 0 && causal != 1)) return DDM_ERR_INVALID;
     if ((!cu_q || !cu_k) && B != 1) return DDM_ERR_INVALID;
     if (Tq == 0) return DDM_OK;
     if (bad_view(q, q_ts, q_hs, dtype) || bad_ptr(out) || bad_ptr(lse)) return DDM_ERR_INVALID;
@@ -201,7 +205,7 @@ int ddm_attention_backward(const void *dout, int64_t g_ts, int64_t g_hs, const v
                            int Tk, int Hq, int Hkv, int D, int dtype, int causal, double scale, void *dq, void *dk,
                            void *dv, void *workspace, size_t workspace_bytes, hipStream_t stream) {
     if (int rc = check(dtype, B, Tq, Tk, Hq, Hkv, D)) return rc;
-    if (!(scale > 0) || !std::isfinite(scale) || (causal != 0 && causal != 1)) return DDM_ERR_INVALID;
+    if (bad_scale(scale) || (causal != 0 && causal != 1)) return DDM_ERR_INVALID;
     if ((!cu_q || !cu_k) && B != 1) return DDM_ERR_INVALID;
     if (Tq && (bad_view(q, q_ts, q_hs, dtype, Hq / Hkv) || bad_view(dout, g_ts, g_hs, dtype, Hq / Hkv) || bad_ptr(out) || bad_ptr(lse) ||
                bad_ptr(dq)))

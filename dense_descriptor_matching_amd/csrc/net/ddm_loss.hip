@@ -590,6 +590,10 @@ int check(int B, int P, int d, int dtype) {
     if (B < 1 || B > (1 << 20) || P < 0 || P > (1 << 24)) return DDM_ERR_INVALID;
     return DDM_OK;
 }
+// The kernels' 32-bit 1 / t and log2(e) / t: as 0 or infinity they would make NaN of a -inf or of a zero.
+bool bad_temperature(double t) {
+    return !(t > 0) || !std::isnormal((float)(1.0 / t)) || !std::isnormal((float)(1.4426950408889634 / t));
+}
 bool off(const void *p, int e) { return !p || (uintptr_t)p % e; }
 
 template <class F>
@@ -632,7 +636,7 @@ int ddm_matching_loss_forward(const void *a, const void *b, const int32_t *cu, i
                               double temperature, float *loss, float *lse_a, float *lse_b, void *workspace,
                               size_t workspace_bytes, hipStream_t stream) {
     if (int rc = check(B, P, d, dtype)) return rc;
-    if (!(temperature > 0) || !std::isfinite(temperature) || (!cu && B != 1)) return DDM_ERR_INVALID;
+    if (bad_temperature(temperature) || (!cu && B != 1)) return DDM_ERR_INVALID;
     if (P == 0) return DDM_OK;
     if (off(a, esize(dtype)) || off(b, esize(dtype)) || off(loss, 4) || off(lse_a, 4) || off(lse_b, 4)) return DDM_ERR_INVALID;
     const Plan pl = make_plan(B, P, d, dtype);
@@ -672,7 +676,7 @@ int ddm_matching_loss_backward(const float *dloss, const void *a, const void *b,
                                const int32_t *cu, int B, int P, int d, int dtype, double temperature, void *da, void *db,
                                void *workspace, size_t workspace_bytes, hipStream_t stream) {
     if (int rc = check(B, P, d, dtype)) return rc;
-    if (!(temperature > 0) || !std::isfinite(temperature) || (!cu && B != 1)) return DDM_ERR_INVALID;
+    if (bad_temperature(temperature) || (!cu && B != 1)) return DDM_ERR_INVALID;
     if (P == 0) return DDM_OK;
     const int es = esize(dtype);
     if (off(a, es) || off(b, es) || off(dloss, 4) || off(lse_a, 4) || off(lse_b, 4) || off(da, es) || off(db, es))

@@ -325,7 +325,7 @@ int ddm_mutual_nn_ex(const void *D1, int H1, int W1, const void *D2, int H2, int
  *                in backward the heads of q's and dout's groups within 512 MB
  *   out, dq, dk, dv  contiguous, in the inputs' type;  lse  float [Tq][Hq]
  *   D            1..DDM_MAX_D with D * element size a multiple of 16 (else DDM_ERR_UNSUPPORTED)
- *   scale        > 0
+ *   scale        > 0; it and scale * log2(e) within float's normal range
  * With few query rows and long sequences the keys are split over workgroups and joined (the workspace holds the parts).
  * Products take the inputs' type with fp32 accumulation; probabilities and their gradients are rounded to that type before
  * the second product. The workspace of backward is scratch: forward keeps only out and lse. */
@@ -362,7 +362,8 @@ int ddm_layer_norm_backward(const void *dy, const void *x, int64_t ldx, const vo
  *   dz_ij = (g_i exp(z_ij - lse_a_i) + g_j exp(z_ij - lse_b_j)) / 2 - g_i [i = j]
  *   da_i = sum_j dz_ij b_j / temperature,  db_j = sum_i dz_ij a_i / temperature
  * where g = dloss (float [P]) is the gradient by the losses (float [P]). The score matrix is never stored.
- *   1 <= d <= DDM_MAX_D; contiguous rows; a and b at any whole element, da and db 16-byte aligned; temperature > 0;
+ *   1 <= d <= DDM_MAX_D; contiguous rows; a and b at any whole element, da and db 16-byte aligned; temperature > 0,
+ *   1 / temperature and log2(e) / temperature within float's normal range;
  *   0 <= P <= 2^24.
  * Rows outside every set: loss and lse 0, gradients 0. */
 size_t ddm_matching_loss_workspace_bytes(int B, int P, int d, int dtype);
