@@ -170,7 +170,10 @@ class _Attention(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout):
         q, k, v, out, lse, cu_q, cu_k = ctx.saved_tensors
-        return attention_backward(dout.contiguous(), q, k, v, out, lse, cu_q, cu_k, **ctx.options) + (None,) * 4
+        dout = dout.contiguous()
+        if dout.data_ptr() % 16:            # a view of a larger gradient
+            dout = dout.clone()
+        return attention_backward(dout, q, k, v, out, lse, cu_q, cu_k, **ctx.options) + (None,) * 4
 
 
 def attention(q, k, v, cu_q=None, cu_k=None, *, causal: bool = False, scale: float | None = None):
