@@ -554,7 +554,8 @@ struct Plan {
     bool direct;                     // backward writes da and db straight away
     bool one;                        // sets may take one pass
     int slots, one_slots, pieces, one_pieces;
-    size_t rows, ml, hit, part, top, row_sum, col_sum, bytes;
+    // what the workspace holds: repacked rows first, then what the forward pass keeps between its kernels, or the backward's parts
+    size_t rows, ml, hit, top, row_sum, col_sum, part, forward_bytes, backward_bytes;
 };
 
 // Some 512 row tiles of 128 and pieces: two directions make 1024 workgroups, four on each CU.
@@ -568,9 +569,10 @@ Plan make_plan(int B, int P, int d, int dtype) {
     size_t at = 0;
     auto take = [&](size_t n) { const size_t o = at; at += (n + 255) / 256 * 256; return o; };
     p.rows = take(2 * (size_t)P * p.dp * esize(dtype));
+    p.part = at;
+    p.backward_bytes = std::max<size_t>(at + (p.direct ? 0 : 2 * (size_t)p.S * P * p.dp * 4), 256);
     p.ml = take(2 * (size_t)p.S * P * sizeof(float2));
     p.hit = take((size_t)P * 4);
-    p.part = take(p.direct ? 0 : 2 * (size_t)p.S * P * p.dp * 4);
     // From 4096 matches on the two launches more are paid back: 4096 x 24 bf16 51.5 us against 51.7, 3000 49 against 48.
     p.one = P >= 4096;
     p.slots = (int)slot_count(B, P, 1, 128);
@@ -580,7 +582,7 @@ Plan make_plan(int B, int P, int d, int dtype) {
     p.top = take(p.one ? 2 * (size_t)p.slots * 4 : 0);
     p.row_sum = take(p.one ? (size_t)p.pieces * P * 4 : 0);
     p.col_sum = take(p.one ? (size_t)std::min(ONE_CHUNKS, (P + ONE_ROWS - 1) / ONE_ROWS) * P * 4 : 0);
-    p.bytes = std::max<size_t>(at, 256);
+    p.forward_bytes = std::max<size_t>(at, 256);
     return p;
 }
 
@@ -627,9 +629,15 @@ hipError_t rows_for(LossArgs &p, const Plan &pl, unsigned char *ws, hipStream_t 
 
 extern "C" {
 
+size_t ddm_matching_loss_forward_workspace_bytes(int B, int P, int d, int dtype) {
+    return check(B, P, d, dtype) == DDM_OK ? make_plan(B, P, d, dtype).forward_bytes : 0;
+}
+size_t ddm_matching_loss_backward_workspace_bytes(int B, int P, int d, int dtype) {
+    return check(B, P, d, dtype) == DDM_OK ? make_plan(B, P, d, dtype).backward_bytes : 0;
+}
 size_t ddm_matching_loss_workspace_bytes(int B, int P, int d, int dtype) {
-    if (check(B, P, d, dtype) != DDM_OK) return 0;
-    return make_plan(B, P, d, dtype).bytes;
+    return std::max(ddm_matching_loss_forward_workspace_bytes(B, P, d, dtype),
+                    ddm_matching_loss_backward_workspace_bytes(B, P, d, dtype));
 }
 
 int ddm_matching_loss_forward(const void *a, const void *b, const int32_t *cu, int B, int P, int d, int dtype,
@@ -640,7 +648,7 @@ int ddm_matching_loss_forward(const void *a, const void *b, const int32_t *cu, i
     if (P == 0) return DDM_OK;
     if (off(a, esize(dtype)) || off(b, esize(dtype)) || off(loss, 4) || off(lse_a, 4) || off(lse_b, 4)) return DDM_ERR_INVALID;
     const Plan pl = make_plan(B, P, d, dtype);
-    if (off(workspace, 16) || workspace_bytes < pl.bytes) return DDM_ERR_WORKSPACE;
+    if (off(workspace, 16) || workspace_bytes < pl.forward_bytes) return DDM_ERR_WORKSPACE;
     unsigned char *ws = (unsigned char *)workspace;
     LossArgs p{};
     p.a = a; p.b = b; p.cu = cu; p.B = B; p.P = P; p.d = d; p.S = pl.S;
@@ -682,7 +690,7 @@ int ddm_matching_loss_backward(const float *dloss, const void *a, const void *b,
     if (off(a, es) || off(b, es) || off(dloss, 4) || off(lse_a, 4) || off(lse_b, 4) || off(da, es) || off(db, es))
         return DDM_ERR_INVALID;
     const Plan pl = make_plan(B, P, d, dtype);
-    if (off(workspace, 16) || workspace_bytes < pl.bytes) return DDM_ERR_WORKSPACE;
+    if (off(workspace, 16) || workspace_bytes < pl.backward_bytes) return DDM_ERR_WORKSPACE;
     unsigned char *ws = (unsigned char *)workspace;
     LossArgs p{};
     p.a = a; p.b = b; p.cu = cu; p.B = B; p.P = P; p.d = d; p.S = pl.S;

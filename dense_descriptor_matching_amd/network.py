@@ -33,8 +33,9 @@ def declare(lib):
     lib.ddm_layer_norm_backward_workspace_bytes.argtypes = [I64, I, I]
     lib.ddm_layer_norm_backward_workspace_bytes.restype = SZ
     lib.ddm_layer_norm_backward.argtypes = [P, P, I64, P, P, P, I64, I, I, I, P, P, P, P, SZ, P]
-    lib.ddm_matching_loss_workspace_bytes.argtypes = [I] * 4
-    lib.ddm_matching_loss_workspace_bytes.restype = SZ
+    for f in (lib.ddm_matching_loss_forward_workspace_bytes, lib.ddm_matching_loss_backward_workspace_bytes,
+              lib.ddm_matching_loss_workspace_bytes):
+        f.argtypes, f.restype = [I] * 4, SZ
     lib.ddm_matching_loss_forward.argtypes = [P, P, P, I, I, I, I, F, P, P, P, P, SZ, P]
     lib.ddm_matching_loss_backward.argtypes = [P, P, P, P, P, P, I, I, I, I, F, P, P, P, SZ, P]
     for f in (lib.ddm_attention_forward, lib.ddm_attention_backward, lib.ddm_layer_norm_forward,
@@ -261,7 +262,7 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-6):
 
 
 # ------------------------------------------------------------------------------------------------- matching loss
-def _match_sizes(a, b, cu):
+def _match_sizes(a, b, cu, what):
     _tensor(a, "a")
     _tensor(b, "b", a.dtype, a.device, a.shape)
     if a.dim() != 2:
@@ -269,14 +270,14 @@ def _match_sizes(a, b, cu):
     B, pcu = _cu(cu, "cu", a.device)
     P, d = a.shape
     sizes = (B, P, d, _DT[a.dtype])
-    return sizes, pcu, _workspace_bytes("ddm_matching_loss_workspace_bytes", *sizes)
+    return sizes, pcu, _workspace_bytes(f"ddm_matching_loss_{what}_workspace_bytes", *sizes)
 
 
 def matching_loss_forward(a, b, cu=None, *, temperature: float = 0.07):
     """Symmetric softmax loss of matched descriptors a, b [P, d]: row p of one is to find row p of the other among the
     rows of its set (an image pair's matches; ``cu`` bounds the sets). Returns (loss, lse_a, lse_b), float32 [P]. Rows outside
     every set have loss 0; NaN in a descriptor makes all losses of its set NaN."""
-    sizes, pcu, nbytes = _match_sizes(a, b, cu)
+    sizes, pcu, nbytes = _match_sizes(a, b, cu, "forward")
     loss = a.new_empty(a.shape[:1], dtype=torch.float32)
     lse_a, lse_b = torch.empty_like(loss), torch.empty_like(loss)
     ws = a.new_empty(nbytes, dtype=torch.uint8)
@@ -287,7 +288,7 @@ def matching_loss_forward(a, b, cu=None, *, temperature: float = 0.07):
 
 def matching_loss_backward(dloss, a, b, lse_a, lse_b, cu=None, *, temperature: float = 0.07):
     """Gradients (da, db) of :func:`matching_loss_forward` for dloss, the gradient by each match's loss (float32 [P])."""
-    sizes, pcu, nbytes = _match_sizes(a, b, cu)
+    sizes, pcu, nbytes = _match_sizes(a, b, cu, "backward")
     for t, name in ((dloss, "dloss"), (lse_a, "lse_a"), (lse_b, "lse_b")):
         _tensor(t, name, torch.float32, a.device, a.shape[:1])
     da, db = torch.empty_like(a), torch.empty_like(b)
