@@ -30,8 +30,8 @@ struct LossArgs {
     float2 *ml;                      // forward: [2][S][P] largest a_i.b_j and the sum of exponentials about it
     float *hit;                      // forward: a_i.b_i
     float *top;                      // [2][slots] largest |a_i|^2, |b_i|^2 of 128 rows, or null: no set takes one pass
-    float *row_sum, *col_sum;        // one pass: [row_pieces][P], [ONE_CHUNKS][P] sums of e^z without the match
-    int slots, one_slots, pieces, one_pieces;
+    float *row_sum, *col_sum;        // one pass: [pieces][P], [chunks][P] sums of e^z without the match
+    int slots, one_rows, one_pieces;
     const float *g, *lse_a, *lse_b;  // backward
     void *da, *db;
     float *part;                     // backward: [2][S][P][DP], or null: written straight to da, db
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(256) void loss_top_kernel(LossArgs p) {
 
 // Whether set s takes one pass: |z_ij| <= |a_i| |b_j| / t is at most 32, so that e^z and sums of up to ONE_N of them, and
 // those by e^-z_ii, stay inside fp32's range; and it is not too long for its sums' places. For the whole workgroup.
-constexpr int ONE_ROWS = 256, ONE_CHUNKS = 128, ONE_N = ONE_ROWS * ONE_CHUNKS, ONE_COLS = 1024;
+constexpr int ONE_N = 32768, ONE_COLS = 1024;
 __device__ __forceinline__ bool takes_one_pass(const LossArgs &p, int s, Span span, float (*red)[4]) {
     const int n = span.hi - span.lo;
     if (!p.top || s == 0 || s == p.B + 1 || n > ONE_N) return false;
@@ -121,8 +121,8 @@ __device__ __forceinline__ void hand_over(float (&v)[16], int lane) {
 // tile's column sums (16 of a column's 32 in each lane half) to its own row of LDS. The match itself is left out:
 // lse - z_ii = log1p(e^-z_ii sum of the others) is exact where that is small. Per score 3.1 instructions and one
 // exponential, for which two passes take twice 3.75 and one. With the gradient: 16384 x 64 bf16 269 us against 319 in two
-// passes, 16 sets of up to 4096 x 24 fp16 168 against 177. Chunks of 256 rows: with 512 there are 1024 workgroups, whose
-// last third the card runs alone (287 us).
+// passes, 16 sets of up to 4096 x 24 fp16 168 against 177. Chunks of 256 rows (with 512 the first of the two has 1024
+// workgroups, whose last third the card runs alone: 287 us), longer ones in calls of very many matches (see the plan).
 template <class T, int D, int BN>
 __global__ __launch_bounds__(256, 2) void loss_one_kernel(LossArgs p) {
     using TL = Tile<T, D>;
@@ -135,16 +135,16 @@ __global__ __launch_bounds__(256, 2) void loss_one_kernel(LossArgs p) {
     float (*const red)[4] = (float (*)[4])(col + 4 * ONE_COLS);
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), h = lane >> 5;
     int chunk;
-    const int s = find_slot(p.cu, p.B, p.P, 1, ONE_ROWS, blockIdx.x, &chunk), piece = blockIdx.y;
+    const int s = find_slot(p.cu, p.B, p.P, 1, p.one_rows, blockIdx.x, &chunk), piece = blockIdx.y;
     const Span span = span_of(p.cu, p.B, p.P, s);
     const int n = span.hi - span.lo;
-    if ((int64_t)chunk * ONE_ROWS >= n) return;
+    if ((int64_t)chunk * p.one_rows >= n) return;
     const int each = one_piece(p, n), from = min((int64_t)n, (int64_t)piece * each), to = min(n, from + each);
     if (from >= n || !takes_one_pass(p, s, span, red)) return;
     const T *xs = (const T *)p.a + (int64_t)span.lo * p.ld, *ys = (const T *)p.b + (int64_t)span.lo * p.ld;
     const int row_at = TL::row_base(lane);
     for (int j = lane; j < to - from; j += 64) col[w * ONE_COLS + j] = 0.f;
-    for (int row0 = chunk * ONE_ROWS; row0 < min(n, (chunk + 1) * ONE_ROWS); row0 += BM) {
+    for (int row0 = chunk * p.one_rows; row0 < min(n, (chunk + 1) * p.one_rows); row0 += BM) {
         const int wave0 = row0 + 32 * w, row = wave0 + (lane & 31);
         Frag<T> xf[DC];
 #pragma unroll
@@ -311,7 +311,7 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs p, float *loss,
     const int i = span.lo + index * 256 + threadIdx.x;
     if (i >= span.hi) return;
     if (one) {
-        const int each = one_piece(p, n), pieces = (n + each - 1) / each, chunks = (n + ONE_ROWS - 1) / ONE_ROWS;
+        const int each = one_piece(p, n), pieces = (n + each - 1) / each, chunks = (n + p.one_rows - 1) / p.one_rows;
         float a = 0.f, b = 0.f;
 #pragma unroll 8
         for (int k = 0; k < pieces; ++k) a += p.row_sum[(int64_t)k * p.P + i];
@@ -553,10 +553,12 @@ struct Plan {
     int dp, S;                       // padded components, pieces of a set's columns
     bool direct;                     // backward writes da and db straight away
     bool one;                        // sets may take one pass
-    int slots, one_slots, pieces, one_pieces;
+    int slots, one_rows, one_slots, pieces, one_pieces;
     // what the workspace holds: repacked rows first, then what the forward pass keeps between its kernels, or the backward's parts
     size_t rows, ml, hit, top, row_sum, col_sum, part, forward_bytes, backward_bytes;
 };
+
+constexpr size_t ONE_BYTES = (size_t)1 << 30;
 
 // Some 512 row tiles of 128 and pieces: two directions make 1024 workgroups, four on each CU.
 Plan make_plan(int B, int P, int d, int dtype) {
@@ -576,12 +578,19 @@ Plan make_plan(int B, int P, int d, int dtype) {
     // From 4096 matches on the two launches more are paid back: 4096 x 24 bf16 51.5 us against 51.7, 3000 49 against 48.
     p.one = P >= 4096;
     p.slots = (int)slot_count(B, P, 1, 128);
-    p.one_slots = (int)slot_count(B, P, 1, ONE_ROWS);
-    p.one_pieces = (int)std::min<long long>(std::max<long long>(1024 / (P / ONE_ROWS + B), 1), 32);
+    // A chunk of rows leaves a sum for each column of its set, which may be any length up to ONE_N: 512 bytes a match with
+    // chunks of 256. Longer ones bound that where there are workgroups enough without (200 sets of 4000 x 24 fp16, with the
+    // gradient: 2057 us against 2129 with 256; 1000 of 1000: 1039 against 1273); past ONE_BYTES for
+    // all sums, 4 M matches, every set takes two passes, which need none of them.
+    p.one_rows = P <= 1 << 18 ? 256 : P <= 1 << 19 ? 512 : 1024;
+    p.one_pieces = (int)std::min<long long>(std::max<long long>(1024 / (P / p.one_rows + B), 1), 32);
     p.pieces = std::max(p.one_pieces, (std::min(P, ONE_N) + ONE_COLS - 1) / ONE_COLS);
+    p.one_slots = (int)slot_count(B, P, 1, p.one_rows);
+    const size_t row_bytes = (size_t)p.pieces * P * 4, col_bytes = (size_t)((std::min(P, ONE_N) + p.one_rows - 1) / p.one_rows) * P * 4;
+    p.one = p.one && row_bytes + col_bytes <= ONE_BYTES;
     p.top = take(p.one ? 2 * (size_t)p.slots * 4 : 0);
-    p.row_sum = take(p.one ? (size_t)p.pieces * P * 4 : 0);
-    p.col_sum = take(p.one ? (size_t)std::min(ONE_CHUNKS, (P + ONE_ROWS - 1) / ONE_ROWS) * P * 4 : 0);
+    p.row_sum = take(p.one ? row_bytes : 0);
+    p.col_sum = take(p.one ? col_bytes : 0);
     p.forward_bytes = std::max<size_t>(at, 256);
     return p;
 }
@@ -654,7 +663,7 @@ int ddm_matching_loss_forward(const void *a, const void *b, const int32_t *cu, i
     p.a = a; p.b = b; p.cu = cu; p.B = B; p.P = P; p.d = d; p.S = pl.S;
     p.c = (float)(1.4426950408889634 / temperature); p.inv_t = (float)(1.0 / temperature);
     p.ml = (float2 *)(ws + pl.ml); p.hit = (float *)(ws + pl.hit);
-    p.slots = pl.slots; p.one_slots = pl.one_slots; p.pieces = pl.pieces; p.one_pieces = pl.one_pieces;
+    p.slots = pl.slots; p.one_rows = pl.one_rows; p.one_pieces = pl.one_pieces;
     if (pl.one) {
         p.top = (float *)(ws + pl.top); p.row_sum = (float *)(ws + pl.row_sum); p.col_sum = (float *)(ws + pl.col_sum);
     }

@@ -367,8 +367,8 @@ int ddm_layer_norm_backward(const void *dy, const void *x, int64_t ldx, const vo
  *   0 <= P <= 2^24.
  * Rows outside every set: loss and lse 0, gradients 0.
  * Each direction has its own workspace size; ddm_matching_loss_workspace_bytes is the larger. With d padded to 32, 64 or 128 as
- * dp, both hold rows repacked (2 P dp elements) where they are not whole 16-byte pieces; forward sums of up to 32 column pieces
- * and 128 row chunks a match besides (640 bytes), backward nothing but where few matches or d not a multiple of 4 need parts (2 P
+ * dp, both hold rows repacked (2 P dp elements) where they are not whole 16-byte pieces; forward sums of up to 640
+ * bytes a match besides (384 from 2^18 matches on, 1 GiB at most), backward nothing but where few matches or d not a multiple of 4 need parts (2 P
  * dp floats, times up to 16 pieces below some 32,000 matches). */
 size_t ddm_matching_loss_forward_workspace_bytes(int B, int P, int d, int dtype);
 size_t ddm_matching_loss_backward_workspace_bytes(int B, int P, int d, int dtype);

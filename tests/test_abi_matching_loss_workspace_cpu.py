@@ -30,3 +30,13 @@ def test_each_direction_refuses_less_than_its_own(L):  # noqa: F811
 @pytest.mark.parametrize("bad", [(0, 8, 24, 1), (1, -1, 24, 1), (1, (1 << 24) + 1, 24, 1), (1, 8, 0, 1), (1, 8, 129, 1), (1, 8, 24, 3)])
 def test_sizes_that_are_refused_have_none(L, bad):  # noqa: F811
     assert L.ddm_matching_loss_forward_workspace_bytes(*bad) == 0 and L.ddm_matching_loss_backward_workspace_bytes(*bad) == 0
+
+
+def test_forward_sums_stay_small_beside_the_card(L):  # noqa: F811
+    """Rows as copied, 640 bytes a match of sums up to 2^18 matches, half a kilobyte beyond, and never more than 1 GiB of them."""
+    for P in (4096, 1 << 18, (1 << 18) + 1, 1 << 19, 1 << 20, 1 << 22, (1 << 22) + 1, 1 << 24):
+        for B in (1, 64):
+            n = L.ddm_matching_loss_forward_workspace_bytes(B, P, 24, 1) - 2 * P * 32 * 2
+            other = (2 * 16 * 8 if P < 1 << 16 else 2 * 8) * P + 4 * P + 16 * (P // 128 + B + 2) + 2048
+            assert n <= (640 if P <= 1 << 18 else 384) * P + other
+            assert n <= (1 << 30) + other
