@@ -76,7 +76,8 @@ int check(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int D) {
     if (B < 1 || Tq < 0 || Tk < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv) return DDM_ERR_INVALID;
     if (D < 1 || D > DDM_MAX_D || D * esize(dtype) % 16) return DDM_ERR_UNSUPPORTED;
     const long long G = Hq / Hkv;
-    if (B > (1 << 20) || (long long)Tq * G * G >= (1ll << 31) || Tk >= INT_MAX - (1 << 22)) return DDM_ERR_INVALID;
+    // rows and keys are counted in 31 bits, with room for the tile or parts of tiles past the last
+    if (B > (1 << 20) || Tq * G > INT_MAX - 4096 || Tk >= INT_MAX - (1 << 22)) return DDM_ERR_INVALID;
     // a launch has fewer than 2^32 threads
     if (slot_count(B, Tq, (int)G, 128) * Hkv >= 1 << 24 || slot_count(B, Tk, 1, KEYS) * Hkv >= 1 << 24) return DDM_ERR_INVALID;
     return DDM_OK;

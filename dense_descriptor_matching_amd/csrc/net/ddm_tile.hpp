@@ -228,9 +228,16 @@ inline __host__ __device__ long long slot_count(int B, int T, int mul, int tile)
     return (long long)T * mul / tile + B + 2;
 }
 
-// r / g by multiplication: m = ceil(2^32 / g) is exact for r g < 2^32; g == 1 has no 32-bit m.
-struct Div { uint32_t g, m; };
-inline Div make_div(uint32_t g) { return Div{g, g > 1 ? (uint32_t)((0x100000000ull + g - 1) / g) : 0}; }
-__device__ __forceinline__ uint32_t div_by(uint32_t r, Div d) { return __umulhi(r, d.m) + (d.m ? 0 : r); }
+// r / g by multiplication, exact for r < 2^31: with 2^(k-1) < g <= 2^k and m = ceil(2^(31 + k) / g), which has 32 bits, r m /
+// 2^(31 + k) exceeds r / g by less than 1 / g. g == 1 has no such m.
+struct Div { uint32_t g, m, shift; };
+inline Div make_div(uint32_t g) {
+    if (g <= 1) return Div{g, 0, 0};
+    const int k = 32 - __builtin_clz(g - 1);
+    return Div{g, (uint32_t)(((1ull << (31 + k)) + g - 1) / g), (uint32_t)(k - 1)};
+}
+__host__ __device__ __forceinline__ uint32_t div_by(uint32_t r, Div d) {
+    return ((uint32_t)((uint64_t)r * d.m >> 32) >> d.shift) + (d.m ? 0 : r);
+}
 
 }  // namespace ddm

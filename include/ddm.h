@@ -326,6 +326,8 @@ int ddm_mutual_nn_ex(const void *D1, int H1, int W1, const void *D2, int H2, int
  *   out, dq, dk, dv  contiguous, in the inputs' type;  lse  float [Tq][Hq]
  *   D            1..DDM_MAX_D with D * element size a multiple of 16 (else DDM_ERR_UNSUPPORTED)
  *   scale        > 0; it and scale * log2(e) within float's normal range
+ *   sizes        B <= 2^20, Tq * (Hq / Hkv) <= 2^31 - 4097, Tk < 2^31 - 2^22 - 1, and for both T = Tq * (Hq / Hkv) and T = Tk
+ *                (T / 128 + B + 2) * Hkv < 2^24 (else DDM_ERR_INVALID, or 0 from a workspace size)
  * With few query rows and long sequences the keys are split over workgroups and joined (the workspace holds the parts).
  * Products take the inputs' type with fp32 accumulation; probabilities and their gradients are rounded to that type before
  * the second product. The workspace of backward is scratch: forward keeps only out and lse. */
@@ -364,7 +366,7 @@ int ddm_layer_norm_backward(const void *dy, const void *x, int64_t ldx, const vo
  * where g = dloss (float [P]) is the gradient by the losses (float [P]). The score matrix is never stored.
  *   1 <= d <= DDM_MAX_D; contiguous rows; a and b at any whole element, da and db 16-byte aligned; temperature > 0,
  *   1 / temperature and log2(e) / temperature within float's normal range;
- *   0 <= P <= 2^24.
+ *   0 <= P <= 2^24, B <= 2^20.
  * Rows outside every set: loss and lse 0, gradients 0.
  * Each direction has its own workspace size; ddm_matching_loss_workspace_bytes is the larger. With d padded to 32, 64 or 128 as
  * dp, both hold rows repacked (2 P dp elements) where they are not whole 16-byte pieces; forward sums of up to 640
