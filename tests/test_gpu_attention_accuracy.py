@@ -92,3 +92,29 @@ def test_half_of_the_keys_far_away(ddm, dtype, mean):
     x["k"][::2, :, 0] += 40
     x["k"][:, :, 1:] += mean
     check(run(ddm, x, False, 0.125), *reference(x, False, 0.125, dtype))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("lens", [((700, 3), (700, 900)), ((300, 257), (333, 300)), ((900,), (130,))])
+@pytest.mark.parametrize("heads,kv,dim", [(2, 2, 64), (8, 2, 128), (6, 3, 80), (12, 1, 32), (4, 4, 24)])
+def test_errors_add_up_as_roundings_do(ddm, dtype, causal, lens, heads, kv, dim):
+    x = make(dtype, heads, kv, dim, *lens, seed=23)
+    check(run(ddm, x, causal, dim ** -0.5), *reference(x, causal, dim ** -0.5, dtype))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("size", [2.0 ** -10, 2.0 ** 6])
+def test_gradients_of_other_sizes(ddm, dtype, size):
+    """What float16 cannot hold of dS is that far below its row's largest, not below 2^-24."""
+    x = make(dtype, 4, 2, 64, (500, 300), (500, 300), seed=24)
+    x["dout"] = x["dout"] * size
+    check(run(ddm, x, True, 0.125), *reference(x, True, 0.125, dtype))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("heads,kv", [(40, 1), (71, 1), (128, 1)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_groups_larger_than_a_tile(ddm, dtype, heads, kv, dim):
+    x = make(dtype, heads, kv, dim, (70, 33), (70, 40), seed=25)
+    check(run(ddm, x, True, dim ** -0.5), *reference(x, True, dim ** -0.5, dtype))
