@@ -44,3 +44,25 @@ def test_131072_packed_tokens_of_128_heads(ddm):
         assert (each == each[:1]).all(), m
         got[m] = each[0]
     check(got, val, tol, ALL)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("heads,kv", [(33, 1), (40, 1), (64, 1), (71, 1), (128, 1), (96, 2)])
+@pytest.mark.parametrize("dim", [32, 64, 128])
+def test_groups_larger_than_a_tile(ddm, dtype, causal, heads, kv, dim):
+    """More query heads on a key head than the gradient's row tiles of 32 or 64 hold (a tile is then a whole part of one query's
+    heads; of 71, a prime, one)."""
+    x = make(dtype, heads, kv, dim, (30, 1, 17), (45, 3, 17), seed=63)
+    check(run(ddm, x, causal, dim ** -0.5), *reference(x, causal, dim ** -0.5, dtype), ALL)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("lens", [((600,), (600,)), ((700, 90), (700, 600)), ((1, 1100), (40, 300)), ((900, 0, 330), (130, 70, 520))])
+@pytest.mark.parametrize("heads,kv,dim", [(8, 1, 64), (24, 2, 128), (71, 1, 32)])
+def test_rows_in_many_parts(ddm, dtype, causal, lens, heads, kv, dim):
+    """Few key tiles and many rows: the gradient by keys and values cuts rows into up to eight parts and joins them, in
+    sequences of as many parts, of fewer and of one."""
+    x = make(dtype, heads, kv, dim, *lens, seed=64)
+    check(run(ddm, x, causal, dim ** -0.5), *reference(x, causal, dim ** -0.5, dtype), ALL)
