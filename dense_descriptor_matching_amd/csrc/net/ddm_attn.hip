@@ -33,7 +33,8 @@ Plan make_plan(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int D) {
     // 64 where 512 workgroups of 128 rows run at once; split, a step of 32 rows takes its 3 ns of the whole card, and
     // the second launch and the join take 10. (1 row of 12 heads of 64 over 8 x 1500 keys: 24 whole, 19 split; 64 rows
     // over 8 x 1000: 19, 28; 100 rows of 16 heads over 40000: 531, 100; 1 row over 256 x 2000 keys of 8 heads of 128:
-    // 359, 432.)
+    // 359, 432.) The step is a long call's: the first twelve take 14 us. Lengths count by their mean: of 256 single tokens
+    // with 500 keys on average, one with 40000 walks over them in one workgroup a key head.
     const double mean_rows = (double)rows / B, steps = Tk / 64.0, wgs = ((double)rows / 128 + B) * Hkv;
     const double whole = steps / B * 0.85 * std::max(1.0, wgs / 512);
     const double apart = 10 + std::ceil(mean_rows / 32) * Hkv * steps * 0.003;

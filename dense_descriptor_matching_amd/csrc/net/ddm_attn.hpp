@@ -329,7 +329,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p) {
 
 // -------------------------------------------------------------------------------------------------------- backward
 // fp16 holds dS to few bits once it is below 2^-14, which small gradients make it; there each row's dS is divided by
-// the power of two next to its largest |do| before it is rounded, and the products are multiplied back in fp32.
+// the power of two next to its largest |do| before it is rounded, and the products are multiplied back in fp32. So
+// |P (do.v - D)| may be up to some 2^16 times the row's largest |do|: v of several thousand in every component.
 template <class T> constexpr bool scaled_ds = sizeof(T) == 2 && !std::is_same_v<T, __bf16>;
 constexpr float NO_EXPONENT = -100.f;
 
@@ -337,7 +338,7 @@ constexpr float NO_EXPONENT = -100.f;
 // times K from the key tile's columns. No sum crosses workgroups, so the result does not depend on their order; the
 // price is that S and dO V^T are computed here and again in attn_dkv_kernel (7 products instead of 5). A row's dS sum
 // to zero before they are rounded and about to zero after (D_i is taken from the rounded out), so that a mean which all
-// keys share reaches dq by the sum of the roundings: with keys of mean 1 and spread 1 the error is 0.0038 of dq's norm in
+// keys share reaches dq by the sum of the roundings: with keys of mean 1 and spread 1 the error is 0.0039 of dq's norm in
 // bfloat16, with keys of mean 0 0.0024. No centre is subtracted from the keys: one that lies far from those that a row
 // attends carries that sum into dq without bound. Measured: 200 us for 8634 causal tokens of 16 over 4 heads of 128 bf16
 // (830 TFLOP/s), 47 us for 6446 tokens over 6453 of 12 heads of 64 (490 TFLOP/s); bound as the forward pass is.
@@ -487,7 +488,8 @@ __global__ __launch_bounds__(NW * 64, sizeof(T) == 2 && D == 64 ? 3 : 2) void at
 // adds them in order. Four waves in step, two workgroups to a CU; eight waves that also share out the rows of a tile
 // were slower (376 us against 330 for the whole call at 2 x 2048 x 16 heads of 128) but where one sequence of 768
 // tokens is all there is (50, 61). Measured: 293 us for the causal tokens named above (755 TFLOP/s), 576 us for 2 x
-// 4096 of 16 heads of 128 (955 TFLOP/s), 53 us for the 12 heads of 64 (585).
+// 4096 of 16 heads of 128 (955 TFLOP/s), 53 us for the 12 heads of 64 (585); it waits for 45% of its wave cycles in the
+// first and 38% in the last.
 constexpr int PART_ROWS = 512;
 struct RowPart { int from, to, begin, parts; };    // rows of one part for a tile; the tile's first part and the end of its parts
 __device__ __forceinline__ RowPart part_of(int first, int rows, int most, int rt, int part) {
@@ -726,7 +728,7 @@ __global__ __launch_bounds__(KW * 64, sizeof(T) == 4 && D == 128 ? 1 : 2) void a
 }
 
 // dk and dv of the key tiles whose rows were cut into parts: a workgroup for 32 keys of one of them. Bound by memory:
-// 16 us for up to 3 parts of 8634 x 4 heads of 128.
+// 34 us for up to 7 parts of 8634 x 4 heads of 128.
 template <class T, int D, int KW>
 __global__ __launch_bounds__(256) void attn_dkv_join_kernel(AttnArgs p) {
     constexpr int BK = KW * 32;

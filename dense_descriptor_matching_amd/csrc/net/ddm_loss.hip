@@ -120,8 +120,10 @@ __device__ __forceinline__ void hand_over(float (&v)[16], int lane) {
 // maximum: a wave keeps 32 rows, whose sums gather in the 16 elements of its score tiles over all columns, and adds each
 // tile's column sums (16 of a column's 32 in each lane half) to its own row of LDS. The match itself is left out:
 // lse - z_ii = log1p(e^-z_ii sum of the others) is exact where that is small. Per score 3.1 instructions and one
-// exponential, for which two passes take twice 3.75 and one. With the gradient: 16384 x 64 bf16 269 us against 319 in two
-// passes, 16 sets of up to 4096 x 24 fp16 168 against 177. Chunks of 256 rows (with 512 the first of the two has 1024
+// exponential, for which two passes take twice 3.75 and one. With the gradient: 16384 x 64 bf16 270 us against 293 in two
+// passes, 8000 x 24 fp32 234 against 272, 16 sets of up to 4096 x 24 fp16 169 against 167. Alone 79 us and 60 us for the first
+// and the last, 310 and 400 ns a tile of 32 x 32 on a SIMD: 95 and 103 vector and some 24 and 42 scalar instructions, and
+// waits for a quarter of the wave cycles. Chunks of 256 rows (with 512 the first of the two has 1024
 // workgroups, whose last third the card runs alone: 287 us), longer ones in calls of very many matches (see the plan).
 template <class T, int D, int BN>
 __global__ __launch_bounds__(256, 2) void loss_one_kernel(LossArgs p) {
@@ -210,7 +212,7 @@ __global__ __launch_bounds__(256, 2) void loss_one_kernel(LossArgs p) {
 // Forward, one direction (blockIdx.z), of the sets that do not take one pass: rows x of one side, columns y of the other.
 // As attention's forward without values; the maximum is exact here, since the loss of a clear match is the logarithm of
 // a sum next to 1. Bound by the vector units, 3.75 instructions and an exponential (four more's time) a score, and the
-// matrix cores behind them: 127 us for 2 x 16384 x 16384 scores of 64 components (bf16), 73 us for 16 sets of up to 4096
+// matrix cores behind them: 110 us for 2 x 16384 x 16384 scores of 64 components (bf16), 74 us for 16 sets of up to 4096
 // matches of 24 (fp16; 3.2e8 scores). Where every set takes one pass its workgroups end at once (5 us).
 template <class T, int D, int BN>
 __global__ __launch_bounds__(256, 2) void loss_fwd_kernel(LossArgs p) {
@@ -271,8 +273,9 @@ __global__ __launch_bounds__(256, 2) void loss_fwd_kernel(LossArgs p) {
         for (int b = 0; b < KB; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
-                // with the match among them the largest score counts as exactly 1; elsewhere ref's rounding is a common
-                // factor of 1 + 2^-20 at most on what is added, and saves an instruction a score
+                // with the match among them the largest score counts as exactly 1; elsewhere ref's rounding is a factor of
+                // up to 1 + |ref| 2^-24 on what this tile adds, no more than lse's own rounding, and saves an instruction a
+                // score
                 if constexpr (decltype(special)::value) sum += exp2_fast((z[b][r] - next_m) * p.c);
                 else s4[r % 4] += exp2_fast(__builtin_fmaf(z[b][r], p.c, -ref));
             }
@@ -347,7 +350,8 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossArgs p, float *loss,
 
 // Backward, one direction: dx of the rows, the gradient by the scores made tile by tile. fp16 holds it to few bits
 // below 2^-14, where a mean over many matches lies: there g is divided by a power of two next to its largest value in
-// reach first. The exponentials bound it, two a score. Where all lse in reach lie within 2^+-30 of a common e^mid, as
+// reach first. The exponentials bound it, two a score, and waits, a third
+// of its wave cycles. Where all lse in reach lie within 2^+-30 of a common e^mid, as
 // they do for unit-norm rows unless t is tiny, one is enough: e^{z - lse_y} = e^{z - lse_x} e^{lse_x - mid} e^{mid -
 // lse_y}, the last two known by row and column (what the first loses to underflow is below 2^-66 of g there). fp32
 // inputs, bound by their products, keep both. Measured on the same: 196 us (298 with two exponentials) and 111 us
@@ -575,7 +579,9 @@ Plan make_plan(int B, int P, int d, int dtype) {
     p.backward_bytes = std::max<size_t>(at + (p.direct ? 0 : 2 * (size_t)p.S * P * p.dp * 4), 256);
     p.ml = take(2 * (size_t)p.S * P * sizeof(float2));
     p.hit = take((size_t)P * 4);
-    // From 4096 matches on the two launches more are paid back: 4096 x 24 bf16 51.5 us against 51.7, 3000 49 against 48.
+    // From 4096 matches on the two launches more are paid back, with the gradient: 4096 x 24 bf16 51 us against 55 in two
+    // passes, fp32 100 against 109, 8000 x 24 fp32 234 against 272, 16384 x 64 bf16 270 against 293 (not quite for 24
+    // components in 16 bits between: 8000 x 24 bf16 82 against 79); below they are not: 3000 x 24 bf16 49 against 48.
     p.one = P >= 4096;
     p.slots = (int)slot_count(B, P, 1, 128);
     // A chunk of rows leaves a sum for each column of its set, which may be any length up to ONE_N: 512 bytes a match with

@@ -330,7 +330,8 @@ int ddm_mutual_nn_ex(const void *D1, int H1, int W1, const void *D2, int H2, int
  *                (T / 128 + B + 2) * Hkv < 2^24 (else DDM_ERR_INVALID, or 0 from a workspace size)
  * With few query rows and long sequences the keys are split over workgroups and joined (the workspace holds the parts).
  * Products take the inputs' type with fp32 accumulation; probabilities and their gradients are rounded to that type before
- * the second product. The workspace of backward is scratch: forward keeps only out and lse. */
+ * the second product; in DDM_F16 those gradients are held in units of the row's largest |dout|, of which
+ * P_ij |dout_i.(v_j - out_i)| is to stay below some 2^16. The workspace of backward is scratch: forward keeps only out and lse. */
 size_t ddm_attention_forward_workspace_bytes(int B, int Tq, int Tk, int Hq, int Hkv, int D, int dtype);
 int ddm_attention_forward(const void *q, int64_t q_ts, int64_t q_hs, const void *k, int64_t k_ts, int64_t k_hs,
                           const void *v, int64_t v_ts, int64_t v_hs, const int32_t *cu_q, const int32_t *cu_k, int B,
@@ -368,10 +369,10 @@ int ddm_layer_norm_backward(const void *dy, const void *x, int64_t ldx, const vo
  *   1 / temperature and log2(e) / temperature within float's normal range;
  *   0 <= P <= 2^24, B <= 2^20.
  * Rows outside every set: loss and lse 0, gradients 0.
- * Each direction has its own workspace size; ddm_matching_loss_workspace_bytes is the larger. With d padded to 32, 64 or 128 as
- * dp, both hold rows repacked (2 P dp elements) where they are not whole 16-byte pieces; forward sums of up to 640
- * bytes a match besides (384 from 2^18 matches on, 1 GiB at most), backward nothing but where few matches or d not a multiple of 4 need parts (2 P
- * dp floats, times up to 16 pieces below some 32,000 matches). */
+ * Each direction has its own workspace size; ddm_matching_loss_workspace_bytes is the larger. With d padded to 32, 64 or 128
+ * as dp, both have room for rows repacked to whole 16-byte pieces (2 P dp elements). Forward has sums of up to 640 bytes a
+ * match besides (384 from 2^18 matches on, 1 GiB at most). Backward has parts where d is no multiple of 4 or matches are few
+ * (2 P dp floats; times up to 16 below some 32,000 matches). */
 size_t ddm_matching_loss_forward_workspace_bytes(int B, int P, int d, int dtype);
 size_t ddm_matching_loss_backward_workspace_bytes(int B, int P, int d, int dtype);
 size_t ddm_matching_loss_workspace_bytes(int B, int P, int d, int dtype);
