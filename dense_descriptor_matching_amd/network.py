@@ -60,7 +60,7 @@ def _workspace_bytes(what, *sizes):
     """The library's workspace size for these sizes (a pure function of them)."""
     n = getattr(_api.lib(), what)(*sizes)
     if n == 0:
-        raise _api.DDMError(-4, f"{what} (unsupported sizes)")
+        raise _api.DDMError(-4, f"{what} (sizes outside the limits stated in include/ddm.h)")
     return n
 
 
