@@ -15,7 +15,8 @@ quoted in "DUSt3R和MASt3R论文阅读", section MASt3R matching).
 Pixel indices are linear, p = x + W * y; :func:`to_xy` converts.
 
 :mod:`dense_descriptor_matching_amd.network` has the operators of the network that
-produces the maps and of its training: :func:`attention`, :func:`layer_norm` and
+produces the maps and of its training: :func:`attention`, :func:`rotary`,
+:func:`layer_norm`, :func:`residual_norm`, :func:`gated_linear` and
 :func:`matching_loss`.
 """
 from __future__ import annotations
@@ -512,11 +513,15 @@ def mutual_nn(D1: torch.Tensor, D2: torch.Tensor, return_nn: bool = False, metri
 
 # ------------------------------------------------------------------- descriptor network
 from . import network  # noqa: E402  (uses this module's handle and checks)
-from .network import (attention, attention_backward, attention_forward, layer_norm, layer_norm_backward,  # noqa: E402
-                      layer_norm_forward, matching_loss, matching_loss_backward, matching_loss_forward)
+from .network import (attention, attention_backward, attention_forward, gated_linear, gated_linear_backward,  # noqa: E402
+                      gated_linear_forward, layer_norm, layer_norm_backward, layer_norm_forward, matching_loss,
+                      matching_loss_backward, matching_loss_forward, residual_norm, residual_norm_backward,
+                      residual_norm_forward, rotary, rotary_backward, rotary_forward, rotary_frequencies)
 
-__all__ = ["attention", "attention_forward", "attention_backward", "layer_norm", "layer_norm_forward",
-           "layer_norm_backward", "matching_loss", "matching_loss_forward", "matching_loss_backward",
+__all__ = ["attention", "attention_forward", "attention_backward", "rotary", "rotary_forward", "rotary_backward",
+           "rotary_frequencies", "layer_norm", "layer_norm_forward", "layer_norm_backward", "residual_norm",
+           "residual_norm_forward", "residual_norm_backward", "gated_linear", "gated_linear_forward", "gated_linear_backward",
+           "matching_loss", "matching_loss_forward", "matching_loss_backward",
            "nn", "frm_match", "frm_match_batched", "frm_match_into", "frm_match_ex", "c2f_match", "mutual_nn",
            "mutual_nn_into", "seed_count", "to_xy", "FrmBuffers", "MutualBuffers", "DDMError", "lib", "LIB_PATH",
            "profile_enable", "profile_read", "frm_set_mode", "frm_get_mode", "frm_set_barrier_polls",

@@ -8,7 +8,8 @@ from concurrent.futures import ThreadPoolExecutor
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "ddm.hip")
-NET_SRCS = [os.path.join(HERE, "csrc", "net", f) for f in ("ddm_attn.hip", "ddm_norm.hip", "ddm_loss.hip")]
+NET_SRCS = [os.path.join(HERE, "csrc", "net", f) for f in ("ddm_attn.hip", "ddm_norm.hip", "ddm_loss.hip", "ddm_rotary.hip",
+                                                           "ddm_residual.hip", "ddm_gated.hip")]
 OBJ_DIR = os.path.join(HERE, "build")
 LIB = os.path.join(HERE, "libddm.so")
 
@@ -49,7 +50,7 @@ def build(verbose: bool = False) -> str:
         run([hipcc, *COMMON_FLAGS, *(MATCH_FLAGS if src == SRC else []), "-c", "-o", obj, src])
         return obj
 
-    with ThreadPoolExecutor(max_workers=4) as pool:
+    with ThreadPoolExecutor(max_workers=7) as pool:
         objs = list(pool.map(compile_one, [SRC, *NET_SRCS]))
     tmp = LIB + ".tmp"
     run([hipcc, "--offload-arch=gfx950", "-shared", "-o", tmp, *objs])

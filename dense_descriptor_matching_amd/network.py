@@ -1,9 +1,10 @@
-"""Operators of the descriptor network and its training: attention, layer norm, matching loss.
+"""Operators of the descriptor network and its training: attention, rotary positions, norms, gated layer, matching loss.
 
 The maps that this package matches come from a transformer over image patches whose descriptor head is trained by a
 symmetric softmax loss over matched descriptors ("MASt3R" note on cv-learn.com, section 手法とアーキテクチャ). Each operator here
 has a forward and a backward function over the C ABI (``include/ddm.h`` documents them) and a differentiable one for
-torch's autograd: :func:`attention`, :func:`layer_norm`, :func:`matching_loss`.
+torch's autograd: :func:`attention`, :func:`rotary`, :func:`layer_norm`, :func:`residual_norm`, :func:`gated_linear`,
+:func:`matching_loss`.
 
 Packed sets: sequences of different lengths lie one after another along the first axis; ``cu`` (int32, device) holds
 the B + 1 places where they begin and end. The lengths stay on the device: no call waits for it.
@@ -12,6 +13,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import math
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -38,8 +40,23 @@ def declare(lib):
         f.argtypes, f.restype = [I] * 4, SZ
     lib.ddm_matching_loss_forward.argtypes = [P, P, P, I, I, I, I, F, P, P, P, P, SZ, P]
     lib.ddm_matching_loss_backward.argtypes = [P, P, P, P, P, P, I, I, I, I, F, P, P, P, SZ, P]
+    heads = [P, I64, I64, I]
+    lib.ddm_rotary.argtypes = heads * 2 + [P, P, I, I, I, I, I, I, I, F, P, I64, I64, P, I64, I64, P]
+    rows = [P, I64]
+    lib.ddm_residual_norm_forward.argtypes = rows * 3 + [P] * 5 + [I64, I, I, I, I, I, F, P, P, P, P]
+    lib.ddm_residual_norm_backward_workspace_bytes.argtypes = [I64, I, I, I]
+    lib.ddm_residual_norm_backward.argtypes = [P, P] + rows * 3 + [P] * 5 + [I64, I, I, I, I, I] + [P] * 9 + [SZ, P]
+    lib.ddm_gated_linear_forward.argtypes = rows + [P, P, I64, I, I, I, I, P, P, P, SZ, P]
+    lib.ddm_gated_linear_backward.argtypes = [P] + rows + [P, P, I64, I, I, I, I, P, P, P, P, SZ, P]
+    for f in (lib.ddm_gated_linear_forward_workspace_bytes, lib.ddm_gated_linear_backward_workspace_bytes):
+        f.argtypes = [I64, I, I, I]
+    for f in (lib.ddm_residual_norm_backward_workspace_bytes, lib.ddm_gated_linear_forward_workspace_bytes,
+              lib.ddm_gated_linear_backward_workspace_bytes):
+        f.restype = SZ
     for f in (lib.ddm_attention_forward, lib.ddm_attention_backward, lib.ddm_layer_norm_forward,
-              lib.ddm_layer_norm_backward, lib.ddm_matching_loss_forward, lib.ddm_matching_loss_backward):
+              lib.ddm_layer_norm_backward, lib.ddm_matching_loss_forward, lib.ddm_matching_loss_backward, lib.ddm_rotary,
+              lib.ddm_residual_norm_forward, lib.ddm_residual_norm_backward, lib.ddm_gated_linear_forward,
+              lib.ddm_gated_linear_backward):
         f.restype = I
 
 
@@ -259,6 +276,314 @@ class _LayerNorm(torch.autograd.Function):
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-6):
     """Differentiable :func:`layer_norm_forward`; returns y alone."""
     return _LayerNorm.apply(x, weight, bias, eps)
+
+
+# ------------------------------------------------------------------------------------------------------- rotary
+def rotary_frequencies(pairs: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
+                       length: int | None = None, slow: float = 1.0, fast: float = 32.0, device=None):
+    """Frequencies base ** (-i / pairs) of the pairs of an axis, float64 [pairs], as :func:`rotary` takes them.
+
+    ``scaling`` fits them to positions ``factor`` times as far as those trained on: "linear" divides all by the factor; "base"
+    raises the base so that the last pair's is divided by it and the first's stays; "ramp" divides those of pairs that turn at
+    most ``slow`` times over ``length`` positions, keeps those that turn ``fast`` times or more, and mixes between them in
+    proportion to the turns (a magnitude of 0.1 log(factor) + 1 goes with it)."""
+    if pairs < 1 or not base > 0 or not factor > 0:
+        raise ValueError("pairs, base and factor must be positive")
+    if scaling == "base" and pairs > 1:
+        base = base * factor ** (pairs / (pairs - 1))
+    f = base ** (-torch.arange(pairs, dtype=torch.float64) / pairs)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "ramp":
+        if length is None or not 0 <= slow < fast:
+            raise ValueError("ramp needs the length trained on, and slow below fast")
+        keep = ((length * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+    elif scaling not in (None, "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return f.to(device)
+
+
+def _rotary_heads(t, name):
+    if t is None:
+        return None, 0, 0, 0
+    if t.stride(2) != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr(), t.stride(0), t.stride(1), t.shape[1]
+
+
+def _rotary(q, k, positions, frequencies, interleaved, magnitude, inverse, out, names):
+    _tensor(q, names[0], contiguous=False)
+    if q.dim() != 3:
+        raise ValueError(f"{names[0]} must be [tokens, heads, head dimension]")
+    dev, (T, _, D) = q.device, q.shape
+    if k is not None:
+        _tensor(k, names[1], q.dtype, dev, contiguous=False)
+        if k.dim() != 3 or k.shape[0] != T or k.shape[2] != D:
+            raise ValueError(f"{names[1]} must share its tokens and its head dimension with {names[0]}")
+    _tensor(frequencies, "frequencies", torch.float64, dev)
+    if frequencies.dim() not in (1, 2) or frequencies.numel() == 0:
+        raise ValueError("frequencies must be [pairs] or [axes, pairs]")
+    axes, pairs = (1, *frequencies.shape) if frequencies.dim() == 1 else frequencies.shape
+    _tensor(positions, "positions", torch.int32, dev)
+    if tuple(positions.shape) not in ((T, axes),) + (((T,),) if axes == 1 else ()):
+        raise ValueError(f"positions must be [{T}, {axes}], one place on each axis a token, not {list(positions.shape)}")
+    if 2 * axes * pairs > D:
+        raise ValueError(f"{axes} axes of {pairs} pairs do not fit into heads of {D}")
+    if out is None:
+        qo = torch.empty_like(q, memory_format=torch.contiguous_format)
+        ko = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
+    else:
+        qo, ko = out
+        for t, s, name in ((qo, q, "out[0]"), (ko, k, "out[1]")):
+            if (t is None) != (s is None):
+                raise ValueError("out must hold one tensor for each of q and k")
+            if t is not None:
+                _tensor(t, name, q.dtype, dev, s.shape, contiguous=False)
+    qv, kv, qw, kw = (_rotary_heads(t, n) for t, n in ((q, names[0]), (k, names[1]), (qo, "out[0]"), (ko, "out[1]")))
+    _call(dev, "ddm_rotary", *qv, *kv, positions.data_ptr(), frequencies.data_ptr(), T, D, axes, pairs, _DT[q.dtype],
+          int(interleaved), int(inverse), float(magnitude), *qw[:3], *kw[:3])
+    return qo, ko
+
+
+def rotary_forward(q, k, positions, frequencies, *, interleaved: bool = False, magnitude: float = 1.0, out=None):
+    """Rotary positions of queries q [T, Hq, D] and keys k [T, Hk, D] (or None) of the same tokens; returns both.
+
+    ``positions`` int32 [T], or [T, axes] (row and column of an image patch); ``frequencies`` float64 [pairs] or [axes, pairs]
+    (:func:`rotary_frequencies`). The first 2 axes pairs elements of a head are turned, axis by axis, the rest stays: element i of an
+    axis' 2 pairs goes with i + pairs, or, ``interleaved``, 2i with 2i + 1, by the angle position * frequency, times ``magnitude``.
+    The tensors may be views (of a packed qkv projection, say) with contiguous heads. ``out`` holds tensors to write to, q and k
+    themselves among them."""
+    return _rotary(q, k, positions, frequencies, interleaved, magnitude, False, out, ("q", "k"))
+
+
+def rotary_backward(dq, dk, positions, frequencies, *, interleaved: bool = False, magnitude: float = 1.0, out=None):
+    """Gradients of :func:`rotary_forward` by q and k, from those by its outputs."""
+    return _rotary(dq, dk, positions, frequencies, interleaved, magnitude, True, out, ("dq", "dk"))
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, positions, frequencies, interleaved, magnitude):
+        ctx.save_for_backward(positions, frequencies)
+        ctx.options = dict(interleaved=interleaved, magnitude=magnitude)
+        ctx.set_materialize_grads(False)
+        q, k = rotary_forward(q, k, positions, frequencies, **ctx.options)
+        return q if k is None else (q, k)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk=None):
+        given = [t.contiguous() for t in (dq, dk) if t is not None]
+        if not given:
+            return (None,) * 6
+        if len(given) == 2:
+            dq, dk = rotary_backward(*given, *ctx.saved_tensors, **ctx.options)
+        else:
+            got, _ = rotary_backward(given[0], None, *ctx.saved_tensors, **ctx.options)
+            dq, dk = (got, None) if dq is not None else (None, got)
+        return dq, dk, None, None, None, None
+
+
+def rotary(q, k, positions, frequencies, *, interleaved: bool = False, magnitude: float = 1.0):
+    """Differentiable :func:`rotary_forward`; without k it returns q alone."""
+    return _Rotary.apply(q, k, positions, frequencies, interleaved, magnitude)
+
+
+# ------------------------------------------------------------------------------------------------ residual norm
+def _rows(t, name, like=None):
+    """(pointer, row stride) of t as rows of its last dimension."""
+    if t is None:
+        return None, 0
+    if like is not None:
+        _tensor(t, name, like.dtype, like.device, like.shape, contiguous=False)
+    cols = t.shape[-1]
+    if t.is_contiguous():
+        return t.data_ptr(), cols
+    if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < cols:
+        raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else cols
+
+
+def _residual_sizes(x, branch, gate, params, branch_norm):
+    _tensor(x, "x", contiguous=False)
+    if x.dim() == 0 or x.shape[-1] == 0:
+        raise ValueError("x must have a last dimension of at least one")
+    wtype = None
+    for name, t in params.items():
+        if t is None:
+            continue
+        _tensor(t, name, None, x.device, x.shape[-1:])
+        if t.dtype not in (torch.float32, x.dtype) or wtype not in (None, t.dtype):
+            raise TypeError("scale, weights and biases must share their dtype, float32 or x's")
+        if name.startswith("branch") and not branch_norm:
+            raise ValueError(f"{name} goes with branch_norm")
+        wtype = t.dtype
+    views = *_rows(x, "x", x), *_rows(branch, "branch", x), *_rows(gate, "gate", x)
+    return x.numel() // x.shape[-1], x.shape[-1], wtype or torch.float32, views
+
+
+def residual_norm_forward(x, branch, weight=None, bias=None, *, scale=None, gate=None, branch_norm: bool = False,
+                          branch_weight=None, branch_bias=None, rms: bool = False, eps: float = 1e-6):
+    """The sum of a residual stream and a block's branch, and its norm, over the last dimension:
+
+        t = branch, or with ``branch_norm`` norm(branch) * branch_weight + branch_bias
+        s = x + scale * sigmoid(gate) * t,    y = norm(s) * weight + bias
+
+    norm is a layer norm, with ``rms`` one without means. x, branch and gate share shape and type; the others have one value a column.
+    Returns (s, y, stats): stats float32 [2, rows...] holds the means and 1 / deviations of s, with ``branch_norm`` [4, rows...] and
+    those of the branch. y is taken of s before it is rounded."""
+    params = dict(scale=scale, branch_weight=branch_weight, branch_bias=branch_bias, weight=weight, bias=bias)
+    N, cols, wtype, views = _residual_sizes(x, branch, gate, params, branch_norm)
+    s, y = (torch.empty_like(x, memory_format=torch.contiguous_format) for _ in range(2))
+    stats = x.new_empty((4 if branch_norm else 2,) + x.shape[:-1], dtype=torch.float32)
+    _call(x.device, "ddm_residual_norm_forward", *views, *map(_at, params.values()), N, cols, _DT[x.dtype], _DT[wtype],
+          int(branch_norm), int(rms), float(eps), s.data_ptr(), y.data_ptr(), stats.data_ptr())
+    return s, y, stats
+
+
+_RESIDUAL_GRADIENTS = ("dx", "dbranch", "dweight", "dbias", "dscale", "dgate", "dbranch_weight", "dbranch_bias")
+
+
+def residual_norm_backward(dy, ds, x, branch, stats, weight=None, *, scale=None, gate=None, branch_norm: bool = False,
+                           branch_weight=None, branch_bias=None, rms: bool = False, wtype=None, needs=None):
+    """Gradients (dx, dbranch, dweight, dbias, dscale, dgate, dbranch_weight, dbranch_bias) of :func:`residual_norm_forward` by its
+    outputs' gradients dy and ds (None for zeros), from its inputs and stats. ``needs`` names those that are wanted, the others are
+    None; by default all but dscale without a scale, dgate without a gate and the branch's without ``branch_norm``. ``wtype`` is
+    the parameters' dtype where none of them is given (float32 by default)."""
+    params = dict(scale=scale, branch_weight=branch_weight, branch_bias=branch_bias, weight=weight)
+    N, cols, wt, views = _residual_sizes(x, branch, gate, params, branch_norm)
+    if wtype is not None and all(t is None for t in params.values()):
+        wt = wtype
+    if wt not in (torch.float32, x.dtype):
+        raise TypeError("wtype must be float32 or x's dtype")
+    for t, name in ((dy, "dy"), (ds, "ds")):
+        if t is not None:
+            _tensor(t, name, x.dtype, x.device, x.shape)
+    _tensor(stats, "stats", torch.float32, x.device, (4 if branch_norm else 2,) + x.shape[:-1])
+    if needs is None:
+        needs = {"dx", "dbranch", "dweight", "dbias"}
+        needs |= ({"dscale"} if scale is not None else set()) | ({"dgate"} if gate is not None else set())
+        needs |= {"dbranch_weight", "dbranch_bias"} if branch_norm else set()
+    needs = set(needs)
+    if needs - set(_RESIDUAL_GRADIENTS):
+        raise ValueError(f"unknown gradients {sorted(needs - set(_RESIDUAL_GRADIENTS))}")
+    if ("dgate" in needs and gate is None) or (not branch_norm and needs & {"dbranch_weight", "dbranch_bias"}):
+        raise ValueError("a gradient by what the call does not have")
+    got = {n: None if n not in needs else
+           torch.empty_like(x, memory_format=torch.contiguous_format) if n in ("dx", "dbranch", "dgate") else
+           x.new_empty(cols, dtype=wt) for n in _RESIDUAL_GRADIENTS}
+    nbytes, ws = 0, None
+    if needs - {"dx", "dbranch", "dgate"}:
+        nbytes = _workspace_bytes("ddm_residual_norm_backward_workspace_bytes", N, cols, _DT[x.dtype], int(branch_norm))
+        ws = x.new_empty(nbytes, dtype=torch.uint8)
+    _call(x.device, "ddm_residual_norm_backward", _at(dy), _at(ds), *views, *map(_at, params.values()), stats.data_ptr(), N, cols,
+          _DT[x.dtype], _DT[wt], int(branch_norm), int(rms),
+          *(_at(got[n]) for n in ("dx", "dbranch", "dgate", "dscale", "dbranch_weight", "dbranch_bias", "dweight", "dbias")),
+          _at(ws), nbytes)
+    return tuple(got[n] for n in _RESIDUAL_GRADIENTS)
+
+
+class _ResidualNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, branch, weight, bias, scale, gate, branch_weight, branch_bias, branch_norm, rms, eps):
+        s, y, stats = residual_norm_forward(x, branch, weight, bias, scale=scale, gate=gate, branch_norm=branch_norm,
+                                            branch_weight=branch_weight, branch_bias=branch_bias, rms=rms, eps=eps)
+        ctx.save_for_backward(x, branch, weight, scale, gate, branch_weight, branch_bias, stats)
+        ctx.options = dict(branch_norm=branch_norm, rms=rms, wtype=None if bias is None else bias.dtype)
+        ctx.set_materialize_grads(False)
+        return s, y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, ds, dy):
+        x, branch, weight, scale, gate, branch_weight, branch_bias, stats = ctx.saved_tensors
+        if ds is None and dy is None:
+            return (None,) * 11
+        ds, dy = (None if t is None else t.contiguous() for t in (ds, dy))
+        needs = {n for n, wanted in zip(_RESIDUAL_GRADIENTS, ctx.needs_input_grad) if wanted}
+        return residual_norm_backward(dy, ds, x, branch, stats, weight, scale=scale, gate=gate, branch_weight=branch_weight,
+                                      branch_bias=branch_bias, needs=needs, **ctx.options) + (None,) * 3
+
+
+def residual_norm(x, branch, weight=None, bias=None, *, scale=None, gate=None, branch_norm: bool = False, branch_weight=None,
+                  branch_bias=None, rms: bool = False, eps: float = 1e-6):
+    """Differentiable :func:`residual_norm_forward`; returns (s, y)."""
+    return _ResidualNorm.apply(x, branch, weight, bias, scale, gate, branch_weight, branch_bias, branch_norm, rms, eps)
+
+
+# ------------------------------------------------------------------------------------------------- gated linear
+ACTIVATIONS = {"silu": 0, "gelu": 1, "sigmoid": 2}
+
+
+def _gated_sizes(x, weight, activation):
+    _tensor(x, "x", contiguous=False)
+    if x.dim() == 0 or x.shape[-1] == 0:
+        raise ValueError("x must have a last dimension of at least one")
+    _tensor(weight, "weight", x.dtype, x.device)
+    if weight.dim() != 2 or weight.shape[1] != x.shape[-1] or weight.shape[0] % 2 or weight.shape[0] == 0:
+        raise ValueError("weight must be [2 * hidden, columns of x]: the gate's rows, then the other projection's")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    return x.numel() // x.shape[-1], x.shape[-1], weight.shape[0] // 2, _DT[x.dtype]
+
+
+def gated_linear_forward(x, weight, bias=None, *, activation: str = "silu", keep: bool = False):
+    """Gated linear layer h = act(x Wg^T + bg) * (x Wu^T + bu) of x [..., C]: weight [2F, C] holds the F rows of Wg and then those of Wu,
+    bias [2F] likewise. Returns (h [..., F], kept): kept [..., 2F] is what :func:`gated_linear_backward` needs with ``keep``, else
+    None. ``activation``: "silu" g * sigmoid(g), "gelu" g * Phi(g), "sigmoid"."""
+    sizes = _gated_sizes(x, weight, activation)
+    F = sizes[2]
+    if bias is not None:
+        _tensor(bias, "bias", x.dtype, x.device, (2 * F,))
+    view = _rows(x, "x")
+    nbytes = _workspace_bytes("ddm_gated_linear_forward_workspace_bytes", *sizes)
+    h = x.new_empty(x.shape[:-1] + (F,))
+    kept = x.new_empty(x.shape[:-1] + (2 * F,)) if keep else None
+    ws = x.new_empty(nbytes, dtype=torch.uint8)
+    _call(x.device, "ddm_gated_linear_forward", *view, weight.data_ptr(), _at(bias), *sizes, ACTIVATIONS[activation], h.data_ptr(),
+          _at(kept), ws.data_ptr(), nbytes)
+    return h, kept
+
+
+def gated_linear_backward(dh, x, weight, kept, *, activation: str = "silu", need_dx: bool = True, need_dweight: bool = True,
+                          need_dbias: bool = True):
+    """Gradients (dx, dweight, dbias) of :func:`gated_linear_forward` by its h; None for those not wanted."""
+    sizes = _gated_sizes(x, weight, activation)
+    F = sizes[2]
+    _tensor(dh, "dh", x.dtype, x.device, x.shape[:-1] + (F,))
+    _tensor(kept, "kept", x.dtype, x.device, x.shape[:-1] + (2 * F,))
+    view = _rows(x, "x")
+    nbytes = _workspace_bytes("ddm_gated_linear_backward_workspace_bytes", *sizes)
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
+    dw = torch.empty_like(weight) if need_dweight else None
+    db = x.new_empty(2 * F) if need_dbias else None
+    ws = x.new_empty(nbytes, dtype=torch.uint8)
+    _call(x.device, "ddm_gated_linear_backward", dh.data_ptr(), *view, weight.data_ptr(), kept.data_ptr(), *sizes,
+          ACTIVATIONS[activation], _at(dx), _at(dw), _at(db), ws.data_ptr(), nbytes)
+    return dx, dw, db
+
+
+class _GatedLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, activation):
+        h, kept = gated_linear_forward(x, weight, bias, activation=activation, keep=any(ctx.needs_input_grad))
+        ctx.save_for_backward(x, weight, kept)
+        ctx.activation = activation
+        return h
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dh):
+        x, weight, kept = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        return gated_linear_backward(dh.contiguous(), x, weight, kept, activation=ctx.activation, need_dx=need[0], need_dweight=need[1],
+                                     need_dbias=need[2]) + (None,)
+
+
+def gated_linear(x, weight, bias=None, *, activation: str = "silu"):
+    """Differentiable :func:`gated_linear_forward`; returns h alone."""
+    return _GatedLinear.apply(x, weight, bias, activation)
 
 
 # ------------------------------------------------------------------------------------------------- matching loss

@@ -383,6 +383,72 @@ int ddm_matching_loss_backward(const float *dloss, const void *a, const void *b,
                                const int32_t *cu, int B, int P, int d, int dtype, double temperature, void *da, void *db,
                                void *workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* Rotary positions: pairs of a head's elements are turned by an angle that grows with the token's position,
+ *   angle = position * frequency,  c = magnitude cos(angle),  s = magnitude sin(angle),  (a, b) -> (a c - b s, a s + b c)
+ * for every head of q and k alike. A token has a position on each of `axes` axes (1 for text, 2 for rows and columns of
+ * patches); a head's first 2 axes pairs elements are turned, axis by axis, the others are copied. Of an axis' 2 pairs elements
+ * x, pair i is (x[i], x[i + pairs]), or (x[2i], x[2i + 1]) with interleaved = 1. inverse = 1 negates the angle: that is the
+ * gradient of the call without it, for dq and dk in the place of q and k.
+ *   q, q_out       [T][Hq][D], row (t, h) at q + (t * q_ts + h * q_hs) elements, D elements contiguous; k, k_out likewise with
+ *                  Hk heads; any non-negative strides. Outputs may be the inputs themselves (with the same strides) but must
+ *                  not overlap them otherwise. Hq or Hk may be 0 (its pointers are not read). Whole 16-byte pieces are fastest.
+ *   positions      device int32[T][axes], any values
+ *   frequencies    device double[axes][pairs]. Angles are taken in 64 bits; up to some 2^30 sine and cosine are within 2^-22.
+ *   1 <= D <= DDM_MAX_ROTARY_D, 2 axes pairs <= D, Hq, Hk <= DDM_MAX_ROTARY_HEADS; magnitude finite. */
+#define DDM_MAX_ROTARY_D 1024
+#define DDM_MAX_ROTARY_HEADS 65536
+int ddm_rotary(const void *q, int64_t q_ts, int64_t q_hs, int Hq, const void *k, int64_t k_ts, int64_t k_hs, int Hk,
+               const int32_t *positions, const double *frequencies, int T, int D, int axes, int pairs, int dtype,
+               int interleaved, int inverse, double magnitude, void *q_out, int64_t qo_ts, int64_t qo_hs, void *k_out,
+               int64_t ko_ts, int64_t ko_hs, hipStream_t stream);
+
+/* The sum of a residual stream and a block's branch with the norms around it, over the last axis of [N][C]:
+ *   t = branch, or with branch_norm = 1 norm(branch) branch_weight + branch_bias
+ *   s = x + scale sigmoid(gate) t,   y = norm(s) weight + bias
+ *   norm(z) = (z - mean) rstd,  rstd = (var + eps)^-1/2;  rms = 1: without the mean, var = mean of squares
+ *   x, branch, gate  in dtype with row strides ldx, ldb, ldg >= C elements, the other rows contiguous; any alignment of whole
+ *                    elements; gate may be NULL (a factor of 1)
+ *   scale, weight, bias, branch_weight, branch_bias  [C] in wtype (DDM_F32 or dtype), each may be NULL (1, 1, 0, 1, 0); the
+ *                    branch's only with branch_norm
+ *   stats            float [2][N]: mean and rstd of s; with branch_norm [4][N]: and those of the branch
+ * y and the statistics are taken of s before it is rounded. Backward takes the gradients dy and ds (contiguous; NULL stands for zeros)
+ * by both outputs, forward's inputs and its stats. Each of its outputs may be NULL when it is not wanted; those by parameters are in wtype.
+ * 1 <= C <= DDM_MAX_NORM_C, 0 <= N < 2^31 (N = 0: the parameters' gradients are zeros), eps >= 0. */
+int ddm_residual_norm_forward(const void *x, int64_t ldx, const void *branch, int64_t ldb, const void *gate, int64_t ldg,
+                              const void *scale, const void *branch_weight, const void *branch_bias, const void *weight,
+                              const void *bias, int64_t N, int C, int dtype, int wtype, int branch_norm, int rms,
+                              double eps, void *s, void *y, float *stats, hipStream_t stream);
+size_t ddm_residual_norm_backward_workspace_bytes(int64_t N, int C, int dtype, int branch_norm);
+int ddm_residual_norm_backward(const void *dy, const void *ds, const void *x, int64_t ldx, const void *branch, int64_t ldb,
+                               const void *gate, int64_t ldg, const void *scale, const void *branch_weight,
+                               const void *branch_bias, const void *weight, const float *stats, int64_t N, int C, int dtype,
+                               int wtype, int branch_norm, int rms, void *dx, void *dbranch, void *dgate, void *dscale,
+                               void *dbranch_weight, void *dbranch_bias, void *dweight, void *dbias, void *workspace,
+                               size_t workspace_bytes, hipStream_t stream);
+
+/* Gated linear layer of [N][C] rows: both projections, the activation and the product in one pass.
+ *   g = x Wg^T + bg,  u = x Wu^T + bu,  h = act(g) u        act: DDM_SILU g sigmoid(g), DDM_GELU g Phi(g), DDM_SIGMOID sigmoid(g)
+ *   dg = dh u act'(g),  du = dh act(g),  dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dbg, dbu = their sums over rows
+ *   x            [N][C] with row stride ldx >= C elements, at most 4 MB; weight [2F][C]: the F rows of Wg, then those of Wu, 16-byte
+ *                aligned; bias [2F] or NULL; all in dtype, as h, dh [N][F], dx [N][C], dweight [2F][C] and dbias [2F], contiguous,
+ *                at any whole element
+ *   kept         [N][2F] in dtype: rows of g and u, what backward needs of forward; NULL when no gradient is wanted
+ *   Each of dx, dweight, dbias may be NULL when it is not wanted.
+ * Products take the inputs' type with fp32 accumulation; g, u (in kept) and dg, du are rounded to that type between the products
+ * of a gradient. Rows that are not whole 16-byte pieces are repacked into the workspace first.
+ * 1 <= C, F <= DDM_MAX_GATED with F C element size (C padded to 16 bytes) below 1 GB, 0 <= N <= DDM_MAX_GATED_ROWS (N = 0: the
+ * gradients of weight and bias are zeros). */
+enum { DDM_SILU = 0, DDM_GELU = 1, DDM_SIGMOID = 2 };
+#define DDM_MAX_GATED 262144
+#define DDM_MAX_GATED_ROWS 16777216
+size_t ddm_gated_linear_forward_workspace_bytes(int64_t N, int C, int F, int dtype);
+int ddm_gated_linear_forward(const void *x, int64_t ldx, const void *weight, const void *bias, int64_t N, int C, int F, int dtype,
+                             int activation, void *h, void *kept, void *workspace, size_t workspace_bytes, hipStream_t stream);
+size_t ddm_gated_linear_backward_workspace_bytes(int64_t N, int C, int F, int dtype);
+int ddm_gated_linear_backward(const void *dh, const void *x, int64_t ldx, const void *weight, const void *kept, int64_t N, int C,
+                              int F, int dtype, int activation, void *dx, void *dweight, void *dbias, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
 /* ------------------------------------------------------- kernel timing ---
  * Benchmark aid, off by default. ddm_profile_enable(mask) makes later calls
  * bracket each fused NN sweep launch with two HIP events on the call's stream:
