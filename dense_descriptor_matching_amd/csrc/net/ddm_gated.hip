@@ -24,10 +24,11 @@ struct GatedArgs {
     int64_t ldp, ldq, ldo;                     // their row strides and the output's, elements
     int64_t seg_p, seg_q;                      // BY_X: from gate to up; BY_W: q alone
     int np, nq, k;                             // FORWARD: np = F pairs of rows
-    int tiles_q, tiles_p, splits;
+    int tiles_q, tiles_p;
+    Shares cut;
     const void *bias;
     void *out, *kept;
-    float *part;                               // splits > 1: [split][output rows][outputs of a row]
+    f32x4 *part;                               // slots of a tile's sums
     int act;
 };
 
@@ -82,197 +83,225 @@ struct Stage {
     }
 };
 
+// N matrix instructions with so many reads of LDS and loads between them, evenly, so that none waits for all of the
+// others.
+template <int N, int READS, int LOADS, int I = 0>
+__device__ __forceinline__ void interleave() {
+    constexpr int reads = (I + 1) * READS / N - I * READS / N, loads = (I + 1) * LOADS / N - I * LOADS / N;
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
+    if constexpr (loads > 0) __builtin_amdgcn_sched_group_barrier(0x020, loads, 0);
+    if constexpr (I + 1 < N) interleave<N, READS, LOADS, I + 1>();
+}
+
 // WQ x WP waves of MQ x MP blocks of 32 x 32 outputs. FORWARD: half of a wave's blocks along p are of Wg, half of the
 // same rows of Wu.
 template <class T, int KIND, int WQ, int WP, int MQ, int MP>
-__global__ __launch_bounds__(WQ *WP * 64) void gated_product_kernel(GatedArgs a) {
-    constexpr int NW = WQ * WP, BQ = WQ * MQ * 32, BP = WP * MP * 32, BK = 128 / (int)sizeof(T);
+struct Product {
+    static constexpr int NW = WQ * WP, BQ = WQ * MQ * 32, BP = WP * MP * 32, PAIRS = KIND == FORWARD ? BP / 2 : BP;
+    static constexpr int W = (KIND == FORWARD ? MP / 2 : MP) * 32;     // columns of a wave's outputs
+    static constexpr int SLOT = NW * MQ * MP * 4 * 64;                 // f32x4 of a tile's sums
+    using St = Stage<T, W>;
     using P = Side<T, BP, KIND != FORWARD, NW>;
     using Q = Side<T, BQ, KIND == BY_W, NW>;
-    constexpr int STEP = P::BYTES + Q::BYTES;
-    constexpr int W = (KIND == FORWARD ? MP / 2 : MP) * 32;            // columns of a wave's outputs
-    constexpr int LDS = 2 * STEP > NW * Stage<T, W>::BYTES ? 2 * STEP : NW * Stage<T, W>::BYTES;
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[LDS];
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wq = w / WP, wp = w % WP;
-    const int tiles = a.tiles_q * a.tiles_p, split = blockIdx.x / tiles;
-    TileAt t = tile_at(blockIdx.x - split * tiles, a.tiles_q, a.tiles_p);
-    // BY_W: the upper half of the tiles along q is that of dWu
-    const int part = KIND == BY_W && t.q >= a.tiles_q / 2;
-    if (part) t.q -= a.tiles_q / 2;
-    constexpr int PAIRS = KIND == FORWARD ? BP / 2 : BP;
-    const int q0 = t.q * BQ, p0 = t.p * PAIRS;
-    const int per = (a.k + BK - 1) / BK, all = KIND == BY_X ? 2 * per : per;
-    const int each = (all + a.splits - 1) / a.splits, begin = split * each, end = min(begin + each, all);
 
-    P feed_p;
-    Q feed_q;
-    auto start = [&](int step) {                                       // at step `step` of all
-        const int seg = KIND == BY_X && step >= per, s = step - seg * per, k = s * BK;
-        const T *p = (const T *)a.p, *q = (const T *)a.q + part * a.seg_q;
-        if (KIND == BY_X) { p += seg * a.seg_p; q += seg * a.seg_q; }
+    // First q and p of tile i of all. BY_W: the upper half of the tiles along q is that of dWu.
+    struct At { int q0, p0, part; };
+    __device__ static __forceinline__ At at(const GatedArgs &a, int i) {
+        TileAt t = tile_at(i, a.tiles_q, a.tiles_p);
+        const int part = KIND == BY_W && t.q >= a.tiles_q / 2;
+        if (part) t.q -= a.tiles_q / 2;
+        return {t.q * BQ, t.p * PAIRS, part};
+    }
+
+    // What is done with row block i of a wave's sums, c. A lane has row l % 32, columns 8 (r / 4) + 4 h + r % 4 of block j.
+    __device__ static __forceinline__ void finish(const GatedArgs &a, At t, int i, int w, int lane, f32x16 (&c)[MP], unsigned char *mine) {
+        const int q = t.q0 + (w / WP * MQ + i) * 32, p = t.p0 + w % WP * W, rows = a.nq - q, cols = a.np - p, h = lane >> 5;
+        T *out = (T *)a.out + (int64_t)(t.part * a.nq + q) * a.ldo + p;
         if constexpr (KIND == FORWARD) {
-            feed_p.start(p + p0 * a.ldp + k, a.ldp, a.k - k, 0, w, lane, [&](int i) {
-                const int sub = i / 32 % MP, f = i / 32 / MP * (MP / 2 * 32) + sub % (MP / 2) * 32 + i % 32;
-                return p0 + f < a.np ? (int64_t)f + (sub >= MP / 2 ? a.np : 0) : -1;
-            });
-        } else {
-            feed_p.start(p + k * a.ldp + p0, a.ldp, a.k - k, a.np - p0, w, lane, [](int) { return -1; });
-        }
-        if constexpr (KIND == BY_W) {
-            feed_q.start(q + k * a.ldq + q0, a.ldq, a.k - k, a.nq - q0, w, lane, [](int) { return -1; });
-        } else {
-            feed_q.start(q + q0 * a.ldq + k, a.ldq, a.k - k, 0, w, lane, [&](int i) { return q0 + i < a.nq ? i : -1; });
-        }
-    };
-    auto next = [&](int step, unsigned char *to) {
-        if (KIND == BY_X && step == per) start(step);
-        feed_q.next(to, w, lane);
-        feed_p.next(to + Q::BYTES, w, lane);
-    };
-
-    f32x16 c[MQ][MP];
+            if (const T *bias = (const T *)a.bias) {
 #pragma unroll
-    for (int i = 0; i < MQ; ++i)
+                for (int j = 0; j < MP; ++j) {
 #pragma unroll
-        for (int j = 0; j < MP; ++j)
+                    for (int r = 0; r < 16; r += 4) {
+                        float b[4];
+                        load_chunk<T, 4>(bias + (j >= MP / 2 ? a.np : 0), p + j % (MP / 2) * 32 + 2 * r + 4 * h, a.np, b);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) c[i][j][r] = 0.f;
-    const int at_q = Q::frag_base(lane), at_p = P::frag_base(lane);
-    if (begin < end) {
-        start(begin);
-        next(begin, lds);
-    }
-    for (int step = begin; step < end; ++step) {
-        const unsigned char *now = lds + ((step - begin) & 1) * STEP;
-        tiles_ready();
-        if (step + 1 < end) next(step + 1, lds + ((step + 1 - begin) & 1) * STEP);
-#pragma unroll
-        for (int s = 0; s < BK / 16; ++s) {
-            Frag<T> fq[MQ], fp[MP];
-#pragma unroll
-            for (int i = 0; i < MQ; ++i) fq[i] = Q::frag(now, at_q, wq * MQ + i, s);
-#pragma unroll
-            for (int j = 0; j < MP; ++j) fp[j] = P::frag(now + Q::BYTES, at_p, wp * MP + j, s);
-#pragma unroll
-            for (int i = 0; i < MQ; ++i)
-#pragma unroll
-                for (int j = 0; j < MP; ++j) mma(c[i][j], fp[j], fq[i]);
-        }
-    }
-
-    // lane: row q of block i, columns 8 (r / 4) + 4 h + r % 4 of block j
-    const int h = lane >> 5;
-    const int first_q = q0 + wq * MQ * 32, first_p = p0 + wp * W, out_q = part * a.nq;
-    if (a.splits > 1) {
-        // FORWARD: all of g, then all of u
-        const int64_t rows = KIND == BY_W ? 2 * (int64_t)a.nq : a.nq, width = KIND == FORWARD ? 2 * (int64_t)a.np : a.np;
-        float *to = a.part + split * rows * width;
-#pragma unroll
-        for (int i = 0; i < MQ; ++i) {
-            const int q = first_q + i * 32 + (lane & 31);
-            if (q >= a.nq) continue;
-#pragma unroll
-            for (int j = 0; j < MP; ++j) {
-                const bool up = KIND == FORWARD && j >= MP / 2;
-                float *row = to + (out_q + q) * width + (up ? a.np : 0);
-#pragma unroll
-                for (int r = 0; r < 16; r += 4) {
-                    const int p = first_p + (up ? j - MP / 2 : j) * 32 + 2 * r + 4 * h;
-                    const float v[4] = {c[i][j][r], c[i][j][r + 1], c[i][j][r + 2], c[i][j][r + 3]};
-                    store_chunk<float, 4>(row, p, a.np, v);
+                        for (int e = 0; e < 4; ++e) c[j][r + e] += b[e];
+                    }
+                    __builtin_amdgcn_sched_barrier(0);                 // few registers at a time
                 }
             }
-        }
-        return;
-    }
-    __syncthreads();                                                   // the last step's tiles have been read
-    unsigned char *mine = lds + w * Stage<T, W>::BYTES;
-    const T *bias = (const T *)a.bias;
-#pragma unroll
-    for (int i = 0; i < MQ; ++i) {
-        const int q = first_q + i * 32, rows = a.nq - q, cols = a.np - first_p;
-        T *out = (T *)a.out + (int64_t)(out_q + q) * a.ldo + first_p;
-        if constexpr (KIND == FORWARD) {
-            if (bias) {
-#pragma unroll
-                for (int j = 0; j < MP; ++j)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int f = first_p + j % (MP / 2) * 32 + r / 4 * 8 + 4 * h + r % 4;
-                        c[i][j][r] += (float)bias[min(f, a.np - 1) + (j >= MP / 2 ? a.np : 0)];
-                    }
-            }
             if (a.kept) {
-                T *to = (T *)a.kept + (int64_t)q * (2 * (int64_t)a.np) + first_p;
+                T *to = (T *)a.kept + (int64_t)q * (2 * (int64_t)a.np) + p;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                    for (int j = 0; j < MP / 2; ++j) Stage<T, W>::put(mine, lane, j, c[i][half * (MP / 2) + j]);
-                    Stage<T, W>::store(mine, lane, to + (half ? a.np : 0), 2 * (int64_t)a.np, rows, cols);
+                    for (int j = 0; j < MP / 2; ++j) St::put(mine, lane, j, c[half * (MP / 2) + j]);
+                    St::store(mine, lane, to + (half ? a.np : 0), 2 * (int64_t)a.np, rows, cols);
                 }
             }
 #pragma unroll
             for (int j = 0; j < MP / 2; ++j) {
                 f32x16 y;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) y[r] = activation(c[i][j][r], a.act).x * c[i][j + MP / 2][r];
-                Stage<T, W>::put(mine, lane, j, y);
+                for (int r = 0; r < 16; ++r) y[r] = activation(c[j][r], a.act).x * c[j + MP / 2][r];
+                St::put(mine, lane, j, y);
+                __builtin_amdgcn_sched_barrier(0);
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < MP; ++j) Stage<T, W>::put(mine, lane, j, c[i][j]);
+            for (int j = 0; j < MP; ++j) St::put(mine, lane, j, c[j]);
         }
-        Stage<T, W>::store(mine, lane, out, a.ldo, rows, cols);
+        St::store(mine, lane, out, a.ldo, rows, cols);
+    }
+};
+
+template <class T, int KIND, int WQ, int WP, int MQ, int MP, int PLACES, int WGS>
+__global__ __launch_bounds__(WQ *WP * 64, WGS * WQ * WP / 4) void gated_product_kernel(GatedArgs a) {
+    using Pr = Product<T, KIND, WQ, WP, MQ, MP>;
+    using P = typename Pr::P;
+    using Q = typename Pr::Q;
+    constexpr int NW = Pr::NW, BK = STEP_BYTES / (int)sizeof(T);
+    constexpr int TILE = P::BYTES + Q::BYTES, LOADS = P::LOADS + Q::LOADS, READS = MQ * Q::READS + MP * P::READS;
+    constexpr int LDS = PLACES * TILE > NW * Pr::St::BYTES ? PLACES * TILE : NW * Pr::St::BYTES;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[LDS];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wq = w / WP, wp = w % WP;
+    const int per = (a.k + BK - 1) / BK, all = KIND == BY_X ? 2 * per : per;       // steps of a segment, of a tile
+    const int at_q = Q::frag_base(lane), at_p = P::frag_base(lane);
+    // this workgroup's steps of a row of tiles' steps
+    int share = 0, from = 0, to = all, tile;
+    if ((int)blockIdx.x < a.cut.whole) {
+        tile = by_xcd(blockIdx.x, a.cut.whole);
+    } else {
+        share = by_xcd(blockIdx.x - a.cut.whole, a.cut.tail * a.cut.of);
+        tile = a.cut.whole + share / a.cut.of;
+        from = share % a.cut.of * a.cut.each;
+        to = min(from + a.cut.each, all);
+    }
+
+    {
+        const typename Pr::At t = Pr::at(a, tile);
+        P feed_p;
+        Q feed_q;
+        auto start = [&](int step) {                                   // at step `step` of the tile's
+            const int seg = KIND == BY_X && step >= per, s = step - seg * per, k = s * BK;
+            const T *p = (const T *)a.p, *q = (const T *)a.q + t.part * a.seg_q;
+            if (KIND == BY_X) { p += seg * a.seg_p; q += seg * a.seg_q; }
+            if constexpr (KIND == FORWARD) {
+                feed_p.start(p + t.p0 * a.ldp + k, a.ldp, a.k - k, 0, w, lane, [&](int i) {
+                    const int sub = i / 32 % MP, f = i / 32 / MP * (MP / 2 * 32) + sub % (MP / 2) * 32 + i % 32;
+                    return t.p0 + f < a.np ? (int64_t)f + (sub >= MP / 2 ? a.np : 0) : -1;
+                });
+            } else {
+                feed_p.start(p + k * a.ldp + t.p0, a.ldp, a.k - k, a.np - t.p0, w, lane, [](int) { return -1; });
+            }
+            if constexpr (KIND == BY_W) {
+                feed_q.start(q + k * a.ldq + t.q0, a.ldq, a.k - k, a.nq - t.q0, w, lane, [](int) { return -1; });
+            } else {
+                feed_q.start(q + t.q0 * a.ldq + k, a.ldq, a.k - k, 0, w, lane, [&](int i) { return t.q0 + i < a.nq ? i : -1; });
+            }
+        };
+        auto next = [&](int step, unsigned char *to) {
+            if (KIND == BY_X && step == per) start(step);
+            feed_q.next(to, w, lane);
+            feed_p.next(to + Q::BYTES, w, lane);
+        };
+
+        f32x16 c[MQ][MP];
+#pragma unroll
+        for (int i = 0; i < MQ; ++i)
+#pragma unroll
+            for (int j = 0; j < MP; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) c[i][j][r] = 0.f;
+        struct Frags { Frag<T> q[MQ], p[MP]; };
+        auto read = [&](Frags &f, const unsigned char *from, int s) {
+#pragma unroll
+            for (int i = 0; i < MQ; ++i) f.q[i] = Q::frag(from, at_q, wq * MQ + i, s);
+#pragma unroll
+            for (int j = 0; j < MP; ++j) f.p[j] = P::frag(from + Q::BYTES, at_p, wp * MP + j, s);
+        };
+        auto multiply = [&](const Frags &f) {
+#pragma unroll
+            for (int i = 0; i < MQ; ++i)
+#pragma unroll
+                for (int j = 0; j < MP; ++j) mma(c[i][j], f.p[j], f.q[i]);
+        };
+        // A step's first operands are in registers when it begins, and its tile and the next one's are in LDS; the tile
+        // that is asked for goes to the place of the last step's, which every wave has read by then. The pointers do
+        // not alias, or each step would wait for the tiles of the next ones.
+        Frags f0, f1;
+        auto body = [&](int step, const unsigned char *__restrict now, const unsigned char *__restrict after, unsigned char *__restrict to) {
+            loaded<(PLACES - 3) * LOADS>();                            // the next step's tile; those behind it may take their time
+            __builtin_amdgcn_sched_barrier(0);
+            next(step + PLACES - 1, to);
+            if constexpr (sizeof(T) == 2) {
+                read(f1, now, 1);
+                multiply(f0);
+                interleave<MQ * MP, READS, LOADS>();
+                __builtin_amdgcn_sched_barrier(0);
+                read(f0, after, 0);
+                multiply(f1);
+                interleave<MQ * MP, READS, 0>();
+            } else {
+                read(f1, after, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(f0);
+                f0 = f1;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        start(from);
+#pragma unroll
+        for (int i = 0; i < PLACES - 1; ++i) next(from + i, lds + i * TILE);
+        loaded<(PLACES - 2) * LOADS>();
+        read(f0, lds, 0);
+        int at = 0;
+        for (int step = from; step < to; ++step) {
+            const int after = at == (PLACES - 1) * TILE ? 0 : at + TILE, before = at == 0 ? (PLACES - 1) * TILE : at - TILE;
+            body(step, lds + at, lds + after, lds + before);
+            at = after;
+        }
+        tiles_ready();                                                 // nothing reads or fills LDS any more
+        if (tile < a.cut.whole) {
+#pragma unroll
+            for (int i = 0; i < MQ; ++i) Pr::finish(a, t, i, w, lane, c[i], lds + w * Pr::St::BYTES);
+            return;
+        }
+        f32x4 *part = a.part + (int64_t)share * Pr::SLOT + w * (MQ * MP * 4 * 64) + lane;
+#pragma unroll
+        for (int i = 0; i < MQ; ++i)
+#pragma unroll
+            for (int j = 0; j < MP; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    part[((i * MP + j) * 4 + r) * 64] = f32x4{c[i][j][4 * r], c[i][j][4 * r + 1], c[i][j][4 * r + 2], c[i][j][4 * r + 3]};
     }
 }
 
-// The sums of all splits, n = rows * width of them, in their order.
-template <class T>
-__global__ __launch_bounds__(256) void gated_join_kernel(const float *part, int splits, int64_t n, T *out) {
-    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < n; i += (int64_t)gridDim.x * 1024) {
-        float sum[4] = {};
-        if (i + 4 <= n) {
-            for (int s = 0; s < splits; ++s) {
-                struct __attribute__((packed, aligned(4))) Raw { float v[4]; };
-                const Raw r = *reinterpret_cast<const Raw *>(part + s * n + i);
+// Adds the slots of a shared tile (blockIdx.x) and finishes row blocks blockIdx.y of its waves.
+template <class T, int KIND, int WQ, int WP, int MQ, int MP>
+__global__ __launch_bounds__(WQ *WP * 64) void gated_join_kernel(GatedArgs a) {
+    using Pr = Product<T, KIND, WQ, WP, MQ, MP>;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[Pr::NW * Pr::St::BYTES];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = blockIdx.y, t = blockIdx.x;
+    const f32x4 *part = a.part + (int64_t)t * a.cut.of * Pr::SLOT + (w * MQ + i) * (MP * 4 * 64) + lane;
+    f32x16 c[MP];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sum[e] += r.v[e];
-            }
-            struct __attribute__((packed, aligned(sizeof(T)))) Out { T v[4]; } o;
+    for (int j = 0; j < MP; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o.v[e] = (T)sum[e];
-            *reinterpret_cast<Out *>(out + i) = o;
-        } else {
-            for (int64_t j = i; j < n; ++j) {
-                float total = 0.f;
-                for (int s = 0; s < splits; ++s) total += part[s * n + j];
-                out[j] = (T)total;
+        for (int r = 0; r < 16; ++r) c[j][r] = 0.f;
+    for (int s = 0; s < a.cut.of; ++s, part += Pr::SLOT)
+#pragma unroll
+        for (int j = 0; j < MP; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const f32x4 v = part[(j * 4 + r) * 64];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[j][4 * r + e] += v[e];
             }
-        }
-    }
-}
-// The same for the forward pass, with what its product does at its end.
-template <class T>
-__global__ __launch_bounds__(256) void gated_join_forward_kernel(GatedArgs a) {
-    const int64_t n = (int64_t)a.nq * a.np;
-    const T *bias = (const T *)a.bias;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t q = i / a.np;
-        const int p = (int)(i - q * a.np);
-        float g = 0.f, u = 0.f;
-        const float *from = a.part + q * 2 * a.np + p;
-        for (int s = 0; s < a.splits; ++s) {
-            g += from[s * 2 * n];
-            u += from[s * 2 * n + a.np];
-        }
-        if (bias) { g += (float)bias[p]; u += (float)bias[p + a.np]; }
-        if (a.kept) {
-            T *kept = (T *)a.kept + q * 2 * a.np + p;
-            kept[0] = (T)g;
-            kept[a.np] = (T)u;
-        }
-        ((T *)a.out)[i] = (T)(activation(g, a.act).x * u);
-    }
+    Pr::finish(a, Pr::at(a, t + a.cut.whole), i, w, lane, c, lds + w * Pr::St::BYTES);
 }
 
 // Rows of at most 32 MQ tokens: the weights' bytes count. A workgroup takes 16 columns of h, as a block of 16 rows of Wg
@@ -446,28 +475,53 @@ int check(int64_t N, int C, int F, int dtype) {
     return DDM_OK;
 }
 
-// How a product is cut up: tiles of bq x bp outputs, splits of k.
-struct Cut { int bq, bp, splits; };
+// How a product is cut up: tiles of `size` x `size` outputs, and how they are shared out.
+struct Cut { int size, tiles_q, tiles_p; Shares s; };
+
+// The cut that takes the least time by a measured model, in microseconds. The card has room for 256 tiles of 256 at a time or
+// 512 of 128 (two to a CU); a step of k takes `step` of such a round, its start and end `round` (FORWARD's activations and
+// three outputs more). Tiles that are left when all places have had as many can be cut along k, every one alike, so that
+// workgroups that run together share what they read, if writing and reading their sums at 4 TB/s and the join cost less
+// than leaving places idle.
 Cut cut_of(int kind, int64_t nq, int64_t np, int64_t k, int dtype) {
-    // np, nq: the whole output's (FORWARD: 2 F)
-    auto tiles = [&](int bq, int bp) { return ((nq + bq - 1) / bq) * ((np + bp - 1) / bp); };
-    Cut c = tiles(256, 256) >= 192 && dtype != DDM_F32 ? Cut{256, 256, 1} : Cut{128, 128, 1};
-    const int64_t n = std::max<int64_t>(tiles(c.bq, c.bp), 1), steps = k * esize(dtype) / 128 + 1;     // no rows: nothing is launched
-    const int64_t places = c.bq == 256 ? 256 : 512;
-    c.splits = (int)std::max<int64_t>(1, std::min<int64_t>(places / n, steps / 8));
-    return c;
+    const int bk = STEP_BYTES / esize(dtype);
+    const int64_t all = (k + bk - 1) / bk * (kind == BY_X ? 2 : 1);
+    Cut best{};
+    double least = 0;
+    for (int size : {128, 256}) {
+        if (size == 256 && dtype == DDM_F32) continue;     // a round of as many tiles of 128 has work for all matrix cores
+        const int64_t places = size == 256 || dtype == DDM_F32 ? 256 : 512;
+        const double step = dtype == DDM_F32 ? 0.85 : size == 256 ? 0.8 : 0.56, round = kind == FORWARD ? 12 : 6;
+        const int64_t tq = (nq + size - 1) / size * (kind == BY_W ? 2 : 1);
+        const int64_t tp = kind == FORWARD ? (np + size / 2 - 1) / (size / 2) : (np + size - 1) / size, n = tq * tp;
+        for (int of = 1; of <= 16 && of * 4 <= std::max<int64_t>(all, 4); ++of) {
+            const int64_t whole = of == 1 ? n : n / places * places, tail = n - whole, each = (all + of - 1) / of;
+            if (of > 1 && tail == 0) break;
+            double t = (double)((whole + places - 1) / places) * (all * step + round);
+            if (of > 1) t += (double)((tail * of + places - 1) / places) * (each * step + round) + 10 + (double)tail * of * size * size * 8 / 4e6;
+            if (best.size == 0 || t < least) {
+                least = t;
+                best = Cut{size, (int)tq, (int)tp, Shares{(int)whole, (int)tail, of, (int)each}};
+            }
+        }
+    }
+    return best;
 }
-Cut cut_forward(int64_t N, int C, int F, int dtype) { return cut_of(FORWARD, N, 2 * (int64_t)F, C, dtype); }
-Cut cut_by_x(int64_t N, int C, int F, int dtype) { return cut_of(BY_X, N, C, 2 * (int64_t)F, dtype); }
-Cut cut_by_w(int64_t N, int C, int F, int dtype) { return cut_of(BY_W, 2 * (int64_t)F, C, N, dtype); }
+Cut cut_forward(int64_t N, int C, int F, int dtype) { return cut_of(FORWARD, N, F, C, dtype); }
+Cut cut_by_x(int64_t N, int C, int F, int dtype) { return cut_of(BY_X, N, C, F, dtype); }
+Cut cut_by_w(int64_t N, int C, int F, int dtype) { return cut_of(BY_W, F, C, N, dtype); }
 
 constexpr int TOKENS = 64;                     // rows of gated_tokens_kernel
 
 size_t repacked(int64_t rows, int C, int dtype) { return whole((size_t)rows * padded(C, dtype) * esize(dtype)); }
-size_t parts_bytes(const Cut &c, int64_t rows, int64_t width) { return c.splits > 1 ? whole((size_t)c.splits * rows * width * 4) : 0; }
+size_t parts_bytes(const Cut &c) { return (size_t)c.s.tail * c.s.of * c.size * c.size * 4; }
 
-constexpr int SLOPE_ROWS = 128;
-int64_t slope_groups(int64_t N) { return (N + SLOPE_ROWS - 1) / SLOPE_ROWS; }
+// Rows of a workgroup of gated_slope_kernel: some 1024 workgroups, of 16 rows at least.
+int slope_rows(int64_t N, int F) {
+    const int64_t across = (F + 511) / 512;
+    return (int)std::min<int64_t>(std::max<int64_t>((N * across / 1024 + 15) / 16 * 16, 16), 128);
+}
+int64_t slope_groups(int64_t N, int F) { return (N + slope_rows(N, F) - 1) / slope_rows(N, F); }
 
 // Workspaces, in order. Both operands' repacked rows have room whether or not they are needed: that depends on addresses.
 struct ForwardPlan { Cut cut; size_t x, w, part, bytes; };
@@ -476,7 +530,7 @@ ForwardPlan forward_plan(int64_t N, int C, int F, int dtype) {
     if (N > TOKENS) p.cut = cut_forward(N, C, F, dtype);
     p.w = repacked(N, C, dtype);
     p.part = p.w + (C % (16 / esize(dtype)) ? repacked(2 * (int64_t)F, C, dtype) : 0);
-    p.bytes = p.part + (N > TOKENS ? parts_bytes(p.cut, N, 2 * (int64_t)F) : 0);
+    p.bytes = p.part + (N > TOKENS ? parts_bytes(p.cut) : 0);
     return p;
 }
 
@@ -489,18 +543,29 @@ void with_type(int dtype, F f) {
 
 template <class T, int KIND>
 void launch_product(GatedArgs a, const Cut &c, hipStream_t s) {
-    const int pairs = KIND == FORWARD ? c.bp / 2 : c.bp;
-    a.tiles_q = (a.nq + c.bq - 1) / c.bq * (KIND == BY_W ? 2 : 1);
-    a.tiles_p = (a.np + pairs - 1) / pairs;
-    a.splits = c.splits;
-    const dim3 grid((unsigned)((int64_t)a.tiles_q * a.tiles_p * a.splits));
+    a.tiles_q = c.tiles_q; a.tiles_p = c.tiles_p; a.cut = c.s;
+    const unsigned grid = (unsigned)(c.s.whole + c.s.tail * c.s.of);
+    auto go = [&](auto wq, auto wp, auto mq, auto mp, auto places, auto wgs) {
+        constexpr int WQ = decltype(wq)::value, WP = decltype(wp)::value, MQ = decltype(mq)::value, MP = decltype(mp)::value;
+        hipLaunchKernelGGL((gated_product_kernel<T, KIND, WQ, WP, MQ, MP, decltype(places)::value, decltype(wgs)::value>), dim3(grid),
+                           dim3(WQ * WP * 64), 0, s, a);
+        if (c.s.tail)
+            hipLaunchKernelGGL((gated_join_kernel<T, KIND, WQ, WP, MQ, MP>), dim3(c.s.tail, MQ), dim3(WQ * WP * 64), 0, s, a);
+    };
+    using std::integral_constant;
     if constexpr (sizeof(T) == 2) {
-        if (c.bq == 256) {
-            hipLaunchKernelGGL((gated_product_kernel<T, KIND, 2, 4, 4, 2>), grid, dim3(512), 0, s, a);
+        if (c.size == 256) {
+            if constexpr (KIND == FORWARD)
+                go(integral_constant<int, 4>{}, integral_constant<int, 2>{}, integral_constant<int, 2>{}, integral_constant<int, 4>{},
+                   integral_constant<int, 5>{}, integral_constant<int, 1>{});
+            else
+                go(integral_constant<int, 2>{}, integral_constant<int, 4>{}, integral_constant<int, 4>{}, integral_constant<int, 2>{},
+                   integral_constant<int, 4>{}, integral_constant<int, 1>{});
             return;
         }
     }
-    hipLaunchKernelGGL((gated_product_kernel<T, KIND, 2, 2, 2, 2>), grid, dim3(256), 0, s, a);
+    go(integral_constant<int, 2>{}, integral_constant<int, 2>{}, integral_constant<int, 2>{}, integral_constant<int, 2>{},
+       integral_constant<int, 5>{}, integral_constant<int, 2>{});
 }
 
 unsigned blocks(int64_t items, int64_t each) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>((items + each - 1) / each, 8192)); }
@@ -546,15 +611,10 @@ int ddm_gated_linear_forward(const void *x, int64_t ldx, const void *weight, con
         a.q = whole_rows<T>(x, a.ldq, N, C, ws, stream);
         a.p = whole_rows<T>(weight, a.ldp, 2 * (int64_t)F, C, ws + pl.w, stream);
         a.np = F; a.nq = (int)N; a.k = C; a.bias = bias; a.out = h; a.kept = kept; a.act = activation;
-        a.part = (float *)(ws + pl.part); a.splits = 1;
+        a.part = (f32x4 *)(ws + pl.part);
         if (N <= 32) hipLaunchKernelGGL((gated_tokens_kernel<T, 1, 8>), dim3((F + 15) / 16), dim3(512), 0, stream, a);
         else if (N <= TOKENS) hipLaunchKernelGGL((gated_tokens_kernel<T, 2, 8>), dim3((F + 15) / 16), dim3(512), 0, stream, a);
-        else {
-            launch_product<T, FORWARD>(a, pl.cut, stream);
-            a.splits = pl.cut.splits;
-            if (a.splits > 1)
-                hipLaunchKernelGGL((gated_join_forward_kernel<T>), dim3(blocks(N * F, 256)), dim3(256), 0, stream, a);
-        }
+        else launch_product<T, FORWARD>(a, pl.cut, stream);
     });
     return hipGetLastError() == hipSuccess ? DDM_OK : DDM_ERR_HIP;
 }
@@ -571,8 +631,8 @@ BackPlan back_plan(int64_t N, int C, int F, int dtype) {
     p.w = repacked(N, C, dtype);
     p.dp = p.w + (C % (16 / esize(dtype)) ? repacked(2 * (int64_t)F, C, dtype) : 0);
     p.bias = p.dp + whole((size_t)N * 2 * padded(F, dtype) * esize(dtype));
-    p.part = p.bias + whole((size_t)slope_groups(N) * 2 * F * 4);
-    p.bytes = p.part + std::max(parts_bytes(p.by_x, N, C), parts_bytes(p.by_w, 2 * (int64_t)F, C));
+    p.part = p.bias + whole((size_t)slope_groups(N, F) * 2 * F * 4);
+    p.bytes = p.part + std::max(parts_bytes(p.by_x), parts_bytes(p.by_w));
     return p;
 }
 
@@ -606,30 +666,24 @@ int ddm_gated_linear_backward(const void *dh, const void *x, int64_t ldx, const 
         }
         SlopeArgs sl{};
         sl.dh = dh; sl.kept = kept; sl.dp = ws + pl.dp; sl.part = dbias ? (float *)(ws + pl.bias) : nullptr;
-        sl.N = N; sl.F = F; sl.pitch = padded(F, dtype); sl.act = activation; sl.rows = SLOPE_ROWS;
-        hipLaunchKernelGGL((gated_slope_kernel<T>), dim3((unsigned)((sl.pitch + 511) / 512 * slope_groups(N))), dim3(256), 0, stream, sl);
+        sl.N = N; sl.F = F; sl.pitch = padded(F, dtype); sl.act = activation; sl.rows = slope_rows(N, F);
+        hipLaunchKernelGGL((gated_slope_kernel<T>), dim3((unsigned)((sl.pitch + 511) / 512 * slope_groups(N, F))), dim3(256), 0, stream, sl);
         if (dbias)
-            hipLaunchKernelGGL((gated_bias_kernel<T>), dim3((2 * F + 31) / 32), dim3(1024), 0, stream, sl.part, (int)slope_groups(N), 2 * F, (T *)dbias);
+            hipLaunchKernelGGL((gated_bias_kernel<T>), dim3((2 * F + 31) / 32), dim3(1024), 0, stream, sl.part, (int)slope_groups(N, F), 2 * F, (T *)dbias);
         GatedArgs a{};
-        a.part = (float *)(ws + pl.part);
+        a.part = (f32x4 *)(ws + pl.part);
         a.ldo = C; a.np = C; a.ldq = 2 * (int64_t)sl.pitch; a.q = sl.dp; a.seg_q = sl.pitch;
-        auto join = [&](int64_t n, void *out) {
-            if (a.splits > 1)
-                hipLaunchKernelGGL((gated_join_kernel<T>), dim3(blocks(n, 1024)), dim3(256), 0, stream, a.part, a.splits, n, (T *)out);
-        };
         if (dx) {
             a.ldp = C;
             a.p = whole_rows<T>(weight, a.ldp, 2 * (int64_t)F, C, ws + pl.w, stream);
-            a.seg_p = F * a.ldp; a.nq = (int)N; a.k = F; a.out = dx; a.splits = pl.by_x.splits;
+            a.seg_p = F * a.ldp; a.nq = (int)N; a.k = F; a.out = dx;
             launch_product<T, BY_X>(a, pl.by_x, stream);
-            join(N * C, dx);
         }
         if (dweight) {
             a.ldp = ldx;
             a.p = whole_rows<T>(x, a.ldp, N, C, ws, stream);
-            a.nq = F; a.k = (int)N; a.out = dweight; a.splits = pl.by_w.splits;
+            a.nq = F; a.k = (int)N; a.out = dweight;
             launch_product<T, BY_W>(a, pl.by_w, stream);
-            join(2 * (int64_t)F * C, dweight);
         }
     });
     return hipGetLastError() == hipSuccess ? DDM_OK : DDM_ERR_HIP;

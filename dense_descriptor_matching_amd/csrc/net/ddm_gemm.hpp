@@ -1,27 +1,31 @@
 // ddm_gemm.hpp -- products of matrices on the matrix cores, out[q][p] = sum_k Q(q, k) P(p, k), with what is to be done
 // with a tile of them left to the caller.
 //
-// A workgroup takes a tile of BQ x BP outputs and walks along k in steps of 128 bytes (64 or 32 elements): the next
-// step's rows of both operands go from memory straight to one half of LDS while the matrix cores work on the other. An
-// operand's rows may run along k (TRANS = false: a tile of BQ rows of 128 bytes) or along its own index (TRANS = true:
-// panels of 128 columns of as many rows as the step has k), read with transposing reads: no product needs a transposed
-// copy of its inputs in memory. P is the matrix instructions' first operand, so that a lane holds runs of four
+// A workgroup takes a tile of BQ x BP outputs and walks along k in steps of 64 bytes (32 or 16 elements): the rows of
+// steps to come go from memory straight to LDS while the matrix cores work on this one's. An operand's rows may run
+// along k (TRANS = false: tiles of BQ rows of 64 bytes) or along its own index (TRANS = true: panels of 128 columns of
+// as many rows as the step has k), read with transposing reads: no product needs a transposed copy of its inputs in
+// memory. P is the matrix instructions' first operand, so that a lane holds runs of four
 // neighbouring p of one q.
 #pragma once
 #include "ddm_tile.hpp"
 
 namespace ddm {
 
+constexpr int STEP_BYTES = 64;                  // of k in a step
+
 // One operand of a tile: R of its indices.
 template <class T, int R, bool TRANS, int NW>
 struct Side {
-    static constexpr int BK = 128 / (int)sizeof(T), PE = 16 / (int)sizeof(T);
+    static constexpr int BK = STEP_BYTES / (int)sizeof(T), PE = 16 / (int)sizeof(T);
     static constexpr int COLS = !TRANS ? BK : R < 128 ? R : 128;      // elements of a row in LDS
     static constexpr int ROWS = !TRANS ? R : BK;                      // rows of a panel
-    static constexpr int PANELS = !TRANS ? 1 : R / COLS, BYTES = R * 128;
+    static constexpr int PANELS = !TRANS ? 1 : R / COLS, BYTES = R * STEP_BYTES;
     using TL = Tile<T, COLS>;
     using In = Dma<T, COLS, NW, ROWS>;
-    static_assert(In::ALL % NW == 0 || In::ALL < NW, "a wave has whole loads, or none");
+    static constexpr int READS = TRANS && sizeof(T) == 2 ? 2 : 1;     // of LDS for an operand of a matrix instruction
+    static constexpr int LOADS = PANELS * In::N;                      // of a wave in a step
+    static_assert(In::ALL % NW == 0, "every wave has as many");
 
     const T *at;
     int64_t pitch;                              // elements from one step to the next
@@ -100,15 +104,31 @@ struct Side {
     }
 };
 
-// Workgroup b of n as a tile of nq x np: workgroups of one XCD (every eighth) get tiles that follow one another, and
-// tiles follow one another down bands of eight q, so that what an XCD works on at a time shares rows of both operands
-// in its L2.
+// All but this wave's N latest loads to LDS have landed, then everyone's.
+template <int N>
+__device__ __forceinline__ void loaded() {
+    static_assert(N < 64, "vmcnt has six bits");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | (N >> 4 << 14));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// Workgroups of one XCD (every eighth) get numbers that follow one another.
+__device__ __forceinline__ int by_xcd(int b, int n) {
+    const int x = b % 8;
+    return b / 8 + x * (n / 8) + min(x, n % 8);
+}
+// Tile i of nq x np: tiles follow one another down bands of eight q, so that what an XCD works on at a time shares rows
+// of both operands in its L2.
 struct TileAt { int q, p; };
-__device__ __forceinline__ TileAt tile_at(int b, int nq, int np) {
-    const int n = nq * np, each = n / 8, more = n % 8, x = b % 8;
-    const int i = b / 8 + x * each + min(x, more);
+__device__ __forceinline__ TileAt tile_at(int i, int nq, int np) {
     const int band = i / (8 * np), high = min(8, nq - band * 8), j = i - band * 8 * np;
     return {band * 8 + j % high, j / high};
 }
+
+// How a product's tiles are shared out: each of the first `whole` to a workgroup, and each of the other `tail` to `of` workgroups
+// that take `each` steps of k one after another; a join adds up what they found, in their order.
+struct Shares { int whole, tail, of, each; };
 
 }  // namespace ddm

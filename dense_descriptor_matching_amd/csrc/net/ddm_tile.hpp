@@ -72,10 +72,10 @@ struct Tile {
     static constexpr int ROW = D * (int)sizeof(T);   // bytes of a row
 
     __device__ static __forceinline__ int swizzle(int r) {
+        if constexpr (NP == 4) return (r >> 2) & 3;
         if constexpr (sizeof(T) == 4) return r & 7;    // NP = 8, 16, 32
         if constexpr (NP == 16) return ((r & 3) << 2) | ((r >> 2) & 3);
-        if constexpr (NP == 8) return ((r & 2) << 1) | ((r >> 2) & 3);
-        return (r >> 2) & 3;
+        return ((r & 2) << 1) | ((r >> 2) & 3);        // NP = 8
     }
     __device__ static __forceinline__ int place(int r, int p) { return r * ROW + ((p ^ swizzle(r)) << 4); }
 
