@@ -87,63 +87,139 @@ __device__ __forceinline__ float2 normed(float (&x)[V][VE], const ResArgs &p, in
 
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + __expf(-x)); }
 
-template <class W, int TEAM, int V, int VE>
-__device__ __forceinline__ void load_param(const void *from, float none, const ResArgs &p, int t, float (&to)[V][VE]) {
+// A chunk of a row as it lies in memory: what the next row needs waits in half the registers.
+template <class T>
+struct Chunk {
+    static constexpr int VE = 16 / sizeof(T);
+    T v[VE];
+    __device__ __forceinline__ void load(const T *row, int c, int C) {
+        if (c + VE <= C) {
+            const Bytes16<sizeof(T)> x = *reinterpret_cast<const Bytes16<sizeof(T)> *>(row + c);
+            __builtin_memcpy(v, &x, 16);
+        } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-#pragma unroll
-        for (int e = 0; e < VE; ++e) to[j][e] = none;
-        if (from) load_chunk<W, VE>((const W *)from, (j * TEAM + t) * VE, p.C, to[j]);
+            for (int e = 0; e < VE; ++e) v[e] = c + e < C ? row[c + e] : (T)0.f;
+        }
     }
-}
+    __device__ __forceinline__ void take(float (&to)[VE]) const {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) to[e] = (float)v[e];
+    }
+};
+
+// Parameters' columns, in LDS for the workgroup: registers are for sums and rows. Zeros behind the last: what rows have
+// there counts for nothing. So for a wave a row, and the next row is fetched ahead (24576 x 1024 bf16 forward 63 -> 47 us,
+// backward 189 -> 92). Four and eight waves' rows have 8 to 16 columns a thread and more parameters than LDS has room for in
+// as many workgroups: in registers, without fetching ahead (10007 x 1285 fp32 forward 44 us, with LDS 60 to 66).
+template <class T, class W, int TEAM, int V>
+struct Params {
+    static constexpr int VE = 16 / sizeof(T), WIDTH = TEAM * V * VE, THREADS = threads_of(TEAM);
+    static constexpr bool IN_LDS = TEAM == 64;
+    static constexpr size_t BYTES = IN_LDS ? WIDTH * sizeof(float) : 0;
+    float *lds;
+    int C, t;
+    float own[IN_LDS ? 1 : 5][V][VE];
+    __device__ __forceinline__ void put(int k, const void *from, float none) {
+        if constexpr (IN_LDS) {
+#pragma unroll
+            for (int i = 0; i < WIDTH / THREADS; ++i) {
+                const int c = i * THREADS + threadIdx.x;
+                lds[k * WIDTH + c] = c >= C ? 0.f : from ? (float)((const W *)from)[c] : none;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) own[k][j][e] = (j * TEAM + t) * VE + e < C ? none : 0.f;
+                if (from) load_chunk<W, VE>((const W *)from, (j * TEAM + t) * VE, C, own[k][j]);
+            }
+        }
+    }
+    __device__ __forceinline__ void get(int k, int j, float (&to)[VE]) const {
+#pragma unroll
+        for (int e = 0; e < VE; e += 4) {
+            if constexpr (IN_LDS) {
+                const float4 x = *reinterpret_cast<const float4 *>(lds + k * WIDTH + (j * TEAM + t) * VE + e);
+                to[e] = x.x; to[e + 1] = x.y; to[e + 2] = x.z; to[e + 3] = x.w;
+            } else {
+#pragma unroll
+                for (int i = e; i < e + 4; ++i) to[i] = own[k][j][i];
+            }
+        }
+    }
+};
 
 template <class T, class W, int TEAM, int V, bool BN>
 __global__ __launch_bounds__(threads_of(TEAM)) void residual_fwd_kernel(ResArgs p) {
-    constexpr int VE = 16 / sizeof(T), TEAMS = threads_of(TEAM) / TEAM;
+    constexpr int VE = 16 / sizeof(T), THREADS = threads_of(TEAM), TEAMS = THREADS / TEAM;
     __shared__ Scratch scratch;
+    extern __shared__ __attribute__((aligned(16))) float param[];      // w, b, scale, bw, bb
+    using Pr = Params<T, W, TEAM, V>;
     const int t = threadIdx.x % TEAM;
+    Pr pr{param, p.C, t};
     const int64_t first = (int64_t)blockIdx.x * TEAMS + threadIdx.x / TEAM, pitch = (int64_t)gridDim.x * TEAMS;
-    float w[V][VE], b[V][VE], scale[V][VE], bw[V][VE], bb[V][VE];
-    load_param<W, TEAM>(p.w, 1.f, p, t, w);
-    load_param<W, TEAM>(p.b, 0.f, p, t, b);
-    load_param<W, TEAM>(p.scale, 1.f, p, t, scale);
-    if constexpr (BN) {
-        load_param<W, TEAM>(p.bw, 1.f, p, t, bw);
-        load_param<W, TEAM>(p.bb, 0.f, p, t, bb);
-    }
-    int turn = 0;
-    for (int64_t n = first; n < p.N; n += pitch) {
-        float x[V][VE], g[V][VE], r[V][VE];
+    Chunk<T> x0[V], r0[V], g0[V] = {};                     // zeros of a gate that is not there
+    auto fetch = [&](int64_t n) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int c = (j * TEAM + t) * VE;
-            load_chunk<T, VE>((const T *)p.branch + n * p.ldb, c, p.C, r[j]);
-            load_chunk<T, VE>((const T *)p.x + n * p.ldx, c, p.C, x[j]);
-            if (p.gate) load_chunk<T, VE>((const T *)p.gate + n * p.ldg, c, p.C, g[j]);
+            r0[j].load((const T *)p.branch + n * p.ldb, c, p.C);
+            x0[j].load((const T *)p.x + n * p.ldx, c, p.C);
+            if (p.gate) g0[j].load((const T *)p.gate + n * p.ldg, c, p.C);
         }
+    };
+    if (Pr::IN_LDS && first < p.N) fetch(first);
+    pr.put(0, p.w, 1.f);
+    pr.put(1, p.b, 0.f);
+    pr.put(2, p.scale, 1.f);
+    if constexpr (BN) {
+        pr.put(3, p.bw, 1.f);
+        pr.put(4, p.bb, 0.f);
+    }
+    __syncthreads();
+    int turn = 0;
+    for (int64_t n = first; n < p.N; n += pitch) {
+        if constexpr (Pr::IN_LDS) asm volatile("" ::: "memory");       // parameters are read again, not kept in registers
+        else fetch(n);
+        float x[V][VE], g[V][VE], r[V][VE];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            r0[j].take(r[j]);
+            x0[j].take(x[j]);
+            g0[j].take(g[j]);
+        }
+        if (Pr::IN_LDS && n + pitch < p.N) fetch(n + pitch);
         if constexpr (BN) {
             const float2 m = normed<TEAM>(r, p, t, scratch, turn);
 #pragma unroll
-            for (int j = 0; j < V; ++j)
+            for (int j = 0; j < V; ++j) {
+                float bw[VE], bb[VE];
+                pr.get(3, j, bw);
+                pr.get(4, j, bb);
 #pragma unroll
-                for (int e = 0; e < VE; ++e) r[j][e] = __builtin_fmaf(r[j][e] * m.y, bw[j][e], bb[j][e]);
+                for (int e = 0; e < VE; ++e) r[j][e] = __builtin_fmaf(r[j][e] * m.y, bw[e], bb[e]);
+            }
             if (t == 0) { p.stats[2 * p.N + n] = m.x; p.stats[3 * p.N + n] = m.y; }
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
+            float scale[VE];
+            pr.get(2, j, scale);
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
                 if (p.gate) r[j][e] *= sigmoid(g[j][e]);
-                r[j][e] = __builtin_fmaf(r[j][e], scale[j][e], x[j][e]);
-                if ((j * TEAM + t) * VE + e >= p.C) r[j][e] = 0.f;      // bb past column C
+                r[j][e] = __builtin_fmaf(r[j][e], scale[e], x[j][e]);
             }
             store_chunk<T, VE>((T *)p.s + n * p.C, (j * TEAM + t) * VE, p.C, r[j]);
         }
         const float2 m = normed<TEAM>(r, p, t, scratch, turn);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
+            float w[VE], b[VE];
+            pr.get(0, j, w);
+            pr.get(1, j, b);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) r[j][e] = __builtin_fmaf(r[j][e] * m.y, w[j][e], b[j][e]);
+            for (int e = 0; e < VE; ++e) r[j][e] = __builtin_fmaf(r[j][e] * m.y, w[e], b[e]);
             store_chunk<T, VE>((T *)p.y + n * p.C, (j * TEAM + t) * VE, p.C, r[j]);
         }
         if (t == 0) { p.stats[n] = m.x; p.stats[p.N + n] = m.y; }
@@ -152,19 +228,38 @@ __global__ __launch_bounds__(threads_of(TEAM)) void residual_fwd_kernel(ResArgs 
 
 template <class T, class W, int TEAM, int V, bool BN, bool PARAMS>
 __global__ __launch_bounds__(threads_of(TEAM)) void residual_bwd_kernel(ResArgs p) {
-    constexpr int VE = 16 / sizeof(T), TEAMS = threads_of(TEAM) / TEAM, NP = BN ? 5 : 3;
+    constexpr int VE = 16 / sizeof(T), THREADS = threads_of(TEAM), TEAMS = THREADS / TEAM, NP = BN ? 5 : 3;
     __shared__ Scratch scratch;
-    extern __shared__ float share[];                       // TEAM == 64: [4][C]
+    extern __shared__ __attribute__((aligned(16))) float param[];      // w, scale, bw, bb; at the end a sum's columns of four teams
+    using Pr = Params<T, W, TEAM, V>;
     const int t = threadIdx.x % TEAM;
+    Pr pr{param, p.C, t};
     const int64_t first = (int64_t)blockIdx.x * TEAMS + threadIdx.x / TEAM, pitch = (int64_t)gridDim.x * TEAMS;
     const float inv_c = 1.f / (float)p.C;
-    float w[V][VE], scale[V][VE], bw[V][VE], bb[V][VE], sum[NP][V][VE];
-    load_param<W, TEAM>(p.w, 1.f, p, t, w);
-    load_param<W, TEAM>(p.scale, 1.f, p, t, scale);
+    Chunk<T> x0[V], r0[V], o0[V] = {}, u0[V] = {}, d0[V] = {};         // zeros of what is not there
+    float mean0 = 0.f, rstd0 = 0.f, bmean0 = 0.f, brstd0 = 0.f;
+    auto fetch = [&](int64_t n) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = (j * TEAM + t) * VE;
+            r0[j].load((const T *)p.branch + n * p.ldb, c, p.C);
+            x0[j].load((const T *)p.x + n * p.ldx, c, p.C);
+            if (p.gate) o0[j].load((const T *)p.gate + n * p.ldg, c, p.C);
+            if (p.dy) u0[j].load((const T *)p.dy + n * p.C, c, p.C);
+            if (p.ds) d0[j].load((const T *)p.ds + n * p.C, c, p.C);
+        }
+        mean0 = p.stats[n];
+        rstd0 = p.stats[p.N + n];
+        if constexpr (BN) { bmean0 = p.stats[2 * p.N + n]; brstd0 = p.stats[3 * p.N + n]; }
+    };
+    if (Pr::IN_LDS && first < p.N) fetch(first);
+    pr.put(0, p.w, 1.f);
+    pr.put(1, p.scale, 1.f);
     if constexpr (BN) {
-        load_param<W, TEAM>(p.bw, 1.f, p, t, bw);
-        load_param<W, TEAM>(p.bb, 0.f, p, t, bb);
+        pr.put(2, p.bw, 1.f);
+        pr.put(3, p.bb, 0.f);
     }
+    float sum[NP][V][VE];
     if constexpr (PARAMS)
 #pragma unroll
         for (int k = 0; k < NP; ++k)
@@ -172,58 +267,66 @@ __global__ __launch_bounds__(threads_of(TEAM)) void residual_bwd_kernel(ResArgs 
             for (int j = 0; j < V; ++j)
 #pragma unroll
                 for (int e = 0; e < VE; ++e) sum[k][j][e] = 0.f;
+    __syncthreads();
     int turn = 0;
     for (int64_t n = first; n < p.N; n += pitch) {
-        const float mean = p.stats[n], rstd = p.stats[p.N + n];
-        float x[V][VE], r[V][VE], o[V][VE], u[V][VE], d[V][VE];
+        if constexpr (Pr::IN_LDS) asm volatile("" ::: "memory");       // parameters are read again, not kept in registers
+        else fetch(n);
+        const float mean = mean0, rstd = rstd0, bmean = bmean0, brstd = brstd0;
+        float x[V][VE], r[V][VE], o[V][VE], u[V][VE], d[V][VE], m[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            r0[j].take(r[j]);
+            x0[j].take(x[j]);
+            o0[j].take(o[j]);
+            u0[j].take(u[j]);
+            d0[j].take(d[j]);
+        }
+        if (Pr::IN_LDS && n + pitch < p.N) fetch(n + pitch);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int c = (j * TEAM + t) * VE;
-            load_chunk<T, VE>((const T *)p.branch + n * p.ldb, c, p.C, r[j]);
-            load_chunk<T, VE>((const T *)p.x + n * p.ldx, c, p.C, x[j]);
+            float w[VE], scale[VE], bw[VE], bb[VE];
+            pr.get(0, j, w);
+            pr.get(1, j, scale);
+            if constexpr (BN) { pr.get(2, j, bw); pr.get(3, j, bb); }
 #pragma unroll
-            for (int e = 0; e < VE; ++e) { o[j][e] = 0.f; u[j][e] = 0.f; d[j][e] = 0.f; }
-            if (p.gate) load_chunk<T, VE>((const T *)p.gate + n * p.ldg, c, p.C, o[j]);
-            if (p.dy) load_chunk<T, VE>((const T *)p.dy + n * p.C, c, p.C, u[j]);
-            if (p.ds) load_chunk<T, VE>((const T *)p.ds + n * p.C, c, p.C, d[j]);
-        }
-        float bmean = 0.f, brstd = 0.f, m[2] = {0.f, 0.f};
-        if constexpr (BN) { bmean = p.stats[2 * p.N + n]; brstd = p.stats[3 * p.N + n]; }
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {                 // past column C: dy = ds = 0, so nothing is added
+            for (int e = 0; e < VE; ++e) {
                 if constexpr (BN) r[j][e] = (r[j][e] - bmean) * brstd;
                 float part = r[j][e];
-                if constexpr (BN) part = __builtin_fmaf(part, bw[j][e], bb[j][e]);
+                if constexpr (BN) part = __builtin_fmaf(part, bw[e], bb[e]);
                 if (p.gate) { o[j][e] = sigmoid(o[j][e]); part *= o[j][e]; }
-                x[j][e] = (__builtin_fmaf(part, scale[j][e], x[j][e]) - mean) * rstd;
+                x[j][e] = (__builtin_fmaf(part, scale[e], x[j][e]) - mean) * rstd;
                 if constexpr (PARAMS) {
                     sum[0][j][e] = __builtin_fmaf(u[j][e], x[j][e], sum[0][j][e]);
                     sum[1][j][e] += u[j][e];
                 }
-                u[j][e] *= w[j][e];
+                u[j][e] *= w[e];
                 m[0] += u[j][e];
                 m[1] = __builtin_fmaf(u[j][e], x[j][e], m[1]);
             }
+        }
         team_sums<TEAM>(m, scratch, turn);
         const float s1 = p.rms ? 0.f : m[0] * inv_c, s2 = m[1] * inv_c;
         m[0] = m[1] = 0.f;
+        if constexpr (Pr::IN_LDS) asm volatile("" ::: "memory");
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int c = (j * TEAM + t) * VE;
+            float scale[VE], bw[VE], bb[VE];
+            pr.get(1, j, scale);
+            if constexpr (BN) { pr.get(2, j, bw); pr.get(3, j, bb); }
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
                 d[j][e] = __builtin_fmaf(rstd, u[j][e] - __builtin_fmaf(x[j][e], s2, s1), d[j][e]);
-                if (c + e >= p.C) d[j][e] = 0.f;
             }
             if (p.dx) store_chunk<T, VE>((T *)p.dx + n * p.C, c, p.C, d[j]);
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
                 float full = r[j][e];                      // t
-                if constexpr (BN) full = __builtin_fmaf(full, bw[j][e], bb[j][e]);
+                if constexpr (BN) full = __builtin_fmaf(full, bw[e], bb[e]);
                 if constexpr (PARAMS) sum[2][j][e] = __builtin_fmaf(d[j][e], p.gate ? full * o[j][e] : full, sum[2][j][e]);
-                d[j][e] *= scale[j][e];
+                d[j][e] *= scale[e];
                 x[j][e] = d[j][e] * full * o[j][e] * (1.f - o[j][e]);
                 if (p.gate) d[j][e] *= o[j][e];
                 if constexpr (BN) {
@@ -231,7 +334,7 @@ __global__ __launch_bounds__(threads_of(TEAM)) void residual_bwd_kernel(ResArgs 
                         sum[3][j][e] = __builtin_fmaf(d[j][e], r[j][e], sum[3][j][e]);
                         sum[4][j][e] += d[j][e];
                     }
-                    d[j][e] *= bw[j][e];
+                    d[j][e] *= bw[e];
                     m[0] += d[j][e];
                     m[1] = __builtin_fmaf(d[j][e], r[j][e], m[1]);
                 }
@@ -260,13 +363,13 @@ __global__ __launch_bounds__(threads_of(TEAM)) void residual_bwd_kernel(ResArgs 
 #pragma unroll
                 for (int j = 0; j < V; ++j) store_chunk<float, VE>(part + k * p.C, (j * TEAM + t) * VE, p.C, sum[k][j]);
             } else {
-                float *mine = share + (threadIdx.x / TEAM) * p.C;
+                float *mine = param + (threadIdx.x / TEAM) * p.C;
                 __syncthreads();
 #pragma unroll
                 for (int j = 0; j < V; ++j) store_chunk<float, VE>(mine, (j * TEAM + t) * VE, p.C, sum[k][j]);
                 __syncthreads();
                 for (int c = threadIdx.x; c < p.C; c += 256)
-                    part[k * p.C + c] = (share[c] + share[p.C + c]) + (share[2 * p.C + c] + share[3 * p.C + c]);
+                    part[k * p.C + c] = (param[c] + param[p.C + c]) + (param[2 * p.C + c] + param[3 * p.C + c]);
             }
         }
     }
@@ -335,6 +438,11 @@ void with_shape(Shape s, F f) {
     else go(std::integral_constant<int, 512>{});
 }
 
+template <void (*KERNEL)(ResArgs), int TEAM>
+void launch_rows(unsigned grid, size_t lds, hipStream_t stream, const ResArgs &a) {
+    hipLaunchKernelGGL(KERNEL, dim3(grid), dim3(threads_of(TEAM)), lds, stream, a);
+}
+
 bool off(const void *p, int e) { return !p || (uintptr_t)p % e; }
 bool odd(const void *p, int e) { return (uintptr_t)p % e; }
 
@@ -360,14 +468,15 @@ int ddm_residual_norm_forward(const void *x, int64_t ldx, const void *branch, in
     a.s = s; a.y = y; a.stats = stats; a.ldx = ldx; a.ldb = ldb; a.ldg = ldg; a.N = N; a.C = C; a.eps = (float)eps; a.rms = rms;
     const Shape shape = shape_of(C, dtype);
     const int teams = threads_of(shape.team) / shape.team;
-    const unsigned grid = (unsigned)std::min<int64_t>((N + teams - 1) / teams, 2048);
+    const unsigned grid = (unsigned)std::min<int64_t>((N + teams - 1) / teams, shape.team == 64 ? 1024 : 2048);
     with_types(dtype, wtype, [&](auto t, auto w) {
         using T = decltype(t);
         using W = decltype(w);
         with_shape<T>(shape, [&](auto team, auto v) {
             constexpr int TEAM = decltype(team)::value, V = decltype(v)::value;
-            if (branch_norm) hipLaunchKernelGGL((residual_fwd_kernel<T, W, TEAM, V, true>), dim3(grid), dim3(threads_of(TEAM)), 0, stream, a);
-            else hipLaunchKernelGGL((residual_fwd_kernel<T, W, TEAM, V, false>), dim3(grid), dim3(threads_of(TEAM)), 0, stream, a);
+            constexpr size_t lds = Params<T, W, TEAM, V>::BYTES;
+            if (branch_norm) launch_rows<residual_fwd_kernel<T, W, TEAM, V, true>, TEAM>(grid, 5 * lds, stream, a);
+            else launch_rows<residual_fwd_kernel<T, W, TEAM, V, false>, TEAM>(grid, 3 * lds, stream, a);
         });
     });
     return hipGetLastError() == hipSuccess ? DDM_OK : DDM_ERR_HIP;
@@ -417,8 +526,8 @@ int ddm_residual_norm_backward(const void *dy, const void *ds, const void *x, in
             constexpr int TEAM = decltype(team)::value, V = decltype(v)::value;
             auto go = [&](auto bn, auto with_params) {
                 constexpr bool BN = decltype(bn)::value, PARAMS = decltype(with_params)::value;
-                hipLaunchKernelGGL((residual_bwd_kernel<T, W, TEAM, V, BN, PARAMS>), dim3(groups), dim3(threads_of(TEAM)),
-                                   PARAMS && TEAM == 64 ? 4 * C * sizeof(float) : 0, stream, a);
+                constexpr size_t lds = Params<T, W, TEAM, V>::BYTES;
+                launch_rows<residual_bwd_kernel<T, W, TEAM, V, BN, PARAMS>, TEAM>(groups, (BN || (PARAMS && TEAM == 64) ? 4 : 2) * lds, stream, a);
             };
             if (branch_norm) params ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
             else params ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
