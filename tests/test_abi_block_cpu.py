@@ -31,7 +31,7 @@ def _rotary(L, **kw):
     (dict(D=1025), -4), (dict(D=63), -1), (dict(axes=0), -1), (dict(pairs=0), -1), (dict(pairs=17), -1), (dict(axes=3), -1),
     (dict(axes=1 << 30, pairs=1 << 30), -1), (dict(dtype=3), -4), (dict(interleaved=2), -1), (dict(inverse=-1), -1),
     (dict(m=float("nan")), -1), (dict(m=1e39), -1), (dict(Hq=-1), -1), (dict(Hk=65537), -1), (dict(qt=-1), -1), (dict(koh=-64), -1),
-    (dict(kt=1 << 41), -1)])
+    (dict(kt=1 << 41), -1), (dict(qot=0), -1), (dict(koh=0), -1)])
 def test_rotary_rejects(L, change, status):
     assert _rotary(L, **change) == status
 
@@ -137,3 +137,7 @@ def test_gated_linear_rejects_one_way(L):
     assert f(0, 64, 48, 1) > 0 and b(0, 64, 48, 1) > 0
     assert b(1000, 64, 48, 1) >= 1000 * 2 * 48 * 2                  # the projections' gradients
     assert f(1000, 61, 48, 1) >= (1000 + 96) * 64 * 2               # both operands repacked
+    for N in (10, 1000, 10 ** 5, 10 ** 7):                          # of sums of tiles cut along k at most 128 MB
+        for C, F in ((64, 64), (1024, 2736), (8192, 1000)):
+            own = (N * C + 2 * N * F + 2 * F * C) * 2 + (N // 16 + 1) * 2 * F * 4
+            assert b(N, C, F, 1) <= own + (1 << 27) + 4096 and f(N, C, F, 1) <= own + (1 << 27) + 4096

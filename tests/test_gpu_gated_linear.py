@@ -103,7 +103,7 @@ def check(ddm, args, kind, dtype):
 
 SIZES = [(1, 1, 1), (1, 64, 16), (2, 1024, 272), (3, 7, 5), (5, 130, 33), (31, 64, 100), (32, 96, 64), (33, 200, 65), (64, 513, 47),
          (65, 64, 64), (100, 1000, 24), (127, 40, 129), (128, 128, 128), (129, 264, 136), (300, 771, 130), (513, 64, 257), (1000, 8, 8),
-         (70, 4104, 40), (2049, 72, 520)]
+         (70, 4104, 40), (2049, 72, 520), (9000, 64, 24)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
