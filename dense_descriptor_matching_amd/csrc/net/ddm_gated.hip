@@ -323,11 +323,11 @@ __global__ __launch_bounds__(WQ *WP * 64) void gated_join_kernel(GatedArgs a) {
     Pr::finish(a, Pr::at(a, t + a.cut.whole), i, w, lane, c, lds + w * Pr::St::BYTES);
 }
 
-// Rows of at most 32 MQ tokens: the weights' bytes count (2 x 1024 to 2736 bf16 5.5 us for 11 MB; 37 x 2048 to 5461 fp16 22 us for 45
-// MB: a wave's loads of 32 bytes from each of 32 rows take the address units as long as whole lines would for twice as many, and
-// x's are as many as the weight's; fetching a piece of k ahead made no difference). A workgroup takes 16 columns of h, as a block of 16 rows of Wg
-// and the same 16 of Wu; its waves share k, each reading its rows' pieces straight into the operands' registers. In the
-// block, rows 8..15 and 24..31 are those of Wu: a lane then holds g and u of the same columns.
+// Rows of at most 32 MQ tokens: the weight's bytes count (2 x 1024 to 2736 bf16 5.5 us for 11 MB; a wave's loads of 32
+// bytes from each of 32 rows take the address units as long as whole lines would for twice as many; fetching a piece of k
+// ahead made no difference). A workgroup takes 16 columns of h, as a block of 16 rows of Wg and the same 16 of Wu; its waves
+// share k, each reading its rows' pieces straight into the operands' registers. In the block, rows 8..15 and 24..31 are
+// those of Wu: a lane then holds g and u of the same columns.
 template <class T, int MQ, int NW>
 __global__ __launch_bounds__(NW * 64) void gated_tokens_kernel(GatedArgs a) {
     constexpr int PE = 16 / (int)sizeof(T), BK = 128 / (int)sizeof(T), PIECES = 8 / PE;
@@ -532,7 +532,10 @@ Cut cut_forward(int64_t N, int C, int F, int dtype) { return cut_of(FORWARD, N, 
 Cut cut_by_x(int64_t N, int C, int F, int dtype) { return cut_of(BY_X, N, C, F, dtype); }
 Cut cut_by_w(int64_t N, int C, int F, int dtype) { return cut_of(BY_W, F, C, N, dtype); }
 
-constexpr int TOKENS = 64;                     // rows of gated_tokens_kernel
+// Up to so many rows gated_tokens_kernel is sooner done than the tiles' product, which in 32 bits keeps the matrix cores busy
+// with rows that are not there (33 to 64 rows of 4096 to 8192: bf16 37 us by tiles, 42 to 55 without; 1024 to 2736: fp32 28 by tiles, 16
+// without).
+int tokens_rows(int dtype) { return dtype == DDM_F32 ? 64 : 32; }
 
 size_t repacked(int64_t rows, int C, int dtype) { return whole((size_t)rows * padded(C, dtype) * esize(dtype)); }
 size_t parts_bytes(const Cut &c) { return (size_t)c.s.tail * c.s.of * c.size * c.size * 4; }
@@ -549,10 +552,10 @@ int64_t slope_groups(int64_t N, int F) { return (N + slope_rows(N, F) - 1) / slo
 struct ForwardPlan { Cut cut; size_t x, w, part, bytes; };
 ForwardPlan forward_plan(int64_t N, int C, int F, int dtype) {
     ForwardPlan p{};
-    if (N > TOKENS) p.cut = cut_forward(N, C, F, dtype);
+    if (N > tokens_rows(dtype)) p.cut = cut_forward(N, C, F, dtype);
     p.w = repacked(N, C, dtype);
     p.part = p.w + (C % (16 / esize(dtype)) ? repacked(2 * (int64_t)F, C, dtype) : 0);
-    p.bytes = p.part + (N > TOKENS ? parts_bytes(p.cut) : 0);
+    p.bytes = p.part + (N > tokens_rows(dtype) ? parts_bytes(p.cut) : 0);
     return p;
 }
 
@@ -637,7 +640,9 @@ int ddm_gated_linear_forward(const void *x, int64_t ldx, const void *weight, con
         // 24576 x 1024 to 2736 bf16 with kept: 336 us past the L2s, which then keep x and the weight, 373 through them
         a.past_l2 = (kept ? 3 : 1) * N * F * e > 32 << 20;
         if (N <= 32) hipLaunchKernelGGL((gated_tokens_kernel<T, 1, 8>), dim3((F + 15) / 16), dim3(512), 0, stream, a);
-        else if (N <= TOKENS) hipLaunchKernelGGL((gated_tokens_kernel<T, 2, 8>), dim3((F + 15) / 16), dim3(512), 0, stream, a);
+        else if (N <= tokens_rows(dtype)) {
+            if constexpr (sizeof(T) == 4) hipLaunchKernelGGL((gated_tokens_kernel<T, 2, 8>), dim3((F + 15) / 16), dim3(512), 0, stream, a);
+        }
         else launch_product<T, FORWARD>(a, pl.cut, stream);
     });
     return hipGetLastError() == hipSuccess ? DDM_OK : DDM_ERR_HIP;
