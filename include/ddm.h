@@ -391,7 +391,7 @@ int ddm_matching_loss_backward(const float *dloss, const void *a, const void *b,
  * gradient of the call without it, for dq and dk in the place of q and k.
  *   q, q_out       [T][Hq][D], row (t, h) at q + (t * q_ts + h * q_hs) elements, D elements contiguous; k, k_out likewise with
  *                  Hk heads; any non-negative strides. Outputs may be the inputs themselves (with the same strides) but must
- *                  not overlap them otherwise. Hq or Hk may be 0 (its pointers are not read). Whole 16-byte pieces are fastest.
+ *                  not overlap them otherwise, nor themselves (an output's stride of 0 is refused). Hq or Hk may be 0 (its pointers are not read). Whole 16-byte pieces are fastest.
  *   positions      device int32[T][axes], any values
  *   frequencies    device double[axes][pairs]. Angles are taken in 64 bits; up to some 2^30 sine and cosine are within 2^-22.
  *   1 <= D <= DDM_MAX_ROTARY_D, 2 axes pairs <= D, Hq, Hk <= DDM_MAX_ROTARY_HEADS; magnitude finite. */
@@ -435,7 +435,8 @@ int ddm_residual_norm_backward(const void *dy, const void *ds, const void *x, in
  *   kept         [N][2F] in dtype: rows of g and u, what backward needs of forward; NULL when no gradient is wanted
  *   Each of dx, dweight, dbias may be NULL when it is not wanted.
  * Products take the inputs' type with fp32 accumulation; g, u (in kept) and dg, du are rounded to that type between the products
- * of a gradient. Rows that are not whole 16-byte pieces are repacked into the workspace first.
+ * of a gradient. Rows that are not whole 16-byte pieces are repacked into the workspace first, which has room for x's always, and at
+ * most 128 MB for the sums of tiles that are cut along k; backward's has dg and du besides.
  * 1 <= C, F <= DDM_MAX_GATED with F C element size (C padded to 16 bytes) below 1 GB, 0 <= N <= DDM_MAX_GATED_ROWS (N = 0: the
  * gradients of weight and bias are zeros). */
 enum { DDM_SILU = 0, DDM_GELU = 1, DDM_SIGMOID = 2 };
