@@ -566,8 +566,8 @@ def gated_linear_backward(dh, x, weight, kept, *, activation: str = "silu", need
 
 class _GatedLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, activation):
-        h, kept = gated_linear_forward(x, weight, bias, activation=activation, keep=any(ctx.needs_input_grad))
+    def forward(ctx, x, weight, bias, activation, keep):
+        h, kept = gated_linear_forward(x, weight, bias, activation=activation, keep=keep)
         ctx.save_for_backward(x, weight, kept)
         ctx.activation = activation
         return h
@@ -578,12 +578,15 @@ class _GatedLinear(torch.autograd.Function):
         x, weight, kept = ctx.saved_tensors
         need = ctx.needs_input_grad
         return gated_linear_backward(dh.contiguous(), x, weight, kept, activation=ctx.activation, need_dx=need[0], need_dweight=need[1],
-                                     need_dbias=need[2]) + (None,)
+                                     need_dbias=need[2]) + (None,) * 2
 
 
 def gated_linear(x, weight, bias=None, *, activation: str = "silu"):
-    """Differentiable :func:`gated_linear_forward`; returns h alone."""
-    return _GatedLinear.apply(x, weight, bias, activation)
+    """Differentiable :func:`gated_linear_forward`; returns h alone. What a gradient needs is kept only where one may be asked
+    for: not under ``torch.no_grad()``."""
+    # asked here: within apply the mode is off, and needs_input_grad follows requires_grad alone
+    keep = torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (x, weight, bias))
+    return _GatedLinear.apply(x, weight, bias, activation, keep)
 
 
 # ------------------------------------------------------------------------------------------------- matching loss
