@@ -340,9 +340,13 @@ def _rotary(q, k, positions, frequencies, interleaved, magnitude, inverse, out, 
                 raise ValueError("out must hold one tensor for each of q and k")
             if t is not None:
                 _tensor(t, name, q.dtype, dev, s.shape, contiguous=False)
+        if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, qo, ko)):
+            raise RuntimeError("out= has no gradient, but one of the tensors requires it: use rotary, or torch.no_grad()")
     qv, kv, qw, kw = (_rotary_heads(t, n) for t, n in ((q, names[0]), (k, names[1]), (qo, "out[0]"), (ko, "out[1]")))
     _call(dev, "ddm_rotary", *qv, *kv, positions.data_ptr(), frequencies.data_ptr(), T, D, axes, pairs, _DT[q.dtype],
           int(interleaved), int(inverse), float(magnitude), *qw[:3], *kw[:3])
+    if out is not None:                     # a backward pass that was to read what stood there raises
+        torch.autograd.graph.increment_version([t for t in out if t is not None])
     return qo, ko
 
 
@@ -353,7 +357,7 @@ def rotary_forward(q, k, positions, frequencies, *, interleaved: bool = False, m
     (:func:`rotary_frequencies`). The first 2 axes pairs elements of a head are turned, axis by axis, the rest stays: element i of an
     axis' 2 pairs goes with i + pairs, or, ``interleaved``, 2i with 2i + 1, by the angle position * frequency, times ``magnitude``.
     The tensors may be views (of a packed qkv projection, say) with contiguous heads. ``out`` holds tensors to write to, q and k
-    themselves among them."""
+    themselves among them; as with torch's own ``out=``, none of the tensors may require a gradient then, unless gradients are off."""
     return _rotary(q, k, positions, frequencies, interleaved, magnitude, False, out, ("q", "k"))
 
 
