@@ -390,7 +390,9 @@ class _Rotary(torch.autograd.Function):
 
 
 def rotary(q, k, positions, frequencies, *, interleaved: bool = False, magnitude: float = 1.0):
-    """Differentiable :func:`rotary_forward`; without k it returns q alone."""
+    """Differentiable (by q and k) :func:`rotary_forward`; without k it returns q alone."""
+    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (frequencies, magnitude)):
+        raise ValueError("frequencies and magnitude get no gradient: give them detached")
     return _Rotary.apply(q, k, positions, frequencies, interleaved, magnitude)
 
 
