@@ -118,7 +118,6 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotArgs p) {
 
 int esize(int dtype) { return dtype == DDM_F32 ? 4 : 2; }
 
-// The strides of heads that there are: an only token's or head's stride says nothing.
 bool bad_heads(const void *p, int64_t ts, int64_t hs, int e) {
     return !p || (uintptr_t)p % e || ts < 0 || hs < 0 || ts >= (1ll << 40) || hs >= (1ll << 40);
 }
@@ -151,6 +150,10 @@ int ddm_rotary(const void *q, int64_t q_ts, int64_t q_hs, int Hq, const void *k,
     if (axes < 1 || pairs < 1 || axes > D || pairs > D || 2 * axes * pairs > D) return DDM_ERR_INVALID;
     if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1) || !std::isfinite((float)magnitude)) return DDM_ERR_INVALID;
     if (T == 0 || Hq + Hk == 0) return DDM_OK;
+    // an only token's or head's stride says nothing
+    for (int64_t *ts : {&q_ts, &k_ts, &qo_ts, &ko_ts}) *ts = T > 1 ? *ts : 0;
+    for (int64_t *hs : {&q_hs, &qo_hs}) *hs = Hq > 1 ? *hs : 0;
+    for (int64_t *hs : {&k_hs, &ko_hs}) *hs = Hk > 1 ? *hs : 0;
     const int e = esize(dtype);
     if (!positions || (uintptr_t)positions % 4 || !frequencies || (uintptr_t)frequencies % 8) return DDM_ERR_INVALID;
     if (Hq && (bad_heads(q, q_ts, q_hs, e) || bad_heads(q_out, qo_ts, qo_hs, e))) return DDM_ERR_INVALID;
