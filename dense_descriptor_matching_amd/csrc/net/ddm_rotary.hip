@@ -122,6 +122,22 @@ bool bad_heads(const void *p, int64_t ts, int64_t hs, int e) {
     return !p || (uintptr_t)p % e || ts < 0 || hs < 0 || ts >= (1ll << 40) || hs >= (1ll << 40);
 }
 
+// Whether rows of n elements at t ts + h hs, t < T, h < H, share some.
+bool rows_meet(int64_t ts, int64_t hs, int T, int H, int n) {
+    if ((T > 1 && ts < n) || (H > 1 && hs < n)) return true;
+    if (T <= 1 || H <= 1) return false;
+    if (ts >= hs * (H - 1) + n || hs >= ts * (T - 1) + n) return false;        // one within the other, as in dense tensors
+    for (int64_t h = 1; h < H; ++h) {
+        const int64_t t = h * hs / ts;                                         // the tokens whose rows are nearest to head h of the first
+        if ((t < T && h * hs - t * ts < n) || (t + 1 < T && (t + 1) * ts - h * hs < n)) return true;
+    }
+    return false;
+}
+bool near(const void *a, const void *b, int bytes) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return (x < y ? y - x : x - y) < (uintptr_t)bytes;
+}
+
 template <class T, int VE>
 void launch(const RotArgs &a, unsigned grid, size_t lds, bool interleaved, hipStream_t s) {
     if (interleaved) hipLaunchKernelGGL((rotary_kernel<T, VE, true>), dim3(grid), dim3(256), lds, s, a);
@@ -158,8 +174,11 @@ int ddm_rotary(const void *q, int64_t q_ts, int64_t q_hs, int Hq, const void *k,
     if (!positions || (uintptr_t)positions % 4 || !frequencies || (uintptr_t)frequencies % 8) return DDM_ERR_INVALID;
     if (Hq && (bad_heads(q, q_ts, q_hs, e) || bad_heads(q_out, qo_ts, qo_hs, e))) return DDM_ERR_INVALID;
     if (Hk && (bad_heads(k, k_ts, k_hs, e) || bad_heads(k_out, ko_ts, ko_hs, e))) return DDM_ERR_INVALID;
-    // outputs that lie over one another
-    if ((Hq && ((T > 1 && !qo_ts) || (Hq > 1 && !qo_hs))) || (Hk && ((T > 1 && !ko_ts) || (Hk > 1 && !ko_hs)))) return DDM_ERR_INVALID;
+    // outputs that lie over one another, or over inputs that other threads still read
+    const int row = D * e;
+    if (Hq && (rows_meet(qo_ts, qo_hs, T, Hq, D) || (near(q_out, q, row) && !(q_out == q && qo_ts == q_ts && qo_hs == q_hs)))) return DDM_ERR_INVALID;
+    if (Hk && (rows_meet(ko_ts, ko_hs, T, Hk, D) || (near(k_out, k, row) && !(k_out == k && ko_ts == k_ts && ko_hs == k_hs)))) return DDM_ERR_INVALID;
+    if (Hq && Hk && (near(q_out, k_out, row) || near(q_out, k, row) || near(k_out, q, row))) return DDM_ERR_INVALID;
     RotArgs a{};
     a.q = {(const char *)q, (char *)q_out, q_ts * e, q_hs * e, qo_ts * e, qo_hs * e};
     a.k = {(const char *)k, (char *)k_out, k_ts * e, k_hs * e, ko_ts * e, ko_hs * e};

@@ -357,7 +357,7 @@ def rotary_forward(q, k, positions, frequencies, *, interleaved: bool = False, m
     (:func:`rotary_frequencies`). The first 2 axes pairs elements of a head are turned, axis by axis, the rest stays: element i of an
     axis' 2 pairs goes with i + pairs, or, ``interleaved``, 2i with 2i + 1, by the angle position * frequency, times ``magnitude``.
     The tensors may be views (of a packed qkv projection, say) with contiguous heads. ``out`` holds tensors to write to, q and k
-    themselves among them; as with torch's own ``out=``, none of the tensors may require a gradient then, unless gradients are off."""
+    themselves (each in its own place) or others that overlap neither them nor one another; as with torch's own ``out=``, none of the tensors may require a gradient then, unless gradients are off."""
     return _rotary(q, k, positions, frequencies, interleaved, magnitude, False, out, ("q", "k"))
 
 

@@ -390,8 +390,10 @@ int ddm_matching_loss_backward(const float *dloss, const void *a, const void *b,
  * x, pair i is (x[i], x[i + pairs]), or (x[2i], x[2i + 1]) with interleaved = 1. inverse = 1 negates the angle: that is the
  * gradient of the call without it, for dq and dk in the place of q and k.
  *   q, q_out       [T][Hq][D], row (t, h) at q + (t * q_ts + h * q_hs) elements, D elements contiguous; k, k_out likewise with
- *                  Hk heads; any non-negative strides (those of an only token or head are not looked at). Outputs may be the inputs themselves (with the same strides) but must
- *                  not overlap them otherwise, nor themselves (an output's stride of 0 is refused). Hq or Hk may be 0 (its pointers are not read). Whole 16-byte pieces are fastest.
+ *                  Hk heads; any non-negative strides (those of an only token or head are not looked at). Outputs may be the
+ *                  inputs themselves, q_out = q and k_out = k with the same strides, and must not overlap anything else: rows of
+ *                  an output that share elements are refused, and so are first rows that share elements with another tensor's.
+ *                  Hq or Hk may be 0 (its pointers are not read). Whole 16-byte pieces are fastest.
  *   positions      device int32[T][axes], any values
  *   frequencies    device double[axes][pairs]. Angles are taken in 64 bits; up to some 2^30 sine and cosine are within 2^-22.
  *   1 <= D <= DDM_MAX_ROTARY_D, 2 axes pairs <= D, Hq, Hk <= DDM_MAX_ROTARY_HEADS; magnitude finite. */
