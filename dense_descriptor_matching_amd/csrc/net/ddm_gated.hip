@@ -607,7 +607,7 @@ const T *whole_rows(const void *from, int64_t &ld, int64_t rows, int C, void *co
 }
 
 bool bad_act(int act) { return act != DDM_SILU && act != DDM_GELU && act != DDM_SIGMOID; }
-bool bad_stride(int64_t ld, int C, int e) { return ld < C || ld * e > 1 << 22; }
+bool bad_stride(int64_t ld, int C, int e) { return ld < C || ld > (1 << 22) / e; }
 bool off(const void *p, int e) { return !p || (uintptr_t)p % e; }
 
 }  // namespace
