@@ -609,6 +609,8 @@ const T *whole_rows(const void *from, int64_t &ld, int64_t rows, int C, void *co
 bool bad_act(int act) { return act != DDM_SILU && act != DDM_GELU && act != DDM_SIGMOID; }
 bool bad_stride(int64_t ld, int C, int e) { return ld < C || ld > (1 << 22) / e; }
 bool off(const void *p, int e) { return !p || (uintptr_t)p % e; }
+// The weight's rows are read in place, in pieces of 16 bytes, or repacked, where they are not made of whole ones.
+bool off_weight(const void *w, int C, int e) { return off(w, C * (int64_t)e % 16 ? e : 16); }
 
 }  // namespace
 
@@ -625,7 +627,7 @@ int ddm_gated_linear_forward(const void *x, int64_t ldx, const void *weight, con
     const int e = esize(dtype);
     if (bad_act(activation) || bad_stride(ldx, C, e)) return DDM_ERR_INVALID;
     if (N == 0) return DDM_OK;
-    if (off(x, e) || off(weight, 16) || off(h, e) || (uintptr_t)bias % e || (uintptr_t)kept % e) return DDM_ERR_INVALID;
+    if (off(x, e) || off_weight(weight, C, e) || off(h, e) || (uintptr_t)bias % e || (uintptr_t)kept % e) return DDM_ERR_INVALID;
     const ForwardPlan pl = forward_plan(N, C, F, dtype);
     if (off(workspace, 16) || workspace_bytes < pl.bytes) return DDM_ERR_WORKSPACE;
     char *ws = (char *)workspace;
@@ -680,7 +682,7 @@ int ddm_gated_linear_backward(const void *dh, const void *x, int64_t ldx, const 
     if (int rc = check(N, C, F, dtype)) return rc;
     const int e = esize(dtype);
     if (bad_act(activation) || bad_stride(ldx, C, e)) return DDM_ERR_INVALID;
-    if (N && (off(dh, e) || off(kept, e) || (dweight && off(x, e)) || (dx && off(weight, 16)))) return DDM_ERR_INVALID;
+    if (N && (off(dh, e) || off(kept, e) || (dweight && off(x, e)) || (dx && off_weight(weight, C, e)))) return DDM_ERR_INVALID;
     if ((uintptr_t)dx % e || (uintptr_t)dweight % e || (uintptr_t)dbias % e) return DDM_ERR_INVALID;
     const BackPlan pl = back_plan(N, C, F, dtype);
     if (off(workspace, 16) || workspace_bytes < pl.bytes) return DDM_ERR_WORKSPACE;

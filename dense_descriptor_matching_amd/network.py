@@ -534,10 +534,17 @@ def _gated_sizes(x, weight, activation):
     return x.numel() // x.shape[-1], x.shape[-1], weight.shape[0] // 2, _DT[x.dtype]
 
 
+def _gated_weight(weight):
+    if weight.data_ptr() % 16 and weight.shape[1] * weight.element_size() % 16 == 0:
+        raise _api.DDMError(-1, "weight off a 16-byte boundary, with rows of whole 16-byte pieces: clone it")
+    return weight.data_ptr()
+
+
 def gated_linear_forward(x, weight, bias=None, *, activation: str = "silu", keep: bool = False):
     """Gated linear layer h = act(x Wg^T + bg) * (x Wu^T + bu) of x [..., C]: weight [2F, C] holds the F rows of Wg and then those of Wu,
     bias [2F] likewise. Returns (h [..., F], kept): kept [..., 2F] is what :func:`gated_linear_backward` needs with ``keep``, else
-    None. ``activation``: "silu" g * sigmoid(g), "gelu" g * Phi(g), "sigmoid"."""
+    None. ``activation``: "silu" g * sigmoid(g), "gelu" g * Phi(g), "sigmoid". x is contiguous or two-dimensional with contiguous rows;
+    a weight whose rows are whole 16-byte pieces begins on such a boundary."""
     sizes = _gated_sizes(x, weight, activation)
     F = sizes[2]
     if bias is not None:
@@ -547,7 +554,7 @@ def gated_linear_forward(x, weight, bias=None, *, activation: str = "silu", keep
     h = x.new_empty(x.shape[:-1] + (F,))
     kept = x.new_empty(x.shape[:-1] + (2 * F,)) if keep else None
     ws = x.new_empty(nbytes, dtype=torch.uint8)
-    _call(x.device, "ddm_gated_linear_forward", *view, weight.data_ptr(), _at(bias), *sizes, ACTIVATIONS[activation], h.data_ptr(),
+    _call(x.device, "ddm_gated_linear_forward", *view, _gated_weight(weight), _at(bias), *sizes, ACTIVATIONS[activation], h.data_ptr(),
           _at(kept), ws.data_ptr(), nbytes)
     return h, kept
 
@@ -565,7 +572,7 @@ def gated_linear_backward(dh, x, weight, kept, *, activation: str = "silu", need
     dw = torch.empty_like(weight) if need_dweight else None
     db = x.new_empty(2 * F) if need_dbias else None
     ws = x.new_empty(nbytes, dtype=torch.uint8)
-    _call(x.device, "ddm_gated_linear_backward", dh.data_ptr(), *view, weight.data_ptr(), kept.data_ptr(), *sizes,
+    _call(x.device, "ddm_gated_linear_backward", dh.data_ptr(), *view, _gated_weight(weight) if need_dx else weight.data_ptr(), kept.data_ptr(), *sizes,
           ACTIVATIONS[activation], _at(dx), _at(dw), _at(db), ws.data_ptr(), nbytes)
     return dx, dw, db
 

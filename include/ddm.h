@@ -432,8 +432,8 @@ int ddm_residual_norm_backward(const void *dy, const void *ds, const void *x, in
  *   g = x Wg^T + bg,  u = x Wu^T + bu,  h = act(g) u        act: DDM_SILU g sigmoid(g), DDM_GELU g Phi(g), DDM_SIGMOID sigmoid(g)
  *   dg = dh u act'(g),  du = dh act(g),  dx = dg Wg + du Wu,  dWg = dg^T x,  dWu = du^T x,  dbg, dbu = their sums over rows
  *   x            [N][C] with row stride ldx >= C elements, at most 4 MB; weight [2F][C]: the F rows of Wg, then those of Wu, 16-byte
- *                aligned; bias [2F] or NULL; all in dtype, as h, dh [N][F], dx [N][C], dweight [2F][C] and dbias [2F], contiguous,
- *                at any whole element
+ *                aligned if its rows are whole 16-byte pieces; bias [2F] or NULL; all in dtype, as h, dh [N][F], dx [N][C],
+ *                dweight [2F][C] and dbias [2F], contiguous, at any whole element
  *   kept         [N][2F] in dtype: rows of g and u, what backward needs of forward; NULL when no gradient is wanted
  *   Each of dx, dweight, dbias may be NULL when it is not wanted.
  * Products take the inputs' type with fp32 accumulation; g, u (in kept) and dg, du are rounded to that type between the products
