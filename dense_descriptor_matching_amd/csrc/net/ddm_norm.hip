@@ -113,7 +113,7 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormArgs p) {
         float x[V][VE], g[V][VE], s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            load_chunk<T, VE>(row, (j * TEAM + t) * VE, p.C, x[j]);
+            load_chunk<T, VE, true>(row, (j * TEAM + t) * VE, p.C, x[j]);     // zeros' norms may be infinite
             load_chunk<T, VE>(grow, (j * TEAM + t) * VE, p.C, g[j]);
         }
 #pragma unroll

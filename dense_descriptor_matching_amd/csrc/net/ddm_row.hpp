@@ -22,9 +22,10 @@ __device__ __forceinline__ float wave_sum(float x) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// VE elements from any aligned address of elements, zeros from column C on.
-template <class T, int VE>
+// VE elements from any aligned address of elements, from column C on zeros or (AGAIN) the last columns again.
+template <class T, int VE, bool AGAIN = false>
 __device__ __forceinline__ void load_chunk(const T *row, int c, int C, float (&out)[VE]) {
+    if (AGAIN && c >= C) c = max(C - VE, 0);
     if (c + VE <= C) {
         struct __attribute__((packed, aligned(sizeof(T)))) Raw { T v[VE]; };
         const Raw r = *reinterpret_cast<const Raw *>(row + c);
@@ -32,7 +33,7 @@ __device__ __forceinline__ void load_chunk(const T *row, int c, int C, float (&o
         for (int e = 0; e < VE; ++e) out[e] = (float)r.v[e];
     } else {
 #pragma unroll
-        for (int e = 0; e < VE; ++e) out[e] = c + e < C ? (float)row[c + e] : 0.f;
+        for (int e = 0; e < VE; ++e) out[e] = c + e < C ? (float)row[c + e] : AGAIN && e ? out[e ? e - 1 : 0] : 0.f;
     }
 }
 // 16 bytes at an address of so many, of whatever type.
