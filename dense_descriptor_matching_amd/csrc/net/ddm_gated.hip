@@ -67,6 +67,13 @@ __device__ __forceinline__ float2 activation(float g, int kind) {
     return {g * t, __builtin_fmaf(g * t, 1.f - t, t)};
 }
 
+// past_l2: through the L2 without staying there, for outputs larger than it that would push out what is read again.
+template <int ALIGN>
+__device__ __forceinline__ void store16(void *to, Bytes16Of16 v, bool past_l2) {
+    if (past_l2) __builtin_nontemporal_store((Bytes16<ALIGN>)v, reinterpret_cast<Bytes16<ALIGN> *>(to));
+    else *reinterpret_cast<Bytes16<ALIGN> *>(to) = v;
+}
+
 // A wave's block of 32 rows q of W columns p, four neighbouring p at a time in a lane, to rows in memory: through LDS of
 // its own, so that a row's columns are written together.
 template <class T, int W>

@@ -41,26 +41,17 @@ typedef uint32_t Bytes16Of2 __attribute__((ext_vector_type(4), aligned(2), may_a
 typedef uint32_t Bytes16Of4 __attribute__((ext_vector_type(4), aligned(4), may_alias));
 typedef uint32_t Bytes16Of16 __attribute__((ext_vector_type(4), aligned(16), may_alias));
 template <int ALIGN> using Bytes16 = std::conditional_t<ALIGN == 2, Bytes16Of2, std::conditional_t<ALIGN == 4, Bytes16Of4, Bytes16Of16>>;
-// past_l2: through the L2 without staying there, for outputs larger than it that would push out what is read again.
-template <int ALIGN>
-__device__ __forceinline__ void store16(void *to, Bytes16Of16 v, bool past_l2) {
-    if (past_l2) __builtin_nontemporal_store((Bytes16<ALIGN>)v, reinterpret_cast<Bytes16<ALIGN> *>(to));
-    else *reinterpret_cast<Bytes16<ALIGN> *>(to) = v;
-}
+// VE elements to any aligned address of elements, those before column C.
 template <class T, int VE>
-__device__ __forceinline__ void store_chunk(T *row, int c, int C, const float (&in)[VE], bool past_l2 = false) {
+__device__ __forceinline__ void store_chunk(T *row, int c, int C, const float (&in)[VE]) {
+    static_assert(VE * sizeof(T) % 16 == 0, "whole 16-byte pieces");
     if (c + VE <= C) {
         struct __attribute__((aligned(16))) Raw { T v[VE]; } r;
 #pragma unroll
         for (int e = 0; e < VE; ++e) r.v[e] = (T)in[e];
-        if constexpr (VE * sizeof(T) % 16 == 0) {
 #pragma unroll
-            for (int i = 0; i < VE * (int)sizeof(T) / 16; ++i)
-                store16<sizeof(T)>((char *)(row + c) + 16 * i, reinterpret_cast<const Bytes16Of16 *>(&r)[i], past_l2);
-        } else {
-            struct __attribute__((packed, aligned(sizeof(T)))) Out { T v[VE]; };
-            *reinterpret_cast<Out *>(row + c) = *reinterpret_cast<const Out *>(&r);
-        }
+        for (int i = 0; i < VE * (int)sizeof(T) / 16; ++i)
+            *reinterpret_cast<Bytes16<sizeof(T)> *>((char *)(row + c) + 16 * i) = reinterpret_cast<const Bytes16Of16 *>(&r)[i];
     } else {
 #pragma unroll
         for (int e = 0; e < VE; ++e)
