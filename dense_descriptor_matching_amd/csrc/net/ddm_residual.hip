@@ -4,7 +4,7 @@
 //   norm(z) = (z - mean) rstd,  rstd = (var + eps)^-1/2;  rms: mean = 0
 //   backward, with zh = norm(s), th = norm(branch), o = sigmoid(gate):
 //   u = dy w,  dx = ds + rstd (u - mean(u) - zh mean(u zh));  dw = sum over rows of dy zh,  db = sum of dy
-//   dscale = sum of dx o t,  v = dx scale,  dgate = v t o (1 - o),  v' = v o
+//   dscale = sum of dx o t,  v = dx scale,  dgate = v t o',  v' = v o
 //   dwb = sum of v' th,  dbb = sum of v',  r = v' wb,  dbranch = rstd_b (r - mean(r) - th mean(r th))   (or v')
 //   rms: without the means of u and r.
 //
@@ -87,7 +87,13 @@ __device__ __forceinline__ float2 normed(float (&x)[V][VE], const ResArgs &p, in
     return {mean, 1.f / sqrtf(sum[0] / (float)p.C + p.eps)};
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + __expf(-x)); }
+// sigmoid(g) and its derivative, with e = exp(-|g|): 1 / (1 + e) or e / (1 + e), and e / (1 + e)^2. As o (1 - o) the derivative of a
+// gate that is far open would lose the digits that 1 - o has (half of them at g = 10, all at 17).
+struct Gate { float open, slope; };
+__device__ __forceinline__ Gate gate_of(float g) {
+    const float e = __expf(-fabsf(g)), r = __builtin_amdgcn_rcpf(1.f + e), shut = e * r;
+    return {g >= 0.f ? r : shut, shut * r};
+}
 
 // A chunk of a row as it lies in memory: what the next row needs waits in half the registers.
 template <class T>
@@ -214,7 +220,7 @@ __global__ __launch_bounds__(threads_of(TEAM)) void residual_fwd_kernel(ResArgs 
             pr.get(2, j, scale);
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                if (p.gate) r[j][e] *= sigmoid(g[j][e]);
+                if (p.gate) r[j][e] *= gate_of(g[j][e]).open;
                 r[j][e] = __builtin_fmaf(r[j][e], scale[e], x[j][e]);
             }
             store_chunk<T, VE>((T *)p.s + n * p.C, (j * TEAM + t) * VE, p.C, r[j]);
@@ -233,8 +239,10 @@ __global__ __launch_bounds__(threads_of(TEAM)) void residual_fwd_kernel(ResArgs 
     }
 }
 
+// Two waves to a SIMD where that takes a few registers less than the compiler would like (24576 x 768 fp16, no norm of the branch: 46 us,
+// 60 with one); others would spill, or have two anyway.
 template <class T, class W, int TEAM, int V, bool BN, bool PARAMS>
-__global__ __launch_bounds__(threads_of(TEAM)) void residual_bwd_kernel(ResArgs p) {
+__global__ __launch_bounds__(threads_of(TEAM), TEAM == 64 && sizeof(T) == 2 && !BN ? 2 : 1) void residual_bwd_kernel(ResArgs p) {
     constexpr int VE = 16 / sizeof(T), THREADS = threads_of(TEAM), TEAMS = THREADS / TEAM, NP = BN ? 5 : 3;
     __shared__ Scratch scratch;
     extern __shared__ __attribute__((aligned(16))) float param[];      // w, scale, bw, bb; at the end a sum's columns of four teams
@@ -280,7 +288,7 @@ __global__ __launch_bounds__(threads_of(TEAM)) void residual_bwd_kernel(ResArgs 
         if constexpr (Pr::IN_LDS) asm volatile("" ::: "memory");       // parameters are read again, not kept in registers
         else fetch(n);
         const float mean = mean0, rstd = rstd0, bmean = bmean0, brstd = brstd0;
-        float x[V][VE], r[V][VE], o[V][VE], u[V][VE], d[V][VE], m[2] = {0.f, 0.f};
+        float x[V][VE], r[V][VE], o[V][VE], slope[V][VE], u[V][VE], d[V][VE], m[2] = {0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             r0[j].take(r[j]);
@@ -302,7 +310,11 @@ __global__ __launch_bounds__(threads_of(TEAM)) void residual_bwd_kernel(ResArgs 
                 if constexpr (BN) r[j][e] = (r[j][e] - bmean) * brstd;
                 float part = r[j][e];
                 if constexpr (BN) part = __builtin_fmaf(part, bw[e], bb[e]);
-                if (p.gate) { o[j][e] = sigmoid(o[j][e]); part *= o[j][e]; }
+                if (p.gate) {
+                    const Gate g = gate_of(o[j][e]);
+                    part *= o[j][e] = g.open;
+                    slope[j][e] = g.slope;
+                }
                 x[j][e] = (__builtin_fmaf(part, scale[e], x[j][e]) - mean) * rstd;
                 if constexpr (PARAMS) {
                     sum[0][j][e] = __builtin_fmaf(u[j][e], x[j][e], sum[0][j][e]);
@@ -334,7 +346,7 @@ __global__ __launch_bounds__(threads_of(TEAM)) void residual_bwd_kernel(ResArgs 
                 if constexpr (BN) full = __builtin_fmaf(full, bw[e], bb[e]);
                 if constexpr (PARAMS) sum[2][j][e] = __builtin_fmaf(d[j][e], p.gate ? full * o[j][e] : full, sum[2][j][e]);
                 d[j][e] *= scale[e];
-                x[j][e] = d[j][e] * full * o[j][e] * (1.f - o[j][e]);
+                x[j][e] = d[j][e] * full * slope[j][e];
                 if (p.gate) d[j][e] *= o[j][e];
                 if constexpr (BN) {
                     if constexpr (PARAMS) {
