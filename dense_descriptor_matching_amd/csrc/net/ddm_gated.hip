@@ -63,7 +63,8 @@ __device__ __forceinline__ float2 activation(float g, int kind) {
         return {g * phi, __builtin_fmaf(g * 0.39894228040143268f, e, phi)};
     }
     const float t = __builtin_amdgcn_rcpf(1.f + exp2_fast(g * -1.4426950408889634f));
-    if (kind == DDM_SIGMOID) return {t, t * (1.f - t)};
+    // sigmoid(-g) by itself: 1 - t has lost its digits where t is near one. (The products' ends take the value alone.)
+    if (kind == DDM_SIGMOID) return {t, t * __builtin_amdgcn_rcpf(1.f + exp2_fast(g * 1.4426950408889634f))};
     return {g * t, __builtin_fmaf(g * t, 1.f - t, t)};
 }
 
