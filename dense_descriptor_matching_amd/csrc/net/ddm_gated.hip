@@ -38,6 +38,7 @@ struct GatedArgs {
     const void *bias;
     void *out, *kept;
     f32x4 *part;                               // slots of a tile's sums
+    const float *unit;                         // float16, BY_X and BY_W: what one of dg and du as held stands for
     int act;
     bool past_l2;                              // FORWARD: outputs are more than the L2s hold (32 MB)
 };
@@ -188,6 +189,11 @@ struct Product {
                 __builtin_amdgcn_sched_barrier(0);
             }
         } else {
+            if constexpr (std::is_same_v<T, _Float16>) {
+                const float unit = *a.unit;
+#pragma unroll
+                for (int j = 0; j < MP; ++j) c[j] *= unit;
+            }
 #pragma unroll
             for (int j = 0; j < MP; ++j) St::put(mine, lane, j, c[j]);
         }
@@ -420,35 +426,88 @@ struct SlopeArgs {
     float *part;                               // [rows' workgroup][2][F], or NULL
     int64_t N;
     int F, pitch, act, rows;                   // rows of a workgroup
+    float *most, *unit;                        // float16: the largest |dg|, |du| of each workgroup, and the unit; or NULL
 };
 
+// dg and du of VE columns from c on.
+template <class T, int VE>
+__device__ __forceinline__ void slopes(const SlopeArgs &a, int64_t n, int c, float (&dg)[VE], float (&du)[VE]) {
+    float d[VE];
+    load_chunk<T, VE>((const T *)a.dh + n * a.F, c, a.F, d);
+    load_chunk<T, VE>((const T *)a.kept + n * 2 * a.F, c, a.F, dg);
+    load_chunk<T, VE>((const T *)a.kept + n * 2 * a.F + a.F, c, a.F, du);
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+        const float2 s = activation<T>(dg[e], a.act);
+        dg[e] = d[e] * du[e] * s.y;            // past column F all three are zeros
+        du[e] = d[e] * s.x;
+    }
+}
+
+// The largest of a workgroup's 256 values.
+__device__ __forceinline__ float workgroup_max(float x, float (&scratch)[4]) {
+#pragma unroll
+    for (int i = 1; i < 64; i *= 2) x = fmaxf(x, __shfl_xor(x, i));
+    scratch[threadIdx.x >> 6] = x;
+    __syncthreads();
+    return fmaxf(fmaxf(scratch[0], scratch[1]), fmaxf(scratch[2], scratch[3]));
+}
+
+// float16 has five bits for exponents: gradients of a mean over many rows lie below its numbers, scaled ones beyond them. Where the
+// largest finite dg or du is not between 1 and 65504, all are held in units of a power of two in which it is between 2^14 and 2^15, so
+// that those down to 2^-28 of it keep their digits; the products' sums are multiplied by the unit. (Between them those down to
+// 2^-14 keep theirs.) Finding it first would read everything twice (24576 x 2736: 119 to 148 us); so the first pass has no unit
+// and notes its largest, and a second one does nothing (6 us) or takes them again in a unit.
+__device__ __forceinline__ int unit_exponent(const SlopeArgs &a, float (&scratch)[4]) {
+    float most = 0.f;
+    for (int i = threadIdx.x; i < (int)gridDim.x; i += 256) most = fmaxf(most, a.most[i]);
+    most = workgroup_max(most, scratch);
+    return most == 0.f || (most >= 1.f && most <= 65504.f) ? 0 : max(ilogbf(most) - 14, -100);
+}
+
 // dg and du from dh and the projections; the columns' sums over a workgroup's rows. A thread has eight columns, a wave
-// 512, and the workgroup's four waves every fourth row.
-template <class T>
+// 512, and the workgroup's four waves every fourth row. AGAIN: float16's second pass.
+template <class T, bool AGAIN = false>
 __global__ __launch_bounds__(256) void gated_slope_kernel(SlopeArgs a) {
     constexpr int VE = 8;
-    __shared__ float sums[4][2][64 * VE];
+    constexpr bool HALF = std::is_same_v<T, _Float16>;
+    __shared__ float sums[4][2][64 * VE], scratch[4];
     const int across = (a.pitch + 64 * VE - 1) / (64 * VE), group = blockIdx.x / across, block = blockIdx.x % across;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, c = (block * 64 + lane) * VE;
     const int64_t first = (int64_t)group * a.rows, last = min(first + a.rows, a.N);
-    float sg[VE] = {}, su[VE] = {};
+    float sg[VE] = {}, su[VE] = {}, most = 0.f, to_unit = 1.f;
+    if constexpr (AGAIN) {
+        const int exponent = unit_exponent(a, scratch);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *a.unit = ldexpf(1.f, exponent);
+        if (exponent == 0) return;
+        to_unit = ldexpf(1.f, -exponent);
+    }
     if (c < a.pitch)
         for (int64_t n = first + w; n < last; n += 4) {
-            float d[VE], g[VE], u[VE];
-            load_chunk<T, VE>((const T *)a.dh + n * a.F, c, a.F, d);
-            load_chunk<T, VE>((const T *)a.kept + n * 2 * a.F, c, a.F, g);
-            load_chunk<T, VE>((const T *)a.kept + n * 2 * a.F + a.F, c, a.F, u);
+            float g[VE], u[VE];
+            slopes<T, VE>(a, n, c, g, u);
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                const float2 s = activation<T>(g[e], a.act);
-                g[e] = d[e] * u[e] * s.y;      // past column F all three are zeros
-                u[e] = d[e] * s.x;
-                sg[e] += g[e];
-                su[e] += u[e];
+                if constexpr (AGAIN) {
+                    g[e] *= to_unit;
+                    u[e] *= to_unit;
+                } else {
+                    sg[e] += g[e];
+                    su[e] += u[e];
+                    if constexpr (HALF) {      // infinities and NaN are what they are in any unit
+                        most = fmaxf(most, fabsf(g[e]) < INFINITY ? fabsf(g[e]) : 0.f);
+                        most = fmaxf(most, fabsf(u[e]) < INFINITY ? fabsf(u[e]) : 0.f);
+                    }
+                }
             }
             store_chunk<T, VE>((T *)a.dp + n * 2 * a.pitch, c, a.pitch, g);
             store_chunk<T, VE>((T *)a.dp + n * 2 * a.pitch + a.pitch, c, a.pitch, u);
         }
+    if constexpr (AGAIN) return;
+    if (HALF && a.most) {
+        most = workgroup_max(most, scratch);
+        if (threadIdx.x == 0) a.most[blockIdx.x] = most;
+    }
     if (!a.part) return;
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
@@ -560,12 +619,13 @@ size_t repacked(int64_t rows, int C, int dtype) { return whole((size_t)rows * pa
 size_t parts_bytes(const Cut &c) { return (size_t)c.s.tail * c.s.of * c.size * c.size * 4; }
 
 // Rows of a workgroup of gated_slope_kernel: some 1024 workgroups, of 16 rows at least and 64 at most (24576 x 2736 bf16:
-// 144 us with 64, 149 with 128, 189 with 256).
+// 144 us with 64, 149 with 128, 189 with 256), and 4096 workgroups at most.
 int slope_rows(int64_t N, int F) {
-    const int64_t across = (F + 511) / 512;
-    return (int)std::min<int64_t>(std::max<int64_t>((N * across / 1024 + 15) / 16 * 16, 16), 64);
+    const int64_t across = (F + 511) / 512, least = (N * across / 4096 + 15) / 16 * 16;
+    return (int)std::max(std::min<int64_t>(std::max<int64_t>((N * across / 1024 + 15) / 16 * 16, 16), 64), least);
 }
 int64_t slope_groups(int64_t N, int F) { return (N + slope_rows(N, F) - 1) / slope_rows(N, F); }
+int64_t slope_blocks(int64_t N, int F) { return slope_groups(N, F) * ((F + 511) / 512); }
 
 // Workspaces, in order. Both operands' repacked rows have room whether or not they are needed: that depends on addresses.
 struct ForwardPlan { Cut cut; size_t x, w, part, bytes; };
@@ -673,7 +733,7 @@ int ddm_gated_linear_forward(const void *x, int64_t ldx, const void *weight, con
 
 namespace {
 
-struct BackPlan { Cut by_x, by_w; size_t x, w, dp, bias, part, bytes; };
+struct BackPlan { Cut by_x, by_w; size_t x, w, dp, bias, most, part, bytes; };
 BackPlan back_plan(int64_t N, int C, int F, int dtype) {
     BackPlan p{};
     p.by_x = cut_by_x(N, C, F, dtype);
@@ -681,7 +741,8 @@ BackPlan back_plan(int64_t N, int C, int F, int dtype) {
     p.w = repacked(N, C, dtype);
     p.dp = p.w + (C % (16 / esize(dtype)) ? repacked(2 * (int64_t)F, C, dtype) : 0);
     p.bias = p.dp + whole((size_t)N * 2 * padded(F, dtype) * esize(dtype));
-    p.part = p.bias + whole((size_t)slope_groups(N, F) * 2 * F * 4);
+    p.most = p.bias + whole((size_t)slope_groups(N, F) * 2 * F * 4);
+    p.part = p.most + (dtype == DDM_F16 ? whole((size_t)(slope_blocks(N, F) + 1) * 4) : 0);
     p.bytes = p.part + std::max(parts_bytes(p.by_x), parts_bytes(p.by_w));
     return p;
 }
@@ -717,11 +778,16 @@ int ddm_gated_linear_backward(const void *dh, const void *x, int64_t ldx, const 
         SlopeArgs sl{};
         sl.dh = dh; sl.kept = kept; sl.dp = ws + pl.dp; sl.part = dbias ? (float *)(ws + pl.bias) : nullptr;
         sl.N = N; sl.F = F; sl.pitch = padded(F, dtype); sl.act = activation; sl.rows = slope_rows(N, F);
-        hipLaunchKernelGGL((gated_slope_kernel<T>), dim3((unsigned)((sl.pitch + 511) / 512 * slope_groups(N, F))), dim3(256), 0, stream, sl);
+        const dim3 slope_grid((unsigned)slope_blocks(N, F));
+        if (std::is_same_v<T, _Float16> && (dx || dweight)) { sl.unit = (float *)(ws + pl.most); sl.most = sl.unit + 1; }
+        hipLaunchKernelGGL((gated_slope_kernel<T>), slope_grid, dim3(256), 0, stream, sl);
+        if constexpr (std::is_same_v<T, _Float16>)
+            if (sl.unit) hipLaunchKernelGGL((gated_slope_kernel<T, true>), slope_grid, dim3(256), 0, stream, sl);
         if (dbias)
             hipLaunchKernelGGL((gated_bias_kernel<T>), dim3((2 * F + 31) / 32), dim3(1024), 0, stream, sl.part, (int)slope_groups(N, F), 2 * F, (T *)dbias);
         GatedArgs a{};
         a.part = (f32x4 *)(ws + pl.part);
+        a.unit = sl.unit;
         a.ldo = C; a.np = C; a.ldq = 2 * (int64_t)sl.pitch; a.q = sl.dp; a.seg_q = sl.pitch;
         if (dx) {
             a.ldp = C;

@@ -561,7 +561,9 @@ def gated_linear_forward(x, weight, bias=None, *, activation: str = "silu", keep
 
 def gated_linear_backward(dh, x, weight, kept, *, activation: str = "silu", need_dx: bool = True, need_dweight: bool = True,
                           need_dbias: bool = True):
-    """Gradients (dx, dweight, dbias) of :func:`gated_linear_forward` by its h; None for those not wanted."""
+    """Gradients (dx, dweight, dbias) of :func:`gated_linear_forward` by its h; None for those not wanted. The projections (kept) and
+    their gradients are rounded to x's type between the products, the latter wherever they lie (in float16 in units that fit the largest).
+    A projection beyond 65504 is infinite in a float16 kept, and what the gradient has through it is infinite or NaN."""
     sizes = _gated_sizes(x, weight, activation)
     F = sizes[2]
     _tensor(dh, "dh", x.dtype, x.device, x.shape[:-1] + (F,))

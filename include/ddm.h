@@ -437,7 +437,11 @@ int ddm_residual_norm_backward(const void *dy, const void *ds, const void *x, in
  *   kept         [N][2F] in dtype: rows of g and u, what backward needs of forward; NULL when no gradient is wanted
  *   Each of dx, dweight, dbias may be NULL when it is not wanted.
  * Products take the inputs' type with fp32 accumulation; g, u (in kept) and dg, du are rounded to that type between the products
- * of a gradient. Rows that are not whole 16-byte pieces are repacked into the workspace first, which has room for x's always, and at
+ * of a gradient: dx and dweight are then 0.0030 of their norm off in bfloat16 and 0.00038 in float16, where rounding them alone makes
+ * 0.0017 and 0.0002. In DDM_F16, where the largest finite dg or du is not between 1 and 65504, they are held in units of a power of two
+ * in which it is; a projection beyond 65504 is kept as infinite, though, and the gradient that passes through it (its row of dx, its
+ * unit's rows of dweight and dbias) is infinite or NaN where h may be finite.
+ * Rows that are not whole 16-byte pieces are repacked into the workspace first, which has room for x's always, and at
  * most 128 MB for the sums of tiles that are cut along k; backward's has dg and du besides.
  * 1 <= C, F <= DDM_MAX_GATED with F C element size (C padded to 16 bytes) below 1 GB, 0 <= N <= DDM_MAX_GATED_ROWS (N = 0: the
  * gradients of weight and bias are zeros). */
