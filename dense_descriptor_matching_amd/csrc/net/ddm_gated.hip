@@ -610,10 +610,20 @@ Cut cut_forward(int64_t N, int C, int F, int dtype) { return cut_of(FORWARD, N, 
 Cut cut_by_x(int64_t N, int C, int F, int dtype) { return cut_of(BY_X, N, C, F, dtype); }
 Cut cut_by_w(int64_t N, int C, int F, int dtype) { return cut_of(BY_W, F, C, N, dtype); }
 
-// Up to so many rows gated_tokens_kernel is sooner done than the tiles' product, which in 32 bits keeps the matrix cores busy
-// with rows that are not there (33 to 64 rows of 4096 to 8192: bf16 37 us by tiles, 42 to 55 without; 1024 to 2736: fp32 28 by tiles, 16
-// without).
-int tokens_rows(int dtype) { return dtype == DDM_F32 ? 64 : 32; }
+// Whether gated_tokens_kernel is sooner done than the tiles' product, by models of both in microseconds that follow what was measured
+// over C of 64 to 16384, F of 64 to 16384 and 1 to 64 rows. A workgroup of it walks along k at a pace that its rows and, from 33 on, a
+// second operand set; workgroups beyond one to a CU (4096 of F) wait. Tiles cost a start, a join and the weight's bytes, in 32 bits
+// a matrix product of rows that are mostly not there. By tokens and by tiles, bf16: 48 x 1024 to 1024 9 and 22 us, 64 x 1024 to 2736
+// 9.8 and 14.5, 33 x 2048 to 5461 22.2 and 23.9, 64 rows of it 29.6 and 25.5, 32 x 16384 to 2048 66 and 54, 64 x 4096 to 8192 55 and 39; fp32:
+// 64 x 1024 to 2736 16.5 and 28, 8 x 8192 to 512 46 and 40, 32 x 8192 to 1024 65 and 52, 64 x 4096 to 8192 108 and 155. Among those sizes the
+// worse one is taken by 20% at most (64 x 4096 to 1024 bf16).
+bool by_tokens(int64_t N, int C, int F, int dtype) {
+    if (N == 0 || N > 64) return N == 0;
+    const double k = C / 1024., product = 1e-6 * F * C, second = N > 32;
+    if (dtype == DDM_F32) return 3 + k * (5.2 + 0.075 * N + 2 * second) * std::max(1., F / 4096.) < 18 + 4.2 * product;
+    const int rounds = (F + 4095) / 4096;
+    return 3.5 + k * (2.2 + 0.043 * N + 0.5 * second) * (rounds == 1 ? 1 : 1.2 * rounds) < 13.5 + 1.6 * k + 0.6 * product;
+}
 
 size_t repacked(int64_t rows, int C, int dtype) { return whole((size_t)rows * padded(C, dtype) * esize(dtype)); }
 size_t parts_bytes(const Cut &c) { return (size_t)c.s.tail * c.s.of * c.size * c.size * 4; }
@@ -628,13 +638,14 @@ int64_t slope_groups(int64_t N, int F) { return (N + slope_rows(N, F) - 1) / slo
 int64_t slope_blocks(int64_t N, int F) { return slope_groups(N, F) * ((F + 511) / 512); }
 
 // Workspaces, in order. Both operands' repacked rows have room whether or not they are needed: that depends on addresses.
-struct ForwardPlan { Cut cut; size_t x, w, part, bytes; };
+struct ForwardPlan { bool tokens; Cut cut; size_t x, w, part, bytes; };
 ForwardPlan forward_plan(int64_t N, int C, int F, int dtype) {
     ForwardPlan p{};
-    if (N > tokens_rows(dtype)) p.cut = cut_forward(N, C, F, dtype);
+    p.tokens = by_tokens(N, C, F, dtype);
+    if (!p.tokens) p.cut = cut_forward(N, C, F, dtype);
     p.w = repacked(N, C, dtype);
     p.part = p.w + (C % (16 / esize(dtype)) ? repacked(2 * (int64_t)F, C, dtype) : 0);
-    p.bytes = p.part + (N > tokens_rows(dtype) ? parts_bytes(p.cut) : 0);
+    p.bytes = p.part + (p.tokens ? 0 : parts_bytes(p.cut));
     return p;
 }
 
@@ -720,10 +731,9 @@ int ddm_gated_linear_forward(const void *x, int64_t ldx, const void *weight, con
         a.part = (f32x4 *)(ws + pl.part);
         // 24576 x 1024 to 2736 bf16 with kept: 336 us past the L2s, which then keep x and the weight, 373 through them
         a.past_l2 = (kept ? 3 : 1) * N * F * e > 32 << 20;
-        if (N <= 32) hipLaunchKernelGGL((gated_tokens_kernel<T, 1, 8>), dim3((F + 15) / 16), dim3(512), 0, stream, a);
-        else if (N <= tokens_rows(dtype)) {
-            if constexpr (sizeof(T) == 4) hipLaunchKernelGGL((gated_tokens_kernel<T, 2, 8>), dim3((F + 15) / 16), dim3(512), 0, stream, a);
-        }
+        const dim3 tokens((F + 15) / 16);
+        if (pl.tokens && N <= 32) hipLaunchKernelGGL((gated_tokens_kernel<T, 1, 8>), tokens, dim3(512), 0, stream, a);
+        else if (pl.tokens) hipLaunchKernelGGL((gated_tokens_kernel<T, 2, 8>), tokens, dim3(512), 0, stream, a);
         else launch_product<T, FORWARD>(a, pl.cut, stream);
     });
     return hipGetLastError() == hipSuccess ? DDM_OK : DDM_ERR_HIP;
