@@ -637,15 +637,15 @@ int slope_rows(int64_t N, int F) {
 int64_t slope_groups(int64_t N, int F) { return (N + slope_rows(N, F) - 1) / slope_rows(N, F); }
 int64_t slope_blocks(int64_t N, int F) { return slope_groups(N, F) * ((F + 511) / 512); }
 
-// Workspaces, in order. Both operands' repacked rows have room whether or not they are needed: that depends on addresses.
-struct ForwardPlan { bool tokens; Cut cut; size_t x, w, part, bytes; };
+// Workspaces, in order. x's repacked rows come last: whether they are needed depends on its address and stride.
+struct ForwardPlan { bool tokens; Cut cut; size_t w, part, x, bytes; };
 ForwardPlan forward_plan(int64_t N, int C, int F, int dtype) {
     ForwardPlan p{};
     p.tokens = by_tokens(N, C, F, dtype);
     if (!p.tokens) p.cut = cut_forward(N, C, F, dtype);
-    p.w = repacked(N, C, dtype);
     p.part = p.w + (C % (16 / esize(dtype)) ? repacked(2 * (int64_t)F, C, dtype) : 0);
-    p.bytes = p.part + (p.tokens ? 0 : parts_bytes(p.cut));
+    p.x = p.part + (p.tokens ? 0 : parts_bytes(p.cut));
+    p.bytes = p.x + repacked(N, C, dtype);
     return p;
 }
 
@@ -685,11 +685,15 @@ void launch_product(GatedArgs a, const Cut &c, hipStream_t s) {
 
 unsigned blocks(int64_t items, int64_t each) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>((items + each - 1) / each, 8192)); }
 
+// Whether rows are whole 16-byte pieces where they are.
+bool are_whole(const void *from, int64_t ld, int64_t rows, int C, int e) {
+    return (uintptr_t)from % 16 == 0 && C * (int64_t)e % 16 == 0 && (ld * e % 16 == 0 || rows == 1);
+}
 // x or the weight as rows of whole 16-byte pieces: themselves, or a copy in the workspace.
 template <class T>
 const T *whole_rows(const void *from, int64_t &ld, int64_t rows, int C, void *copy, hipStream_t s) {
     constexpr int PE = 16 / sizeof(T);
-    if ((uintptr_t)from % 16 == 0 && C % PE == 0 && (ld % PE == 0 || rows == 1)) return (const T *)from;
+    if (are_whole(from, ld, rows, C, sizeof(T))) return (const T *)from;
     const int pitch = (C + PE - 1) / PE * PE;
     hipLaunchKernelGGL((gated_repack_kernel<T>), dim3(blocks(rows * (pitch / PE), 256)), dim3(256), 0, s, (const T *)from, ld, rows, C, pitch, (T *)copy);
     ld = pitch;
@@ -699,12 +703,21 @@ const T *whole_rows(const void *from, int64_t &ld, int64_t rows, int C, void *co
 bool bad_act(int act) { return act != DDM_SILU && act != DDM_GELU && act != DDM_SIGMOID; }
 bool bad_stride(int64_t ld, int C, int e) { return ld < C || ld > (1 << 22) / e; }
 bool off(const void *p, int e) { return !p || (uintptr_t)p % e; }
+// What a plan's workspace comes to for this x.
+template <class Plan>
+size_t needed(const Plan &p, const void *x, int64_t ldx, int64_t N, int C, int e) {
+    return std::max<size_t>(are_whole(x, ldx, N, C, e) ? p.x : p.bytes, 16);
+}
 // The weight's rows are read in place, in pieces of 16 bytes, or repacked, where they are not made of whole ones.
 bool off_weight(const void *w, int C, int e) { return off(w, C * (int64_t)e % 16 ? e : 16); }
 
 }  // namespace
 
 extern "C" {
+
+size_t ddm_gated_linear_repack_bytes(int64_t N, int C, int dtype) {
+    return check(N, C, 1, dtype) != DDM_OK ? 0 : repacked(N, C, dtype);
+}
 
 size_t ddm_gated_linear_forward_workspace_bytes(int64_t N, int C, int F, int dtype) {
     if (check(N, C, F, dtype) != DDM_OK) return 0;
@@ -719,13 +732,13 @@ int ddm_gated_linear_forward(const void *x, int64_t ldx, const void *weight, con
     if (N == 0) return DDM_OK;
     if (off(x, e) || off_weight(weight, C, e) || off(h, e) || (uintptr_t)bias % e || (uintptr_t)kept % e) return DDM_ERR_INVALID;
     const ForwardPlan pl = forward_plan(N, C, F, dtype);
-    if (off(workspace, 16) || workspace_bytes < pl.bytes) return DDM_ERR_WORKSPACE;
+    if (off(workspace, 16) || workspace_bytes < needed(pl, x, ldx, N, C, e)) return DDM_ERR_WORKSPACE;
     char *ws = (char *)workspace;
     with_type(dtype, [&](auto t) {
         using T = decltype(t);
         GatedArgs a{};
         a.ldq = ldx; a.ldp = C; a.ldo = F;
-        a.q = whole_rows<T>(x, a.ldq, N, C, ws, stream);
+        a.q = whole_rows<T>(x, a.ldq, N, C, ws + pl.x, stream);
         a.p = whole_rows<T>(weight, a.ldp, 2 * (int64_t)F, C, ws + pl.w, stream);
         a.np = F; a.nq = (int)N; a.k = C; a.bias = bias; a.out = h; a.kept = kept; a.act = activation;
         a.part = (f32x4 *)(ws + pl.part);
@@ -743,17 +756,17 @@ int ddm_gated_linear_forward(const void *x, int64_t ldx, const void *weight, con
 
 namespace {
 
-struct BackPlan { Cut by_x, by_w; size_t x, w, dp, bias, most, part, bytes; };
+struct BackPlan { Cut by_x, by_w; size_t w, dp, bias, most, part, x, bytes; };
 BackPlan back_plan(int64_t N, int C, int F, int dtype) {
     BackPlan p{};
     p.by_x = cut_by_x(N, C, F, dtype);
     p.by_w = cut_by_w(N, C, F, dtype);
-    p.w = repacked(N, C, dtype);
     p.dp = p.w + (C % (16 / esize(dtype)) ? repacked(2 * (int64_t)F, C, dtype) : 0);
     p.bias = p.dp + whole((size_t)N * 2 * padded(F, dtype) * esize(dtype));
     p.most = p.bias + whole((size_t)slope_groups(N, F) * 2 * F * 4);
     p.part = p.most + (dtype == DDM_F16 ? whole((size_t)(slope_blocks(N, F) + 1) * 4) : 0);
-    p.bytes = p.part + std::max(parts_bytes(p.by_x), parts_bytes(p.by_w));
+    p.x = p.part + std::max(parts_bytes(p.by_x), parts_bytes(p.by_w));
+    p.bytes = p.x + repacked(N, C, dtype);
     return p;
 }
 
@@ -775,7 +788,7 @@ int ddm_gated_linear_backward(const void *dh, const void *x, int64_t ldx, const 
     if (N && (off(dh, e) || off(kept, e) || (dweight && off(x, e)) || (dx && off_weight(weight, C, e)))) return DDM_ERR_INVALID;
     if ((uintptr_t)dx % e || (uintptr_t)dweight % e || (uintptr_t)dbias % e) return DDM_ERR_INVALID;
     const BackPlan pl = back_plan(N, C, F, dtype);
-    if (off(workspace, 16) || workspace_bytes < pl.bytes) return DDM_ERR_WORKSPACE;
+    if (off(workspace, 16) || workspace_bytes < needed(pl, x, ldx, N, C, e)) return DDM_ERR_WORKSPACE;
     if (!dx && !dweight && !dbias) return DDM_OK;
     char *ws = (char *)workspace;
     with_type(dtype, [&](auto t) {
@@ -807,7 +820,7 @@ int ddm_gated_linear_backward(const void *dh, const void *x, int64_t ldx, const 
         }
         if (dweight) {
             a.ldp = ldx;
-            a.p = whole_rows<T>(x, a.ldp, N, C, ws, stream);
+            a.p = whole_rows<T>(x, a.ldp, N, C, ws + pl.x, stream);
             a.nq = F; a.k = (int)N; a.out = dweight;
             launch_product<T, BY_W>(a, pl.by_w, stream);
         }

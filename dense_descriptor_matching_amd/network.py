@@ -50,7 +50,8 @@ def declare(lib):
     lib.ddm_gated_linear_backward.argtypes = [P] + rows + [P, P, I64, I, I, I, I, P, P, P, P, SZ, P]
     for f in (lib.ddm_gated_linear_forward_workspace_bytes, lib.ddm_gated_linear_backward_workspace_bytes):
         f.argtypes = [I64, I, I, I]
-    for f in (lib.ddm_residual_norm_backward_workspace_bytes, lib.ddm_gated_linear_forward_workspace_bytes,
+    lib.ddm_gated_linear_repack_bytes.argtypes = [I64, I, I]
+    for f in (lib.ddm_residual_norm_backward_workspace_bytes, lib.ddm_gated_linear_repack_bytes, lib.ddm_gated_linear_forward_workspace_bytes,
               lib.ddm_gated_linear_backward_workspace_bytes):
         f.restype = SZ
     for f in (lib.ddm_attention_forward, lib.ddm_attention_backward, lib.ddm_layer_norm_forward,
@@ -540,6 +541,15 @@ def _gated_weight(weight):
     return weight.data_ptr()
 
 
+def _gated_workspace(direction, x, ldx, sizes):
+    """(tensor, bytes): without room for a copy of x where its rows are whole 16-byte pieces."""
+    nbytes, (N, C, _, dtype) = _workspace_bytes(f"ddm_gated_linear_{direction}_workspace_bytes", *sizes), sizes
+    e = x.element_size()
+    if N and x.data_ptr() % 16 == 0 and C * e % 16 == 0 and (ldx * e % 16 == 0 or N == 1):
+        nbytes = max(nbytes - _workspace_bytes("ddm_gated_linear_repack_bytes", N, C, dtype), 16)
+    return x.new_empty(nbytes, dtype=torch.uint8), nbytes
+
+
 def gated_linear_forward(x, weight, bias=None, *, activation: str = "silu", keep: bool = False):
     """Gated linear layer h = act(x Wg^T + bg) * (x Wu^T + bu) of x [..., C]: weight [2F, C] holds the F rows of Wg and then those of Wu,
     bias [2F] likewise. Returns (h [..., F], kept): kept [..., 2F] is what :func:`gated_linear_backward` needs with ``keep``, else
@@ -550,10 +560,9 @@ def gated_linear_forward(x, weight, bias=None, *, activation: str = "silu", keep
     if bias is not None:
         _tensor(bias, "bias", x.dtype, x.device, (2 * F,))
     view = _rows(x, "x")
-    nbytes = _workspace_bytes("ddm_gated_linear_forward_workspace_bytes", *sizes)
     h = x.new_empty(x.shape[:-1] + (F,))
     kept = x.new_empty(x.shape[:-1] + (2 * F,)) if keep else None
-    ws = x.new_empty(nbytes, dtype=torch.uint8)
+    ws, nbytes = _gated_workspace("forward", x, view[1], sizes)
     _call(x.device, "ddm_gated_linear_forward", *view, _gated_weight(weight), _at(bias), *sizes, ACTIVATIONS[activation], h.data_ptr(),
           _at(kept), ws.data_ptr(), nbytes)
     return h, kept
@@ -569,11 +578,10 @@ def gated_linear_backward(dh, x, weight, kept, *, activation: str = "silu", need
     _tensor(dh, "dh", x.dtype, x.device, x.shape[:-1] + (F,))
     _tensor(kept, "kept", x.dtype, x.device, x.shape[:-1] + (2 * F,))
     view = _rows(x, "x")
-    nbytes = _workspace_bytes("ddm_gated_linear_backward_workspace_bytes", *sizes)
     dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
     dw = torch.empty_like(weight) if need_dweight else None
     db = x.new_empty(2 * F) if need_dbias else None
-    ws = x.new_empty(nbytes, dtype=torch.uint8)
+    ws, nbytes = _gated_workspace("backward", x, view[1], sizes)
     _call(x.device, "ddm_gated_linear_backward", dh.data_ptr(), *view, _gated_weight(weight) if need_dx else weight.data_ptr(), kept.data_ptr(), *sizes,
           ACTIVATIONS[activation], _at(dx), _at(dw), _at(db), ws.data_ptr(), nbytes)
     return dx, dw, db

@@ -441,13 +441,15 @@ int ddm_residual_norm_backward(const void *dy, const void *ds, const void *x, in
  * 0.0017 and 0.0002. In DDM_F16, where the largest finite dg or du is not between 1 and 65504, they are held in units of a power of two
  * in which it is; a projection beyond 65504 is kept as infinite, though, and the gradient that passes through it (its row of dx, its
  * unit's rows of dweight and dbias) is infinite or NaN where h may be finite.
- * Rows that are not whole 16-byte pieces are repacked into the workspace first, which has room for x's always, and at
- * most 128 MB for the sums of tiles that are cut along k; backward's has dg and du besides.
+ * Rows that are not whole 16-byte pieces are repacked into the workspace first, which has at most 128 MB for the sums of tiles that are
+ * cut along k; backward's has dg and du besides. Its bytes allow for a copy of x; where x lies on whole pieces (address, C and, with
+ * more rows than one, ldx), ddm_gated_linear_repack_bytes less are enough, and 16 always needed.
  * 1 <= C, F <= DDM_MAX_GATED with F C element size (C padded to 16 bytes) below 1 GB, 0 <= N <= DDM_MAX_GATED_ROWS (N = 0: the
  * gradients of weight and bias are zeros). */
 enum { DDM_SILU = 0, DDM_GELU = 1, DDM_SIGMOID = 2 };
 #define DDM_MAX_GATED 262144
 #define DDM_MAX_GATED_ROWS 16777216
+size_t ddm_gated_linear_repack_bytes(int64_t N, int C, int dtype);
 size_t ddm_gated_linear_forward_workspace_bytes(int64_t N, int C, int F, int dtype);
 int ddm_gated_linear_forward(const void *x, int64_t ldx, const void *weight, const void *bias, int64_t N, int C, int F, int dtype,
                              int activation, void *h, void *kept, void *workspace, size_t workspace_bytes, hipStream_t stream);
