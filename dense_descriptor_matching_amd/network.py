@@ -535,19 +535,26 @@ def _gated_sizes(x, weight, activation):
     return x.numel() // x.shape[-1], x.shape[-1], weight.shape[0] // 2, _DT[x.dtype]
 
 
-def _gated_weight(weight):
-    if weight.data_ptr() % 16 and weight.shape[1] * weight.element_size() % 16 == 0:
-        raise _api.DDMError(-1, "weight off a 16-byte boundary, with rows of whole 16-byte pieces: clone it")
-    return weight.data_ptr()
+def _gated_call(x, weight, what, *args):
+    try:
+        _call(x.device, what, *args)
+    except _api.DDMError as e:
+        if e.status == -1 and weight.data_ptr() % 16 and weight.shape[1] * weight.itemsize % 16 == 0:
+            raise _api.DDMError(-1, f"{what}: a weight off a 16-byte boundary, with rows of whole 16-byte pieces (clone it)") from None
+        raise
 
 
-def _gated_workspace(direction, x, ldx, sizes):
-    """(tensor, bytes): without room for a copy of x where its rows are whole 16-byte pieces."""
-    nbytes, (N, C, _, dtype) = _workspace_bytes(f"ddm_gated_linear_{direction}_workspace_bytes", *sizes), sizes
-    e = x.element_size()
-    if N and x.data_ptr() % 16 == 0 and C * e % 16 == 0 and (ldx * e % 16 == 0 or N == 1):
-        nbytes = max(nbytes - _workspace_bytes("ddm_gated_linear_repack_bytes", N, C, dtype), 16)
-    return x.new_empty(nbytes, dtype=torch.uint8), nbytes
+@functools.lru_cache(maxsize=1024)
+def _gated_bytes(what, copy, N, C, F, dtype):
+    """The workspace's bytes, with room for a copy of x or without."""
+    nbytes = _workspace_bytes(what, N, C, F, dtype)
+    return nbytes if copy or N == 0 else max(nbytes - _workspace_bytes("ddm_gated_linear_repack_bytes", N, C, dtype), 16)
+
+
+def _copied(view, x):
+    """Whether x's rows are copied first: they are not whole 16-byte pieces."""
+    e = x.itemsize
+    return (view[0] | view[1] * e | x.shape[-1] * e) % 16 != 0
 
 
 def gated_linear_forward(x, weight, bias=None, *, activation: str = "silu", keep: bool = False):
@@ -560,11 +567,12 @@ def gated_linear_forward(x, weight, bias=None, *, activation: str = "silu", keep
     if bias is not None:
         _tensor(bias, "bias", x.dtype, x.device, (2 * F,))
     view = _rows(x, "x")
+    nbytes = _gated_bytes("ddm_gated_linear_forward_workspace_bytes", _copied(view, x), *sizes)
     h = x.new_empty(x.shape[:-1] + (F,))
     kept = x.new_empty(x.shape[:-1] + (2 * F,)) if keep else None
-    ws, nbytes = _gated_workspace("forward", x, view[1], sizes)
-    _call(x.device, "ddm_gated_linear_forward", *view, _gated_weight(weight), _at(bias), *sizes, ACTIVATIONS[activation], h.data_ptr(),
-          _at(kept), ws.data_ptr(), nbytes)
+    ws = x.new_empty(nbytes, dtype=torch.uint8)
+    _gated_call(x, weight, "ddm_gated_linear_forward", *view, weight.data_ptr(), _at(bias), *sizes, ACTIVATIONS[activation],
+                h.data_ptr(), _at(kept), ws.data_ptr(), nbytes)
     return h, kept
 
 
@@ -578,12 +586,13 @@ def gated_linear_backward(dh, x, weight, kept, *, activation: str = "silu", need
     _tensor(dh, "dh", x.dtype, x.device, x.shape[:-1] + (F,))
     _tensor(kept, "kept", x.dtype, x.device, x.shape[:-1] + (2 * F,))
     view = _rows(x, "x")
+    nbytes = _gated_bytes("ddm_gated_linear_backward_workspace_bytes", _copied(view, x), *sizes)
     dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
     dw = torch.empty_like(weight) if need_dweight else None
     db = x.new_empty(2 * F) if need_dbias else None
-    ws, nbytes = _gated_workspace("backward", x, view[1], sizes)
-    _call(x.device, "ddm_gated_linear_backward", dh.data_ptr(), *view, _gated_weight(weight) if need_dx else weight.data_ptr(), kept.data_ptr(), *sizes,
-          ACTIVATIONS[activation], _at(dx), _at(dw), _at(db), ws.data_ptr(), nbytes)
+    ws = x.new_empty(nbytes, dtype=torch.uint8)
+    _gated_call(x, weight, "ddm_gated_linear_backward", dh.data_ptr(), *view, weight.data_ptr(), kept.data_ptr(), *sizes,
+                ACTIVATIONS[activation], _at(dx), _at(dw), _at(db), ws.data_ptr(), nbytes)
     return dx, dw, db
 
 
