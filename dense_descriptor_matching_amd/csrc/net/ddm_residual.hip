@@ -11,8 +11,9 @@
 // Bound by memory: each input is read once, each output written once. A row lies in the registers of a team of threads
 // (a wave, or four or eight for wide rows), 16 columns a thread at most, so that backward keeps its share of up to five
 // sums over rows beside a row of five inputs. Measured, 24576 x 1024 bf16 with gate, scale and both norms: forward 47 us
-// (252 MB, 5.3 TB/s; a copy of 2 x 200 MB reaches 5.4 here), backward 92 us (403 MB, 4.4 TB/s, one wave to a SIMD: 302
-// registers) and 4 us for the last sums; 10007 x 1285 fp32, rms: 46 and 86 us (206 and 360 MB). Backward takes s again from x and the branch
+// (252 MB, 5.3 TB/s; a copy of 2 x 200 MB reaches 5.4 here), backward 96 us (403 MB, 4.2 TB/s, one wave to a SIMD: 328
+// registers) and 4 us for the last sums; 10007 x 1285 fp32, rms: 44 and 84 us (206 and 309 MB). From 4097 columns on, teams of eight
+// waves spill backward's registers (4096 x 8192 bf16, everything: 110 and 671 us). Backward takes s again from x and the branch
 // in 32 bits: the s that forward gives back is rounded, and what that costs dw would not average out.
 #include "../../../include/ddm.h"
 #include "ddm_row.hpp"
@@ -122,7 +123,7 @@ struct Chunk {
 
 // Parameters' columns, in LDS for the workgroup: registers are for sums and rows. Zeros behind the last: what rows have
 // there counts for nothing. So for a wave a row, and the next row is fetched ahead (24576 x 1024 bf16 forward 63 -> 47 us,
-// backward 189 -> 92). Four and eight waves' rows have 8 to 16 columns a thread and more parameters than LDS has room for in
+// backward 189 -> 96). Four and eight waves' rows have 8 to 16 columns a thread and more parameters than LDS has room for in
 // as many workgroups: in registers, without fetching ahead (10007 x 1285 fp32 forward 44 us, with LDS 60 to 66).
 template <class T, class W, int TEAM, int V>
 struct Params {

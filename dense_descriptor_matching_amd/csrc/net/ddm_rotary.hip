@@ -6,7 +6,7 @@
 // Bound by memory: every element of q and k is read once and written once. A workgroup takes a few tokens, puts the
 // sines and cosines of their pairs into LDS and then walks over the tokens' heads, q's and k's, in the order of their
 // addresses: one angle serves all heads. 24576 tokens x 32 heads of 64 bf16, two axes: 41 us (201 MB, 4.9 TB/s; a copy
-// of 2 x 200 MB reaches 5.4 here); 40001 x 40 heads of 128 fp16, a quarter of each turned: 158 us (819 MB, 5.2 TB/s). Six
+// of 2 x 200 MB reaches 5.4 here); 40001 x 40 heads of 128 fp16, half of each turned: 158 us (819 MB, 5.2 TB/s). Six
 // tokens x 40 heads take 3 us, beside some 10 of the host's call.
 #include "../../../include/ddm.h"
 #include "ddm_tile.hpp"
