@@ -8,10 +8,11 @@
 // rows of Wu into one tile, so that a lane has g and u of an element and finishes it in registers. The gradient makes dg and du in a
 // pass over memory (each is an operand of two products, and rounding them to the inputs' type is what the matrix cores take) and then
 // runs two more products from the same loop. Measured, 24576 x 1024 to 2736 bf16 (275 GFLOP a product; a product of 8192^3 reaches
-// 1454 TFLOP/s here, the library takes 329, 229 and 389 us for the three): forward with g and u kept 350 us (a tile's three
-// outputs are written while no matrix core works: 250 without them), dg and du 158 us behind it (672 MB, 4.3 TB/s; 144 where g and u
-// are in the caches, which that forward's outputs pass by), by x 270 + 14 us to join tiles cut along k, by W 265 + 24. 256 tiles in step take 1.45 to 1.6 us for 64 of k, 32 tiles 1.1: where all CUs work, memory
-// and power count. Tiles of 128 everywhere: 435, 354 and 320 us; 64 of k a step with two steps ahead: 385, 332, 313.
+// 1454 TFLOP/s here, the library takes 329, 229 and 389 us for the three): forward with g and u kept 350 us (a tile's three outputs
+// are written while no matrix core works: 250 without them), dg and du 158 us behind it (672 MB, 4.3 TB/s; 144 where g and u are in
+// the caches, which that forward's outputs pass by), by x 270 + 14 us to join tiles cut along k, by W 265 + 24. 256 tiles in step take
+// 1.45 to 1.6 us for 64 of k, 32 tiles 1.1: where all CUs work, memory and power count. Tiles of 128 everywhere: 435, 354 and 320 us;
+// 64 of k a step with two steps ahead: 385, 332, 313.
 #include "../../../include/ddm.h"
 #include "ddm_gemm.hpp"
 #include "ddm_row.hpp"

@@ -347,7 +347,7 @@ def _rotary(q, k, positions, frequencies, interleaved, magnitude, inverse, out, 
     _call(dev, "ddm_rotary", *qv, *kv, positions.data_ptr(), frequencies.data_ptr(), T, D, axes, pairs, _DT[q.dtype],
           int(interleaved), int(inverse), float(magnitude), *qw[:3], *kw[:3])
     if out is not None:                     # a backward pass that was to read what stood there raises
-        torch.autograd.graph.increment_version([t for t in out if t is not None])
+        torch.autograd.graph.increment_version([t for t in (qo, ko) if t is not None])
     return qo, ko
 
 

@@ -48,7 +48,7 @@ def test_what_was_saved_for_a_gradient_is_guarded(ddm, places):
         a, v = heads(requires_grad=True), heads()
         y = (a * v).sum()                   # keeps v
         q, k = (v, heads(1)) if which == 0 else (heads(1), v)
-        ddm.rotary_forward(q, k, *places, out=(q, k))
+        ddm.rotary_forward(q, k, *places, out=iter((q, k)))
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             y.backward()
     a, v = heads(requires_grad=True), heads()
